@@ -28,9 +28,15 @@ CONV_WIDTH = 4
 EXPORTS = ("gdn_last_error", "gdn_build_conv_chunks", "gdn_causal_conv1d_varlen", "gdn_causal_conv1d_varlen_tiles",
            "gdn_causal_conv1d_update", "gdn_fused_recurrent_decode", "gdn_chunk_gated_delta_rule",
            "gdn_fused_conv_decode", "gdn_chunk_workspace_size", "gdn_chunk_rule_and_fused_decode",
-           "gdn_chunk_rule_and_fused_decode_noalloc")
+           "gdn_chunk_rule_and_fused_decode_noalloc",
+           "gdn_build_step_tables", "gdn_rope_frequencies", "gdn_rope_append_kv8",
+           "gdn_paged_attention_kv8_workspace_size", "gdn_paged_attention_kv8",
+           "gdn_gated_rms_norm", "gdn_residual_rms_norm")
 # bytes of the static device scratch gdn_chunk_rule_and_fused_decode_noalloc uses (gdn.h)
 NOALLOC_SCRATCH_BYTES = 64 << 20
+# requests one gdn_build_step_tables call takes at most (gdn.h)
+STEP_MAX_SEQS = 4096
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class GDNError(RuntimeError):
@@ -55,7 +61,7 @@ def _bind(path):
     lib.gdn_chunk_gated_delta_rule.argtypes = [P, i64, P, i64, P, i64, P, P, P, i32, P, P, P, P, i64,
                                                i32, i32, i32, i32, i32, i32, P, ctypes.c_size_t, f32, i32, P]
     for name in EXPORTS[1:]:
-        if name != "gdn_chunk_workspace_size":
+        if not name.endswith("_workspace_size"):
             getattr(lib, name).restype = ctypes.c_int
     lib.gdn_fused_conv_decode.argtypes = [P, i64, P, P, P, i32, P, P, P, i32, P, P, i64, P, i64,
                                           i32, i32, i32, i32, i32, i32, f32, i32, P]
@@ -69,6 +75,17 @@ def _bind(path):
         P, i32, i32, i32, i32, i32, f32, i32, P]                                       # shared
     lib.gdn_chunk_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.gdn_chunk_workspace_size.restype = ctypes.c_size_t
+    f64, size = ctypes.c_double, ctypes.c_size_t
+    lib.gdn_build_step_tables.argtypes = [P, P, i32, P, P, i32, P, i64, i32, i32, P, P, P, P, i32, P, i32, P, P]
+    lib.gdn_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, P]
+    lib.gdn_rope_append_kv8.argtypes = [P, i64, P, i64, P, i64, P, P, P, i32, i32, f64, P, i64,
+                                        P, P, P, P, i32, i32, i32, i32, i32, i32, P]
+    lib.gdn_paged_attention_kv8_workspace_size.argtypes = [i32] * 6
+    lib.gdn_paged_attention_kv8_workspace_size.restype = size
+    lib.gdn_paged_attention_kv8.argtypes = [P, i64, P, P, P, P, i32, i32, P, i64, i32, P, P, i32, P, i64,
+                                            i32, i32, i32, i32, i32, f32, i32, i32, P, size, P]
+    lib.gdn_gated_rms_norm.argtypes = [P, i64, P, i64, P, P, i64, i32, i32, i32, f32, f32, P]
+    lib.gdn_residual_rms_norm.argtypes = [P, i64, P, i64, P, P, i64, P, P, i64, P, i64, i32, i32, f32, f32, f32, P]
     return lib
 
 
@@ -502,3 +519,233 @@ def gdn_chunk_rule_and_fused_decode_noalloc(q, k, v, g, beta, state_indices, o, 
     rc = lib.gdn_chunk_rule_and_fused_decode_noalloc(*pre, *post, float(scale), int(bool(qk_l2norm)),
                                                      _stream(stream))
     _check(rc, "gdn_chunk_rule_and_fused_decode_noalloc")
+
+
+# ---------------------------------------------------------------------------
+# the attention layers' operators and the block norms
+# ---------------------------------------------------------------------------
+
+def _vector(t, dt, n, name):
+    """A packed 1-D operand of n entries."""
+    if t.dtype != dt:
+        raise TypeError("%s must be %s, got %s" % (name, dt, t.dtype))
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be packed with %d entries, got shape %s" % (name, n, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _current(*named):
+    """Every (name, tensor or None) on the current GPU."""
+    cur = None
+    for name, t in named:
+        if t is None:
+            continue
+        at = t.get_device()
+        if at < 0:
+            raise ValueError("%s must be a GPU tensor, got one on %s" % (name, t.device))
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if at != cur:
+            raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, at, cur))
+
+
+def gdn_build_step_tables(context_lens, query_lens, free_pages, num_free, block_table, page_size, query_start_loc,
+                          seq_lens, positions, slot_mapping, counts, chunks=None, stream=None):
+    """A step's tables from its requests' lengths; see gdn.h.
+
+    context_lens, query_lens: int32 [S]; free_pages int32 [F], num_free int32
+    [1]; block_table int32 [S][max_pages] (in place, rows may be strided);
+    query_start_loc int32 [S+1]; seq_lens int32 [S]; positions int32 [T] and
+    slot_mapping int64 [T]; counts int32 [4]: tokens, descriptors, pages
+    taken, pages missing; chunks int32 [n][2] or None.  Lengths and counts
+    stay on the GPU.
+    """
+    i32 = torch.int32
+    if context_lens.dim() != 1 or free_pages.dim() != 1 or positions.dim() != 1:
+        raise ValueError("context_lens, free_pages and positions must be 1-D")
+    S, F, T = context_lens.shape[0], free_pages.shape[0], positions.shape[0]
+    if block_table.dtype != i32:
+        raise TypeError("block_table must be %s, got %s" % (i32, block_table.dtype))
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must have %d rows, got shape %s" % (S, tuple(block_table.shape)))
+    n = 0
+    if chunks is not None:
+        if chunks.dtype != i32 or chunks.dim() != 2 or chunks.shape[1] != 2 or not chunks.is_contiguous():
+            raise ValueError("chunks must be a contiguous int32 [n][2] tensor, got shape %s" % (tuple(chunks.shape),))
+        n = chunks.shape[0]
+    args = (_vector(context_lens, i32, S, "context_lens"), _vector(query_lens, i32, S, "query_lens"), S,
+            _vector(free_pages, i32, F, "free_pages"), _vector(num_free, i32, 1, "num_free"), F,
+            block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1], page_size,
+            _vector(query_start_loc, i32, S + 1, "query_start_loc"), _vector(seq_lens, i32, S, "seq_lens"),
+            _vector(positions, i32, T, "positions"), _vector(slot_mapping, torch.int64, T, "slot_mapping"), T,
+            chunks.data_ptr() if n else None, n, _vector(counts, i32, 4, "counts"))
+    _current(("context_lens", context_lens), ("query_lens", query_lens), ("free_pages", free_pages),
+             ("num_free", num_free), ("block_table", block_table), ("query_start_loc", query_start_loc),
+             ("seq_lens", seq_lens), ("positions", positions), ("slot_mapping", slot_mapping), ("counts", counts),
+             ("chunks", chunks))
+    _check(lib.gdn_build_step_tables(*args, _stream(stream)), "gdn_build_step_tables")
+
+
+def gdn_rope_frequencies(rotary_dim, base, scaling="plain", factor=1.0, original_context=0.0, beta_fast=32.0,
+                         beta_slow=1.0):
+    """Rotary frequencies (float64 array of rotary_dim / 2) and the factor of
+    the rotated elements, on the host; scaling: "plain", "linear", "ntk" or
+    "yarn"; see gdn.h."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("scaling must be one of %s, got %r" % (", ".join(ROPE_SCALINGS), scaling))
+    out, rope_scale = np.empty(max(int(rotary_dim) // 2, 1), np.float64), ctypes.c_double(0.0)
+    _check(lib.gdn_rope_frequencies(rotary_dim, base, ROPE_SCALINGS[scaling], factor, original_context, beta_fast,
+                                    beta_slow, out.ctypes.data, ctypes.byref(rope_scale)), "gdn_rope_frequencies")
+    return out, rope_scale.value
+
+
+def _kv8(k_cache, v_cache, k_scale, v_scale):
+    """dtypes and shapes of the 8-bit paged cache; returns (pages, HK, page, D)."""
+    f8 = torch.float8_e4m3fn
+    if k_cache.dtype != f8 or v_cache.dtype != f8:
+        raise TypeError("k_cache and v_cache must be %s, got %s and %s" % (f8, k_cache.dtype, v_cache.dtype))
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("k_scale and v_scale must be torch.float32, got %s and %s" % (k_scale.dtype, v_scale.dtype))
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages][HK][page][D], got shape %s" % (tuple(k_cache.shape),))
+    n, hk, page, d = k_cache.shape
+    if v_cache.shape != (n, hk, d, page):
+        raise ValueError("v_cache must have shape %s, got %s" % ((n, hk, d, page), tuple(v_cache.shape)))
+    if k_scale.shape != (n, hk) or v_scale.shape != (n, hk):
+        raise ValueError("k_scale and v_scale must have shape %s, got %s and %s"
+                         % ((n, hk), tuple(k_scale.shape), tuple(v_scale.shape)))
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_cache, v_cache, k_scale and v_scale must be contiguous")
+    return n, hk, page, d
+
+
+def _bf16_heads(t, T, H, d, name):
+    """Token stride of a bf16 [T][H][d] operand with packed heads."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.shape != (T, H, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (T, H, d), tuple(t.shape)))
+    return _heads(t, name)
+
+
+def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale,
+                        interleaved=False, rope_scale=1.0, stream=None):
+    """Rotary positions on q and k, and k and v written into the 8-bit paged
+    cache; see gdn.h.
+
+    q, q_out: bf16 [T][HQ][D], or both None; q_out may be q; k, v: bf16
+    [T][HK][D] (token rows may be strided views of one projection's output);
+    positions int32 [T]; slot_mapping int64 [T]; frequencies float64
+    [rotary_dim / 2] on the GPU, or None for no rotation; k_cache
+    float8_e4m3fn [pages][HK][page][D]; v_cache [pages][HK][D][page]; k_scale,
+    v_scale fp32 [pages][HK] (all four in place).
+    """
+    n, hk, page, d = _kv8(k_cache, v_cache, k_scale, v_scale)
+    T = k.shape[0]
+    ks, vs = _bf16_heads(k, T, hk, d, "k"), _bf16_heads(v, T, hk, d, "v")
+    hq = qs = os_ = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out must be given together")
+    if q is not None:
+        _dims(q, 3, "q")
+        hq = q.shape[1]
+        qs, os_ = _bf16_heads(q, T, hq, d, "q"), _bf16_heads(q_out, T, hq, d, "q_out")
+    rot = 0
+    if frequencies is not None:
+        _dims(frequencies, 1, "frequencies")
+        rot = 2 * frequencies.shape[0]
+    args = (_ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _vector(positions, torch.int32, T, "positions"),
+            _vector(slot_mapping, torch.int64, T, "slot_mapping"),
+            _vector(frequencies, torch.float64, rot // 2, "frequencies") if rot else None, rot, 1 if interleaved else 0,
+            rope_scale, _ptr(q_out), os_, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            n, page, T, hq, hk, d)
+    _current(("k", k), ("v", v), ("positions", positions), ("slot_mapping", slot_mapping), ("frequencies", frequencies),
+             ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("q", q),
+             ("q_out", q_out))
+    _check(lib.gdn_rope_append_kv8(*args, _stream(stream)), "gdn_rope_append_kv8")
+
+
+def gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                           max_seq_len) -> int:
+    """Bytes of device scratch gdn_paged_attention_kv8 needs."""
+    return int(lib.gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                          max_seq_len))
+
+
+def gdn_paged_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o,
+                            max_seq_len, scale, causal=True, window=0, workspace=None, stream=None):
+    """Attention of a step's tokens over the 8-bit paged cache; see gdn.h.
+
+    q, o: bf16 [T][HQ][D]; the cache as gdn_rope_append_kv8 leaves it;
+    block_table int32 [S][max_pages]; seq_lens int32 [S]; query_start_loc int32
+    [S+1]; max_seq_len: the largest of seq_lens as the caller knows it.
+    ``workspace`` is a contiguous uint8 device tensor of at least
+    gdn_paged_attention_kv8_workspace_size(...) bytes; when omitted, torch
+    allocates one for the call where it is needed.
+    """
+    n, hk, page, d = _kv8(k_cache, v_cache, k_scale, v_scale)
+    _dims(q, 3, "q")
+    T, hq = q.shape[0], q.shape[1]
+    qs, os_ = _bf16_heads(q, T, hq, d, "q"), _bf16_heads(o, T, hq, d, "o")
+    _dims(seq_lens, 1, "seq_lens")
+    S = seq_lens.shape[0]
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must have %d rows, got shape %s" % (S, tuple(block_table.shape)))
+    args = (q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
+            block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
+            _vector(seq_lens, torch.int32, S, "seq_lens"),
+            _vector(query_start_loc, torch.int32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
+            d, scale, 1 if causal else 0, window)
+    _current(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+             ("block_table", block_table), ("seq_lens", seq_lens), ("query_start_loc", query_start_loc), ("o", o),
+             ("workspace", workspace))
+    need = lib.gdn_paged_attention_kv8_workspace_size(T, S, hq, hk, d, max_seq_len)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, q.device, stream)
+    _check(lib.gdn_paged_attention_kv8(*args, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                       _stream(stream)), "gdn_paged_attention_kv8")
+
+
+def gdn_gated_rms_norm(x, weight, y, gate=None, eps=1e-6, weight_offset=0.0, stream=None):
+    """Root-mean-square norm of each head, times silu(gate) where one is
+    given; see gdn.h.  x, gate, y: bf16 [T][H][D] (token rows may be strided
+    views; y may be x); weight: bf16 [D]."""
+    _dims(x, 3, "x")
+    T, H, d = x.shape
+    xs, ys = _bf16_heads(x, T, H, d, "x"), _bf16_heads(y, T, H, d, "y")
+    gs = 0 if gate is None else _bf16_heads(gate, T, H, d, "gate")
+    w = _vector(weight, torch.bfloat16, d, "weight")
+    _current(("x", x), ("weight", weight), ("y", y), ("gate", gate))
+    _check(lib.gdn_gated_rms_norm(x.data_ptr(), xs, _ptr(gate), gs, w, y.data_ptr(), ys, T, H, d, eps, weight_offset,
+                                  _stream(stream)), "gdn_gated_rms_norm")
+
+
+def gdn_residual_rms_norm(x, residual, weight, new_residual, y, post_weight=None, gate=None, residual_scale=1.0,
+                          eps=1e-6, weight_offset=0.0, stream=None):
+    """new_residual = residual + residual_scale * (norm after the block of x,
+    where post_weight is given) * sigmoid(gate), y = its norm before the next
+    block; see gdn.h.  x, residual, gate, new_residual, y: bf16 [rows][hidden]
+    (strided rows allowed; new_residual may be residual or x, y may be x);
+    weight, post_weight: bf16 [hidden]."""
+    _dims(x, 2, "x")
+    shape, bf16 = x.shape, torch.bfloat16
+    R, D = shape
+    strides = []
+    for name, t in (("x", x), ("residual", residual), ("gate", gate), ("new_residual", new_residual), ("y", y)):
+        if t is None:
+            strides.append(0)
+            continue
+        if t.dtype != bf16:
+            raise TypeError("%s must be %s, got %s" % (name, bf16, t.dtype))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        strides.append(_rows(t, name))
+    w = _vector(weight, bf16, D, "weight")
+    pw = None if post_weight is None else _vector(post_weight, bf16, D, "post_weight")
+    _current(("x", x), ("residual", residual), ("weight", weight), ("new_residual", new_residual), ("y", y),
+             ("post_weight", post_weight), ("gate", gate))
+    _check(lib.gdn_residual_rms_norm(x.data_ptr(), strides[0], residual.data_ptr(), strides[1], pw, _ptr(gate),
+                                     strides[2], w, new_residual.data_ptr(), strides[3], y.data_ptr(), strides[4], R, D,
+                                     residual_scale, eps, weight_offset, _stream(stream)), "gdn_residual_rms_norm")

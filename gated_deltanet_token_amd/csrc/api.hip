@@ -7,14 +7,13 @@
 
 #include <mutex>
 
+#include "api_check.h"
 #include "gdn.h"
 #include "gdn_internal.h"
 
-#define GDN_EXPORT extern "C" __attribute__((visibility("default")))
+namespace gdn {
 
-namespace {
-
-thread_local char g_err[512];
+static thread_local char g_err[512];
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -29,25 +28,11 @@ int ok() {
     return GDN_OK;
 }
 
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace gdn
 
-// byte range of a strided row buffer [rows][stride] whose rows use `cols`
-// elements of `elem` bytes
-struct Span {
-    uintptr_t lo, hi;
-};
-Span row_span(const void *p, int64_t rows, int64_t stride, int64_t cols, int64_t elem) {
-    const uintptr_t lo = (uintptr_t)p;
-    if (rows <= 0 || cols <= 0) return {lo, lo};
-    return {lo, lo + (uintptr_t)(((rows - 1) * stride + cols) * elem)};
-}
-// empty ranges overlap nothing
-bool overlap(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
+using namespace gdn;
 
-int hip_status(hipError_t e, const char *what) {
-    if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-    return ok();
-}
+namespace {
 
 int check_conv_common(const void *x, int64_t x_stride, const void *weight, const void *bias,
                       const void *conv_state, int32_t num_slots, const void *y, int64_t y_stride,
@@ -74,7 +59,7 @@ int check_conv_common(const void *x, int64_t x_stride, const void *weight, const
 
 }  // namespace
 
-GDN_EXPORT const char *gdn_last_error(void) { return g_err; }
+GDN_EXPORT const char *gdn_last_error(void) { return gdn::g_err; }
 
 GDN_EXPORT int gdn_build_conv_chunks(const int32_t *qsl_host, int32_t num_seqs, gdn_conv_chunk *out_host,
                                      int32_t capacity, int32_t *n_out) {

@@ -2,7 +2,7 @@
  * gdn.h -- C ABI of the Gated DeltaNet (GDN) token-mixer library for AMD
  * Instinct MI355X (gfx950).
  *
- * The calls that form the layer's data-parallel hot path:
+ * The calls that form the GDN layer's data-parallel hot path:
  *
  *   gdn_build_conv_chunks       host: exact (sequence, 8-token chunk) list
  *   gdn_causal_conv1d_varlen    GPU: width-4 causal conv over packed prefill
@@ -18,6 +18,23 @@
  *                               GPU: the chunkwise rule on a step's prefill
  *                               tokens and the fused decode of its decode
  *                               rows, sharing one grid
+ *
+ * and those of the hybrid model's other layers on the same engine step:
+ *
+ *   gdn_build_step_tables       GPU: a step's query_start_loc, positions,
+ *                               cache slots, pages and conv descriptors from
+ *                               the requests' lengths
+ *   gdn_rope_frequencies        host: rotary frequencies, scaled for long
+ *                               contexts
+ *   gdn_rope_append_kv8         GPU: rotary positions on q and k; k and v
+ *                               written into the 8-bit paged cache
+ *   gdn_paged_attention_kv8     GPU: attention over that cache, any mix of
+ *                               decode rows and prompt chunks
+ *   gdn_paged_attention_kv8_workspace_size
+ *                               host: scratch bytes the attention needs
+ *   gdn_gated_rms_norm          GPU: norm of each head with its output gate
+ *   gdn_residual_rms_norm       GPU: norm after a block, its gate, residual
+ *                               scale and sum, and the next block's norm
  *
  * Conventions shared by every call
  * --------------------------------
@@ -485,6 +502,251 @@ int gdn_chunk_rule_and_fused_decode_noalloc(
     float *state, int32_t num_slots, int32_t num_k_heads, int32_t num_v_heads,
     int32_t head_k_dim, int32_t head_v_dim, float scale, int32_t qk_l2norm,
     void *stream);
+
+/* ------------------------------------------------------------------------
+ * The full-attention layers' side of an engine step, and the norms between
+ * blocks.  A call without tokens (rows, requests) is valid, enqueues nothing
+ * and checks no more than its counts; gdn_build_step_tables fills its outputs
+ * still.
+ * ------------------------------------------------------------------------ */
+
+/* Sequences one gdn_build_step_tables call takes at most. */
+#define GDN_STEP_MAX_SEQS 4096
+
+/*
+ * gdn_build_step_tables -- what every layer of an engine step needs to know
+ * about its requests, built on the GPU from their lengths in one launch:
+ * nothing is read back to the host, so the call can sit in a captured graph.
+ *
+ * With c = context_lens[s] tokens of request s already in the cache, n =
+ * query_lens[s] new ones (negative lengths count as 0) and P = page_size:
+ *   query_start_loc[s] = sum of n over the requests before s;  seq_lens[s] = c + n
+ *   request s holds ceil(c / P) pages, the first entries of its block_table
+ *   row, and takes ceil((c + n) / P) - ceil(c / P) more.  The pages taken,
+ *   counted p = 0, 1, ... over the requests in order, come off the end of the
+ *   free list, free_pages[num_free[0] - 1 - p], and are appended to the rows.
+ *   positions[t] = c + i and slot_mapping[t] = block_table[s][(c + i) / P] * P
+ *   + (c + i) % P for t = query_start_loc[s] + i
+ *   chunks: {s, i} for i < ceil(n / 8), sequences in order: the list that
+ *   gdn_build_conv_chunks makes of query_start_loc
+ *   counts[0..3] = tokens, descriptors, pages taken, pages missing
+ * The caller's free list is not changed: the last counts[2] of its first
+ * num_free[0] entries are in use after the call.
+ *
+ * Room: tokens past num_tokens and descriptors past n_chunks are not written
+ * (counts still has the full numbers).  Entries past the step's own are
+ * filled: positions and slot_mapping with -1, descriptors with {-1, 0}, which
+ * the conv calls skip.  When the free list runs out, or a row of max_pages
+ * entries is full, the missing page's entry (inside the row) and its tokens'
+ * slots are -1 and counts[3] counts it.  Sums past 2^31 - 1 saturate.
+ *
+ *   context_lens, query_lens  int32 [num_seqs]
+ *   free_pages                int32 [free_capacity];  num_free: int32 [1],
+ *                             on the device, clamped to [0, free_capacity]
+ *   block_table               int32 [num_seqs][block_table_stride], in place,
+ *                             max_pages entries of a row in use
+ *   query_start_loc           int32 [num_seqs + 1];  seq_lens: int32 [num_seqs]
+ *   positions                 int32 [num_tokens];  slot_mapping: int64 [num_tokens]
+ *   chunks                    gdn_conv_chunk [n_chunks], or NULL/0
+ *   counts                    int32 [4]
+ *
+ * Errors: GDN_ERR_INVALID (a pointer NULL that its count needs, negative
+ * counts, page_size not a power of two from 1 to 1024, max_pages < 1,
+ * block_table_stride < max_pages, (chunks == NULL) != (n_chunks == 0), an
+ * output overlapping an input or another output); GDN_ERR_UNSUPPORTED (more
+ * than GDN_STEP_MAX_SEQS requests, a pointer off its type's alignment);
+ * GDN_ERR_HIP.
+ */
+int gdn_build_step_tables(const int32_t *context_lens, const int32_t *query_lens, int32_t num_seqs,
+                          const int32_t *free_pages, const int32_t *num_free, int32_t free_capacity,
+                          int32_t *block_table, int64_t block_table_stride, int32_t max_pages,
+                          int32_t page_size, int32_t *query_start_loc, int32_t *seq_lens,
+                          int32_t *positions, int64_t *slot_mapping, int32_t num_tokens,
+                          gdn_conv_chunk *chunks, int32_t n_chunks, int32_t *counts, void *stream);
+
+typedef enum gdn_rope_scaling {
+    GDN_ROPE_PLAIN = 0,    /* f_i = base^(-2i / rotary_dim) */
+    GDN_ROPE_LINEAR = 1,   /* positions interpolated: f_i / factor */
+    GDN_ROPE_NTK = 2,      /* base raised to base * factor^(r / (r - 2)), r = rotary_dim */
+    GDN_ROPE_YARN = 3      /* slow frequencies divided by factor, fast ones kept, a ramp between */
+} gdn_rope_scaling;
+
+/*
+ * gdn_rope_frequencies -- host only, synchronous: the rotary_dim / 2 rotary
+ * frequencies in 64 bits, and the factor of the rotated elements that goes
+ * with them (1 but for YaRN).
+ *
+ * Sources: Su et al., "RoFormer" (2021) for the frequencies; Peng et al.,
+ * "YaRN: Efficient Context Window Extension of Large Language Models" (2023)
+ * for the scalings: with r_i = original_context f_i / 2pi turns over the
+ * original context, f_i gamma + (f_i / factor) (1 - gamma), gamma = clamp((r_i
+ * - beta_slow) / (beta_fast - beta_slow), 0, 1), and the factor 0.1 ln(factor)
+ * + 1.
+ *
+ *   out           host, double [rotary_dim / 2]
+ *   rope_scale    host, receives the factor
+ *   factor        >= 1 (ignored by GDN_ROPE_PLAIN); original_context, beta_fast
+ *                 and beta_slow are GDN_ROPE_YARN's (customary: 32 and 1)
+ *
+ * Errors: GDN_ERR_INVALID (NULL pointers, rotary_dim odd or < 2, base <= 1,
+ * an unknown scaling, factor < 1, for NTK rotary_dim 2, for YaRN
+ * original_context < 1 or beta_fast <= beta_slow).
+ */
+int gdn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                         double original_context, double beta_fast, double beta_slow,
+                         double *out, double *rope_scale);
+
+/*
+ * The 8-bit paged cache of gdn_rope_append_kv8 and gdn_paged_attention_kv8:
+ *   k_cache  e4m3 (OCP: 4 exponent bits, bias 7, 3 mantissa bits, no
+ *            infinities) [num_pages][num_kv_heads][page_size][head_dim]
+ *   v_cache  e4m3 [num_pages][num_kv_heads][head_dim][page_size]: a page's
+ *            tokens are contiguous for each element, the order in which the
+ *            products of weights and values read them
+ *   k_scale, v_scale  fp32 [num_pages][num_kv_heads]
+ * An element is its code times its page's and head's scale.  page_size is 16,
+ * 32 or 64; head_dim 64, 128 or 256.  The caches are 16-byte aligned.
+ */
+
+/*
+ * gdn_rope_append_kv8 -- rotary positions on q and k, and the new k and v
+ * written into the cache, in one launch.
+ *
+ * For token t and pair i < rotary_dim / 2, with angle positions[t] *
+ * frequencies[i]: (a, b) -> rope_scale (a cos - b sin, b cos + a sin), where
+ * (a, b) are elements (i, i + rotary_dim / 2) of a head, or (2i, 2i + 1) with
+ * interleaved != 0; elements from rotary_dim on are kept.  Angles and products
+ * are in 64 bits: a position of a million costs no accuracy.  q_out is rounded
+ * to bf16, k to fp32 before it is coded.
+ *
+ * Cache: token t goes to slot slot_mapping[t] = page * page_size + offset; a
+ * slot outside [0, num_pages * page_size) (padding, -1) is not written.  The
+ * tokens of one page must be consecutive in the call, at consecutive offsets
+ * (the order gdn_build_step_tables gives; otherwise the codes of that page are
+ * undefined, but nothing outside the cache is accessed).  With m the largest
+ * finite magnitude among a page's and head's new elements, the scale is the
+ * least power of two s >= 2^-100 with m <= 448 s -- or the page's present
+ * scale, where its tokens begin at an offset above 0 and that is larger.
+ * Codes are rounded to nearest even.  Where a page's scale grows, the codes
+ * below the first new offset are rounded again to the new one, exact for
+ * powers of two but for codes that leave e4m3's normal range.  Infinities and
+ * NaN are coded as NaN.  Codes past the last new offset stay as they are.
+ *
+ *   q, k, v       bf16, token t head j at q + t*q_stride + j*head_dim (may be
+ *                 column views of one projection's output)
+ *   q_out         bf16 [.][q_out_stride]: not overlapping q, k or v, or q itself
+ *                 with the same stride; q NULL (and q_out NULL): no q
+ *   positions     int32 [num_tokens]
+ *   slot_mapping  int64 [num_tokens]
+ *   frequencies   fp64 [rotary_dim / 2], device; NULL with rotary_dim 0
+ *
+ * Errors: GDN_ERR_INVALID (required pointer NULL, negative counts, head
+ * counts < 1, num_pages < 1, strides too small, q without q_out, an output
+ * overlapping an input); GDN_ERR_UNSUPPORTED (page_size, head_dim, rotary_dim
+ * not a multiple of 16 from 0 to head_dim, strides or pointers off the
+ * alignment contract); GDN_ERR_HIP.
+ */
+int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, int64_t k_stride,
+                        const gdn_bf16 *v, int64_t v_stride, const int32_t *positions,
+                        const int64_t *slot_mapping, const double *frequencies, int32_t rotary_dim,
+                        int32_t interleaved, double rope_scale, gdn_bf16 *q_out, int64_t q_out_stride,
+                        uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+                        int32_t num_pages, int32_t page_size, int32_t num_tokens,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void *stream);
+
+/*
+ * gdn_paged_attention_kv8 -- attention of a step's tokens over the cache.
+ *
+ * Request s owns the tokens [a, a + n) of query_start_loc and keys j in [0,
+ * L), L = seq_lens[s] (its own new tokens among them); key j is row j %
+ * page_size of page block_table[s][j / page_size].  For its token i, at
+ * position p = L - n + i, and q head h (kv head h / (num_q_heads /
+ * num_kv_heads)):
+ *   x_j = scale * (q . k_j);  w = softmax of x over the keys with j <= p if
+ *   causal, j > p - window if window > 0;  o = sum_j w_j v_j
+ * A token that sees no key gets o = 0.  Keys of a page outside [0, num_pages)
+ * (-1 in the block table) or past max_pages are not seen.  Masked keys have
+ * no influence whatever their codes and scales hold, NaN included; cache
+ * bytes past L are free to hold anything.
+ *
+ * Products, softmax statistics and sums are fp32; o is rounded to bf16.
+ *
+ *   q            bf16, token t head h at q + t*q_stride + h*head_dim
+ *   block_table  int32 [num_seqs][block_table_stride], max_pages entries used
+ *   seq_lens     int32 [num_seqs] (negative counts as 0)
+ *   max_seq_len  the largest of seq_lens as the caller knows it; it decides
+ *                how the work is split, and results do not depend on it but
+ *                for rounding (0 < it; a request may be longer)
+ *   o            bf16 [.][o_stride], rows of tokens that no request owns are
+ *                left as they are; must not overlap an input
+ *   workspace    device scratch of gdn_paged_attention_kv8_workspace_size
+ *                bytes for these sizes, 256-byte aligned, contents free (may
+ *                be NULL when that is 0).  Calls that share one must not
+ *                overlap in time.
+ *
+ * Errors: GDN_ERR_INVALID (required pointer NULL, negative counts,
+ * num_q_heads not a positive multiple of num_kv_heads, num_pages or max_pages
+ * < 1, max_seq_len < 1, window < 0, strides too small, o or the workspace
+ * overlapping an operand); GDN_ERR_UNSUPPORTED (page_size, head_dim,
+ * alignment contract); GDN_ERR_CAPACITY (workspace too small); GDN_ERR_HIP.
+ */
+size_t gdn_paged_attention_kv8_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
+
+int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, const uint8_t *k_cache,
+                            const uint8_t *v_cache, const float *k_scale, const float *v_scale,
+                            int32_t num_pages, int32_t page_size, const int32_t *block_table,
+                            int64_t block_table_stride, int32_t max_pages, const int32_t *seq_lens,
+                            const int32_t *query_start_loc, int32_t max_seq_len,
+                            gdn_bf16 *o, int64_t o_stride, int32_t num_seqs, int32_t num_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                            int32_t causal, int32_t window, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * gdn_gated_rms_norm -- root-mean-square norm of each head, times its output
+ * gate (the GDN mixer's output norm; without a gate, the norm of q and k
+ * heads):
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight) * silu(gate)
+ * over head_dim elements, in fp32, rounded once.
+ *
+ *   x, gate, y  bf16, token t head h at x + t*x_stride + h*head_dim; gate may
+ *               be NULL; y may be x itself with the same stride
+ *   weight      bf16 [head_dim] (weight_offset 1: stored about zero)
+ *
+ * Errors: GDN_ERR_INVALID (required pointer NULL, negative num_tokens,
+ * num_heads < 1, strides too small, y overlapping x otherwise, gate or
+ * weight); GDN_ERR_UNSUPPORTED (head_dim not a multiple of 8 up to 512,
+ * alignment contract); GDN_ERR_HIP.
+ */
+int gdn_gated_rms_norm(const gdn_bf16 *x, int64_t x_stride, const gdn_bf16 *gate, int64_t gate_stride,
+                       const gdn_bf16 *weight, gdn_bf16 *y, int64_t y_stride, int32_t num_tokens,
+                       int32_t num_heads, int32_t head_dim, float eps, float weight_offset, void *stream);
+
+/*
+ * gdn_residual_rms_norm -- between two blocks, in one pass over each row:
+ *   u = x;  with post_weight: u = u / sqrt(mean(u^2) + eps) * (weight_offset + post_weight)
+ *   with gate: u = u * sigmoid(gate)
+ *   h = residual + residual_scale * u;  new_residual = h (rounded to bf16)
+ *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
+ * in fp32; y is formed from h before its rounding, so the sum's rounding does
+ * not enter the next block.
+ *
+ *   x, residual, gate, new_residual, y  bf16 [rows][stride], hidden elements
+ *               used; gate may be NULL; new_residual may be residual or x, and
+ *               y may be x, each itself with the same stride
+ *   weight, post_weight  bf16 [hidden]; post_weight may be NULL
+ *
+ * Errors: GDN_ERR_INVALID (required pointer NULL, negative rows, strides too
+ * small, an output overlapping an operand otherwise, or the other output);
+ * GDN_ERR_UNSUPPORTED (hidden not a multiple of 8 up to 16384, alignment
+ * contract); GDN_ERR_HIP.
+ */
+int gdn_residual_rms_norm(const gdn_bf16 *x, int64_t x_stride, const gdn_bf16 *residual, int64_t residual_stride,
+                          const gdn_bf16 *post_weight, const gdn_bf16 *gate, int64_t gate_stride,
+                          const gdn_bf16 *weight, gdn_bf16 *new_residual, int64_t new_residual_stride,
+                          gdn_bf16 *y, int64_t y_stride, int32_t rows, int32_t hidden,
+                          float residual_scale, float eps, float weight_offset, void *stream);
 
 #ifdef __cplusplus
 }
