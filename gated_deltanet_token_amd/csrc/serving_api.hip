@@ -201,8 +201,8 @@ GDN_EXPORT int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, cons
         return fail(GDN_ERR_INVALID, "num_q_heads must be a positive multiple of num_kv_heads");
     if (max_pages < 1 || block_table_stride < max_pages)
         return fail(GDN_ERR_INVALID, "max_pages must be >= 1 and at most block_table_stride");
-    if (max_pages > 0x7fffffff / page_size)
-        return fail(GDN_ERR_UNSUPPORTED, "a row of %d pages of %d tokens passes 2^31 tokens", max_pages, page_size);
+    if (max_pages > (0x7fffffff - 1024) / page_size)     // key numbers, a few tiles past the end too, are 32-bit
+        return fail(GDN_ERR_UNSUPPORTED, "a row of %d pages of %d tokens passes 2^31 - 1024 tokens", max_pages, page_size);
     if (max_seq_len < 1) return fail(GDN_ERR_INVALID, "max_seq_len must be >= 1");
     if (window < 0) return fail(GDN_ERR_INVALID, "negative window");
     const int64_t w = (int64_t)num_q_heads * head_dim;
