@@ -9,7 +9,8 @@ __device__ __forceinline__ bool is_finite(float x) {
     return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
 }
 
-// four codes from four values, round to nearest even; |x| <= 448 or NaN
+// four codes from four values, round to nearest even; |x| <= 448, or infinite or
+// NaN: NaN (the format has no infinities)
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);

@@ -148,6 +148,9 @@ GDN_EXPORT int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gd
         return fail(GDN_ERR_INVALID, "a token stride is smaller than its row of heads");
     if (k_stride % 8 || v_stride % 8 || (q && (q_stride % 8 || q_out_stride % 8)))
         return fail(GDN_ERR_UNSUPPORTED, "token strides must be multiples of 8 elements");
+    // the kernel addresses a page's rows with 32-bit byte offsets
+    if (k_stride >= (1 << 24) || v_stride >= (1 << 24))
+        return fail(GDN_ERR_UNSUPPORTED, "k's and v's token strides must be below 2^24 elements");
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out))
         return fail(GDN_ERR_UNSUPPORTED, "q, k, v and q_out must be 16-byte aligned");
     if (!aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(frequencies, 8))

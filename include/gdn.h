@@ -633,7 +633,8 @@ int gdn_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, doubl
  * NaN are coded as NaN.  Codes past the last new offset stay as they are.
  *
  *   q, k, v       bf16, token t head j at q + t*q_stride + j*head_dim (may be
- *                 column views of one projection's output)
+ *                 column views of one projection's output); k_stride and
+ *                 v_stride below 2^24 elements
  *   q_out         bf16 [.][q_out_stride]: not overlapping q, k or v, or q itself
  *                 with the same stride; q NULL (and q_out NULL): no q
  *   positions     int32 [num_tokens]
