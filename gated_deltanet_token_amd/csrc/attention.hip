@@ -25,6 +25,7 @@ namespace gdn {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
@@ -107,12 +108,46 @@ __device__ __forceinline__ Splits splits_of(int lo, int hi, int chunk, int n) {
     return s;
 }
 
-// partial results of (row, split): D sums and, behind all of them, the maximum and the sum of weights
-__device__ __forceinline__ float *part_o(const AttentionArgs &a, long long row, int split, int n) {
-    return a.workspace + (row * n + split) * a.d;
+// Which requests a launch takes: all, those of at most kSmallRows rows per kv
+// head, or the larger ones.
+enum class Take { kAll, kSmall, kLarge };
+constexpr int kSmallRows = 32;
+
+// A launch's division of its requests' keys, and its partial results: a row's D
+// sums per split, and behind all of them a maximum and a sum of weights per
+// (row, split).  Rows are (token, q head), or for the small requests alone
+// (request, row of kSmallRows, kv head).
+struct Division {
+    int chunk, splits;
+    float *sums, *stats;
+};
+__device__ __forceinline__ float *part_o(const Division &v, int d, long long row, int split) {
+    return v.sums + (row * v.splits + split) * d;
 }
-__device__ __forceinline__ float *part_ml(const AttentionArgs &a, long long row, int split, int n) {
-    return a.workspace + (long long)a.num_tokens * a.num_q_heads * n * a.d + (row * n + split) * 2;
+__device__ __forceinline__ float *part_ml(const Division &v, long long row, int split) {
+    return v.stats + (row * v.splits + split) * 2;
+}
+template <Take TAKE>
+__device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int t, int h, long long row, int hk) {
+    return TAKE == Take::kSmall ? ((long long)s * kSmallRows + row) * a.num_kv_heads + hk
+                                : (long long)t * a.num_q_heads + h;
+}
+
+// The largest finite magnitude m of a row of q, brought to [128, 256): the
+// power of two for it, within [2^-120, 2^126].
+__device__ __forceinline__ float split_factor(float m) {
+    const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
+    return __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
+}
+// four elements' two parts
+__device__ __forceinline__ void split4(const float *f, float up, int &hi, int &lo) {
+    float v[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f[e] * up;           // infinities and NaN: NaN codes
+    const uint32_t w = e4m3x4(v[0], v[1], v[2], v[3]);
+    e4m3_values(w, b);
+    hi = (int)w;
+    lo = (int)e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
 }
 
 // ---------------------------------------------------------------------------
@@ -128,8 +163,8 @@ __device__ __forceinline__ float *part_ml(const AttentionArgs &a, long long row,
 // one pair of scales per lane.  For that, row i of the a-th K operand is key
 // 16 (i / 4) + 4 a + i % 4.
 // ---------------------------------------------------------------------------
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionArgs a, int chunk, int n_splits) {
+template <int D, int W, Take TAKE>
+__global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionArgs a, Division v) {
     constexpr int KS = D >= 128 ? D / 128 : 1;       // contraction steps of 128
     constexpr int KL = D / 64;                       // 16-byte loads per key operand
     constexpr int DT = D / 16;                       // operands of 16 value elements
@@ -141,27 +176,32 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
     constexpr bool QLDS = D == 256;
     __shared__ i32x4 q_lds[QLDS ? 4 * KS : 1][64];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4, kg = c >> 2;
     const int G = a.num_q_heads / a.num_kv_heads;
-    const long long unit = blockIdx.x / n_splits;
-    const int split = blockIdx.x - (int)(unit * n_splits);
+    const long long unit = blockIdx.x / v.splits;
+    const int split = blockIdx.x - (int)(unit * v.splits);
     const long long tile = unit / a.num_kv_heads;
     const int hk = (int)(unit - tile * a.num_kv_heads);
-    int within;
-    const int s = find_request(a, tile, G, kTileRows, within);
+    int within, s;
+    if constexpr (TAKE == Take::kSmall) {
+        s = (int)(tile / (kSmallRows / kTileRows));
+        within = (int)(tile % (kSmallRows / kTileRows));
+    } else {
+        s = find_request(a, tile, G, kTileRows, within);
+    }
     const Request rq = request_of(a, s);
     const long long row0 = (long long)within * kTileRows, n_rows = (long long)rq.n * G;
-    if (within < 0 || row0 >= n_rows) return;
+    if (within < 0 || row0 >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
     const int i_first = (int)(row0 / G), i_last = (int)(min(row0 + kTileRows, n_rows) - 1) / G;
     int lo, hi, x0, x1;                              // keys that some row sees, that every row sees
     key_range(a, rq, i_first, lo, x1);
     key_range(a, rq, i_last, x0, hi);
-    const Splits sp = splits_of(lo, hi, chunk, n_splits);
+    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
     if (split != sp.first && (split < sp.first || split > sp.last)) return;
     const bool whole = sp.last <= sp.first;          // no other split: write o itself
-    const int k_lo = max(lo, split * chunk);
-    const int k_hi = split == n_splits - 1 ? hi : min(hi, (split + 1) * chunk);
+    const int k_lo = max(lo, split * v.chunk);
+    const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
 
     const long long row = row0 + c;
     const int i_row = (int)(row / G), h = hk * G + (int)(row - (long long)i_row * G);
@@ -192,30 +232,22 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
             for (int e = 0; e < 16; ++e) m = is_finite(f[l][e]) ? fmaxf(m, fabsf(f[l][e])) : m;
         }
         m = max_over(max_over(m, 16), 32);
-        // up = 2^(7 - exponent of m), within [2^-120, 2^126]
-        const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
-        const float up = __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
+        const float up = split_factor(m);
         unscale = 1.f / up;
 #pragma unroll
-        for (int l = 0; l < KL; ++l) {
+        for (int l = 0; l < KL; ++l)
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                float v[4], b[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = is_finite(f[l][4 * w + e]) ? f[l][4 * w + e] * up : __builtin_bit_cast(float, 0x7fc00000u);
-                const uint32_t hw = e4m3x4(v[0], v[1], v[2], v[3]);
-                e4m3_values(hw, b);
-                const uint32_t lw = e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
+                int hw, lw;
+                split4(&f[l][4 * w], up, hw, lw);
                 if constexpr (D == 64) {
-                    qh[0][w] = (int)hw;
-                    qh[0][4 + w] = (int)lw;
+                    qh[0][w] = hw;
+                    qh[0][4 + w] = lw;
                 } else {
-                    qh[l / 2][4 * (l & 1) + w] = (int)hw;
-                    ql[l / 2][4 * (l & 1) + w] = (int)lw;
+                    qh[l / 2][4 * (l & 1) + w] = hw;
+                    ql[l / 2][4 * (l & 1) + w] = lw;
                 }
             }
-        }
     }
     const float to_log2 = a.scale * kLog2e * unscale;
     if constexpr (QLDS) {
@@ -423,7 +455,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
 #pragma unroll
     for (int w = 0; w < W; ++w) l_all += red_l[w][c] * __builtin_amdgcn_exp2f(red_m[w][c] - at);
     const float f = __builtin_amdgcn_exp2f(m - at);
-    const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
+    const long long out_row = part_row<TAKE>(a, s, rq.begin + i_row, h, row, hk);
     const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
 #pragma unroll
     for (int t0 = 0; t0 < DT; t0 += DTH) {
@@ -443,53 +475,418 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
                 w.y = pack_bf16x2(sum.z * inv, sum.w * inv);
                 *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = w;
             } else {
-                *reinterpret_cast<f32x4 *>(part_o(a, out_row, split, n_splits) + d) = sum;
+                *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, split) + d) = sum;
             }
         }
     }
     if (!whole && wave == 0 && g == 0 && live) {
-        float *ml = part_ml(a, out_row, split, n_splits);
+        float *ml = part_ml(v, out_row, split);
         ml[0] = m_all;
         ml[1] = l_all;
     }
 }
 
 // ---------------------------------------------------------------------------
-// The splits of a row joined: one wave per row, its splits' sums brought to
-// the common maximum.
+// Many rows: one workgroup of four waves per (128 rows of one request that
+// share a kv head, split of its keys); a wave holds 32 of the rows.  Bound by
+// the matrix cores and the exponentials: tiles of 64 keys and values pass
+// through the LDS once for all four waves, the next one on its way from HBM
+// to registers meanwhile, with one barrier per tile between two buffers.
+//
+// Lanes: with c = lane % 32 and h = lane / 32, a lane holds row c and the keys
+// 32 h .. 32 h + 31 of the tile, x[a][r] being key 32 h + 16 a + r.  For that,
+// row i of the a-th K operand is key 32 (i / 4 % 2) + 16 a + 4 (i / 8) + i % 4.
+// LDS rows are cut into 16-byte pieces, piece p of a row kept at p ^ (a few
+// bits of the row's number) so that 16 lanes that read the same piece of their
+// rows find it in 16 different places of the 256 bytes that the banks span.
 // ---------------------------------------------------------------------------
+constexpr int kManyRows = 128, kManyThreads = 256;
+
 template <int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, int chunk, int n_splits) {
+struct ManyLds {
+    uint4 k[2][kTileKeys * D / 16], v[2][kTileKeys * D / 16];
+    float ks[2][4], vs[2][4];
+    int ok[2][4];
+};
+
+template <int D>
+__device__ __forceinline__ int k_piece(int key, int p) {
+    constexpr int shift = D == 256 ? 0 : D == 128 ? 1 : 2;
+    return key * (D / 16) + (p ^ (((key & 7) | (key >> 5 & 1) << 3) >> shift));
+}
+__device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (d >> 2 & 3)); }
+
+template <int D>
+__global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many_kernel(AttentionArgs a, Division v) {
+    constexpr int KS = D / 64;                       // contraction steps of 64
+    constexpr int DT = D / 32;                       // operands of 32 value elements
+    constexpr int NL = D / 64;                       // 16-byte loads of a thread, of keys and of values
+    __shared__ ManyLds<D> lds;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 31, h2 = lane >> 5;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    // the last tiles see the most keys and go first; a kv head's workgroups are
+    // num_kv_heads apart, so that with eight heads an XCD keeps to one
+    const long long units = gridDim.x / v.splits, unit = blockIdx.x / v.splits;
+    const int split = blockIdx.x - (int)(unit * v.splits);
+    const long long tile = units / a.num_kv_heads - 1 - unit / a.num_kv_heads;
+    const int hk = (int)(unit % a.num_kv_heads);
+    int within;
+    const int s = find_request(a, tile, G, kManyRows, within);
+    const Request rq = request_of(a, s);
+    const long long row0 = (long long)within * kManyRows, n_rows = (long long)rq.n * G;
+    if (within < 0 || row0 >= n_rows || n_rows <= kSmallRows) return;
+    int lo, hi, x0, x1;
+    key_range(a, rq, (int)(row0 / G), lo, x1);
+    key_range(a, rq, (int)(min(row0 + kManyRows, n_rows) - 1) / G, x0, hi);
+    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
+    if (split != sp.first && (split < sp.first || split > sp.last)) return;
+    const bool whole = sp.last <= sp.first;
+    const int k_lo = max(lo, split * v.chunk);
+    const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
+
+    // this wave's rows
+    const long long wrow = row0 + 32 * wave, row = wrow + c;
+    const bool live = row < n_rows;
+    const int i_row = live ? (int)(row / G) : 0, h = hk * G + (live ? (int)(row - (long long)i_row * G) : 0);
+    int jb = 0, je = 0;
+    if (live) key_range(a, rq, i_row, jb, je);
+    jb = max(jb, k_lo);
+    je = min(je, k_hi);
+    // keys that some row of the wave sees [w_lo, w_hi), that all do [w_all0, w_all1)
+    int w_lo = 0, w_hi = 0, w_all0 = 0, w_all1 = 0;
+    if (wrow < n_rows) {
+        key_range(a, rq, (int)(wrow / G), w_lo, w_all1);
+        key_range(a, rq, (int)((min(wrow + 32, n_rows) - 1) / G), w_all0, w_hi);
+        w_lo = max(w_lo, k_lo);
+        w_hi = min(w_hi, k_hi);
+        w_all0 = max(w_all0, k_lo);
+        w_all1 = min(w_all1, k_hi);
+    }
+
+    // q's two parts: bytes 16 m + e of step st are elements 64 st + 32 h2 + 16 m + e
+    i32x8 qh[KS], ql[KS];
+    float to_log2;
+    {
+        const uint16_t *qp = a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D + 32 * h2;
+        float m = 0.f;
+#pragma unroll
+        for (int st = 0; st < KS; ++st)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float f[8];
+                unpack8(*reinterpret_cast<const uint4 *>(qp + 64 * st + 8 * b), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = is_finite(f[e]) ? fmaxf(m, fabsf(f[e])) : m;
+            }
+        m = max_over(m, 32);
+        const float up = split_factor(m);
+        to_log2 = a.scale * kLog2e * (1.f / up);
+#pragma unroll
+        for (int st = 0; st < KS; ++st)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float f[8];
+                unpack8(*reinterpret_cast<const uint4 *>(qp + 64 * st + 8 * b), f);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    int hw, lw;
+                    split4(f + 4 * w, up, hw, lw);
+                    qh[st][2 * b + w] = hw;
+                    ql[st][2 * b + w] = lw;
+                }
+            }
+    }
+
+    // staging: a thread's 16-byte pieces of a tile
+    const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
+    const int32_t *bt = a.block_table + s * a.block_table_stride;
+    auto page_at = [&](int j) {
+        const int p = j >> shift;
+        const int id = j < k_hi && p < a.max_pages ? bt[p] : -1;
+        return (unsigned)id < (unsigned)a.num_pages ? id : -1;
+    };
+    constexpr int PPK = D / 16, KEYS = kManyThreads / PPK;      // pieces per key; keys per load
+    const int k_key = tid / PPK, k_p = tid % PPK, v_g = tid & 3, v_d = tid >> 2;
+    uint4 kr[NL], vr[NL];
+    float s_ks = 0.f, s_vs = 0.f;
+    int idk[NL], idv;
+    auto load_ids = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + i * KEYS + k_key);
+        idv = page_at(j0 + 16 * v_g);
+    };
+    int ok_next = 0;
+    auto load_tile = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int j = j0 + i * KEYS + k_key;
+            kr[i] = *reinterpret_cast<const uint4 *>(
+                a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + (j & in_page)) * D + 16 * k_p);
+        }
+        const int jv = j0 + 16 * v_g;
+        const long long ph = (long long)max(idv, 0) * a.num_kv_heads + hk;
+        const uint8_t *p = a.v_cache + (ph * D + v_d) * a.page + (jv & in_page);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const uint4 *>(p + (long long)64 * i * a.page);
+        if (tid < 4) {
+            s_ks = a.k_scale[ph];
+            s_vs = a.v_scale[ph];
+        }
+        ok_next = idv >= 0;
+    };
+    auto put_tile = [&](int j0, int buf) {
+        // values that no row of the workgroup sees may be anything: zero
+        if (j0 < k_lo || j0 + kTileKeys > k_hi || !ok_next) {
+            uint32_t keep[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                keep[w] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int j = j0 + 16 * v_g + 4 * w + b;
+                    if (ok_next && j >= k_lo && j < k_hi) keep[w] |= 0xffu << (8 * b);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                vr[i].x &= keep[0];
+                vr[i].y &= keep[1];
+                vr[i].z &= keep[2];
+                vr[i].w &= keep[3];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            lds.k[buf][k_piece<D>(i * KEYS + k_key, k_p)] = kr[i];
+            lds.v[buf][v_piece(64 * i + v_d, v_g)] = vr[i];
+        }
+        if (tid < 4) {
+            lds.ks[buf][tid] = s_ks;
+            lds.vs[buf][tid] = s_vs;
+            lds.ok[buf][tid] = ok_next;
+        }
+    };
+
+    f32x16 o[DT] = {};
+    float m = kNegInf, l = 0.f;
+    int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
+    if (j0 < k_hi) {
+        load_ids(j0);
+        load_tile(j0);
+        load_ids(j0 + kTileKeys);
+        put_tile(j0, 0);
+    }
+    __syncthreads();
+    for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
+        const int jn = j0 + kTileKeys;
+        if (jn < k_hi) {
+            load_tile(jn);
+            load_ids(jn + kTileKeys);
+        }
+        if (j0 < w_hi && j0 + kTileKeys > w_lo) {
+            f32x16 x[2] = {};
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int key = 32 * (c >> 2 & 1) + 16 * t + 4 * (c >> 3) + (c & 3);
+#pragma unroll
+                for (int st = 0; st < KS; ++st) {
+                    const uint4 u = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2)];
+                    const uint4 w = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2 + 1)];
+                    const i32x8 k8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
+                    x[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[st], x[t], 0, 0, 0, 0, 0, 0);
+                    x[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x[t], 0, 0, 0, 0, 0, 0);
+                }
+            }
+            const int ok0 = lds.ok[buf][2 * h2], ok1 = lds.ok[buf][2 * h2 + 1];
+            const bool masked = j0 < w_all0 || jn > w_all1 || __any(!(ok0 && ok1));
+            float mx = kNegInf;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float factor = to_log2 * lds.ks[buf][2 * h2 + t];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[t][r] *= factor;
+            }
+            if (masked)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int j = j0 + 32 * h2 + 16 * t + r;
+                        if (!((t ? ok1 : ok0) && j >= jb && j < je)) x[t][r] = kNegInf;
+                    }
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[t][r]);
+            mx = max_over(mx, 32);
+            if (__any(mx > m)) {
+                const float m_new = fmaxf(m, mx);
+                const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+                m = m_new;
+                l *= f;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) o[t] *= f;
+            }
+            const float at = m == kNegInf ? 0.f : m;
+            bf16x8 p[4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float vs = lds.vs[buf][2 * h2 + t];
+                uint32_t pw[8];
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    float e0 = __builtin_amdgcn_exp2f(x[t][r] - at), e1 = __builtin_amdgcn_exp2f(x[t][r + 1] - at);
+                    l += e0 + e1;
+                    e0 *= vs;
+                    e1 *= vs;
+                    if (masked) {        // a masked key's scale may be anything
+                        if (x[t][r] == kNegInf) e0 = 0.f;
+                        if (x[t][r + 1] == kNegInf) e1 = 0.f;
+                    }
+                    pw[r / 2] = pack_bf16x2(e0, e1);
+                }
+                const i32x4 u = {(int)pw[0], (int)pw[1], (int)pw[2], (int)pw[3]};
+                const i32x4 w = {(int)pw[4], (int)pw[5], (int)pw[6], (int)pw[7]};
+                p[2 * t] = __builtin_bit_cast(bf16x8, u);
+                p[2 * t + 1] = __builtin_bit_cast(bf16x8, w);
+            }
+            // NaN among the values that some rows see must reach those only
+            bool bad = false;
+            if (masked) {
+                uint32_t any = 0;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint4 w = lds.v[buf][v_piece(32 * t + c, 2 * h2 + g)];
+                        any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+                    }
+                bad = __any(any != 0);
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint4 w = lds.v[buf][v_piece(32 * t + c, 2 * h2 + g)];
+                    if (bad) {
+                        // zeroed here; the rows that see them get theirs from a count
+                        uint32_t d[4] = {w.x, w.y, w.z, w.w}, ones[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t b = nan_codes(d[i]) >> 7;
+                            d[i] &= ~(b * 0xffu);
+                            ones[i] = b * 0x38u;                     // e4m3 1.0
+                        }
+                        w = make_uint4(d[0], d[1], d[2], d[3]);
+                        bf16x8 n0, n1;
+                        codes_to_bf16(make_uint4(ones[0], ones[1], ones[2], ones[3]), n0, n1);
+                        uint32_t see[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = j0 + 32 * h2 + 16 * g + 2 * i;
+                            see[i] = (j >= jb && j < je ? 0x3f80u : 0u) | (j + 1 >= jb && j + 1 < je ? 0x3f800000u : 0u);
+                        }
+                        const i32x4 s0 = {(int)see[0], (int)see[1], (int)see[2], (int)see[3]};
+                        const i32x4 s1 = {(int)see[4], (int)see[5], (int)see[6], (int)see[7]};
+                        f32x16 count = {};
+                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n0, __builtin_bit_cast(bf16x8, s0), count, 0, 0, 0);
+                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n1, __builtin_bit_cast(bf16x8, s1), count, 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (count[r] > 0.f) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
+                    }
+                    bf16x8 v0, v1;
+                    codes_to_bf16(w, v0, v1);
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, p[2 * g], o[t], 0, 0, 0);
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, p[2 * g + 1], o[t], 0, 0, 0);
+                }
+        }
+        if (jn < k_hi) put_tile(jn, buf ^ 1);
+        __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
+    // element 32 t + 8 q + 4 h2 + r of row c is o[t][4 q + r]
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int d = 32 * t + 8 * q + 4 * h2;
+            if (whole) {
+                uint2 w;
+                w.x = pack_bf16x2(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
+                w.y = pack_bf16x2(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
+                *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = w;
+            } else {
+                *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, split) + d) =
+                    f32x4{o[t][4 * q], o[t][4 * q + 1], o[t][4 * q + 2], o[t][4 * q + 3]};
+            }
+        }
+    if (!whole && h2 == 0) {
+        float *ml = part_ml(v, out_row, split);
+        ml[0] = m;
+        ml[1] = l;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The splits of a row joined: one wave per row of the launch that made them,
+// its splits' sums brought to the common maximum.
+// ---------------------------------------------------------------------------
+template <int D, Take TAKE>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Division v, long long rows, int tile_rows) {
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= (long long)a.num_tokens * a.num_q_heads) return;
-    const int t = (int)(row / a.num_q_heads), h = (int)(row - (long long)t * a.num_q_heads);
-    // the request of token t: tiles of one row per token are its tokens
-    int lo = 0, n = a.num_seqs;
-    while (n > 1) {
-        const int step = (n + 63) / 64;
-        const unsigned long long b = __ballot(lane * step < n && a.qsl[lo + lane * step] <= t);
-        const int k = b ? 63 - __builtin_clzll(b) : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    const Request rq = request_of(a, lo);
-    if (t < rq.begin || t >= rq.begin + rq.n) return;
-    // the keys of the row's tile decide which splits wrote
+    const long long part = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (part >= rows) return;
     const int G = a.num_q_heads / a.num_kv_heads;
-    const long long r = (long long)(t - rq.begin) * G + h % G, r0 = r / kTileRows * kTileRows;
-    const int i_first = (int)(r0 / G), i_last = (int)(min(r0 + kTileRows, (long long)rq.n * G) - 1) / G;
+    int s, t, h;
+    long long r;                            // the row within its request and kv head
+    if constexpr (TAKE == Take::kSmall) {
+        const int hk = (int)(part % a.num_kv_heads);
+        r = part / a.num_kv_heads % kSmallRows;
+        s = (int)(part / a.num_kv_heads / kSmallRows);
+        h = hk * G + (int)(r % G);
+        t = 0;
+    } else {
+        t = (int)(part / a.num_q_heads);
+        h = (int)(part - (long long)t * a.num_q_heads);
+        s = 0;
+        int n = a.num_seqs;                 // the request of token t, 64 candidates per step
+        while (n > 1) {
+            const int step = (n + 63) / 64;
+            const unsigned long long b = __ballot(lane * step < n && a.qsl[s + lane * step] <= t);
+            const int k = b ? 63 - __builtin_clzll(b) : 0;
+            s += k * step;
+            n = min(step, n - k * step);
+        }
+    }
+    const Request rq = request_of(a, s);
+    const long long n_rows = (long long)rq.n * G;
+    if constexpr (TAKE == Take::kSmall) {
+        if (n_rows > kSmallRows || r >= n_rows) return;
+        t = rq.begin + (int)(r / G);
+    } else {
+        if (t < rq.begin || t >= rq.begin + rq.n || (TAKE == Take::kLarge && n_rows <= kSmallRows)) return;
+        r = (long long)(t - rq.begin) * G + h % G;
+    }
+    // the keys of the row's tile decide which splits wrote
+    const long long r0 = r / tile_rows * tile_rows;
     int k_lo, k_hi, x;
-    key_range(a, rq, i_first, k_lo, x);
-    key_range(a, rq, i_last, x, k_hi);
-    const Splits sp = splits_of(k_lo, k_hi, chunk, n_splits);
+    key_range(a, rq, (int)(r0 / G), k_lo, x);
+    key_range(a, rq, (int)((min(r0 + tile_rows, n_rows) - 1) / G), x, k_hi);
+    const Splits sp = splits_of(k_lo, k_hi, v.chunk, v.splits);
     if (sp.last <= sp.first) return;
     float m = kNegInf, l = 0.f, o[E] = {};
-    for (int i = sp.first; i <= sp.last; ++i) m = fmaxf(m, part_ml(a, row, i, n_splits)[0]);
+    for (int i = sp.first; i <= sp.last; ++i) m = fmaxf(m, part_ml(v, part, i)[0]);
     const float at = m == kNegInf ? 0.f : m;
     for (int i = sp.first; i <= sp.last; ++i) {
-        const float *ml = part_ml(a, row, i, n_splits), *p = part_o(a, row, i, n_splits);
+        const float *ml = part_ml(v, part, i), *p = part_o(v, D, part, i);
         const float f = __builtin_amdgcn_exp2f(ml[0] - at);
         l = __builtin_fmaf(ml[1], f, l);
 #pragma unroll
@@ -502,53 +899,94 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, in
 }
 
 // ---------------------------------------------------------------------------
-// How a call is split.  A workgroup of the few-rows kernel holds eight waves;
-// splits are made until there is a workgroup for every CU, each split at least
-// one tile per wave.
+// How a call is split.  With at most a token per request on average the
+// few-rows kernel takes everything; else it takes the requests of up to
+// kSmallRows rows, and the many-rows kernel the others (16 rows of a wave cost
+// it as much as 32, and it reads a key once for 128 rows).  Keys are split
+// until there is a workgroup for every CU, each with at least kMinChunk keys.
 // ---------------------------------------------------------------------------
 constexpr int few_waves(int d) { return d == 256 ? 4 : 8; }
 constexpr int kCUs = 256;
 constexpr int kMinChunk = 8 * kTileKeys;
 
-struct Plan {
-    long long units;    // (row tile, kv head) pairs, upper bound
+struct Launch {
+    long long units;        // (row tile, kv head) pairs, upper bound; 0: none
+    long long rows;         // of partial results
     int chunk, splits;
+    long long floats;       // of partial results
 };
 
-static Plan plan_of(long long num_tokens, long long num_seqs, int num_q_heads, int num_kv_heads, int max_seq_len) {
-    Plan p;
-    const long long group = num_q_heads / num_kv_heads;
-    p.units = (num_tokens * group / kTileRows + num_seqs) * num_kv_heads;
-    // tiles that hold rows, as far as the host can tell
-    const long long full = num_tokens * group / kTileRows, asked = num_tokens < num_seqs ? num_tokens : num_seqs;
-    const long long busy = num_kv_heads * (full > asked ? full : asked);
-    long long want = busy > 0 ? (kCUs + busy - 1) / busy : 1;
+// `busy`: row tiles that hold rows, as far as the host can tell
+static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len) {
+    Launch p{tiles * kv_heads, rows, 0x40000000, 1, 0};
+    busy *= kv_heads;
+    long long want = busy > 0 ? kCUs / busy : 1;
     const long long most = (max_seq_len + (long long)kMinChunk - 1) / kMinChunk;
     if (want > most) want = most;
-    if (want < 1) want = 1;
-    long long chunk = (max_seq_len + want - 1) / want;
-    chunk = (chunk + kTileKeys - 1) / kTileKeys * kTileKeys;
-    p.splits = (int)((max_seq_len + chunk - 1) / chunk);
-    p.chunk = (int)(p.splits == 1 ? 0x40000000 : chunk);
+    if (want > 1) {
+        const long long chunk = ((max_seq_len + want - 1) / want + kTileKeys - 1) / kTileKeys * kTileKeys;
+        p.splits = (int)((max_seq_len + chunk - 1) / chunk);
+        if (p.splits > 1) {
+            p.chunk = (int)chunk;
+            p.floats = rows * p.splits * (d + 2);
+        }
+    }
+    return p;
+}
+
+struct Plan {
+    Take few_takes;
+    Launch few, many;
+};
+
+static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len) {
+    const long long G = q_heads / kv_heads;
+    Plan p{};
+    if (T <= S) {
+        p.few_takes = Take::kAll;
+        const long long full = T * G / kTileRows;
+        p.few = divide(full + S, full > T ? full : T, T * q_heads, kv_heads, d, max_seq_len);
+    } else {
+        p.few_takes = Take::kSmall;
+        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len);
+        const long long full = T * G / kManyRows;
+        p.many = divide(full + S, full > 1 ? full : 1, T * q_heads, kv_heads, d, max_seq_len);
+    }
     return p;
 }
 
 int64_t attention_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d, int max_seq_len) {
-    const Plan p = plan_of(num_tokens, num_seqs, num_q_heads, num_kv_heads, max_seq_len);
-    if (p.splits == 1) return 0;
-    return (int64_t)num_tokens * num_q_heads * p.splits * (d + 2) * 4;
+    const Plan p = plan_of(num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
+    return (p.few.floats + p.many.floats) * 4;
+}
+
+template <int D, Take TAKE>
+static hipError_t launch_few(const AttentionArgs &a, const Launch &p, float *ws, hipStream_t stream) {
+    const long long blocks = p.units * p.splits;
+    if (blocks > 0x7fffffffLL || p.rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const Division v{p.chunk, p.splits, ws, ws + p.rows * p.splits * D};
+    hipLaunchKernelGGL((attention_few_kernel<D, few_waves(D), TAKE>), dim3((unsigned)blocks), dim3(64 * few_waves(D)), 0,
+                       stream, a, v);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((attention_join_kernel<D, TAKE>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, a, v,
+                           p.rows, kTileRows);
+    return hipGetLastError();
 }
 
 template <int D>
 static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
-    const Plan p = plan_of(a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, a.max_seq_len);
-    const long long blocks = p.units * p.splits, rows = (long long)a.num_tokens * a.num_q_heads;
-    if (blocks > 0x7fffffffLL || rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((attention_few_kernel<D, few_waves(D)>), dim3((unsigned)blocks), dim3(64 * few_waves(D)), 0, stream, a, p.chunk,
-                       p.splits);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((attention_join_kernel<D>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, a, p.chunk,
-                           p.splits);
+    const Plan p = plan_of(a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
+    if (p.few_takes == Take::kAll) return launch_few<D, Take::kAll>(a, p.few, a.workspace, stream);
+    const long long blocks = p.many.units * p.many.splits;
+    if (blocks > 0x7fffffffLL || p.many.rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    const hipError_t e = launch_few<D, Take::kSmall>(a, p.few, a.workspace, stream);
+    if (e != hipSuccess) return e;
+    float *ws = a.workspace + p.few.floats;
+    const Division v{p.many.chunk, p.many.splits, ws, ws + p.many.rows * p.many.splits * D};
+    hipLaunchKernelGGL((attention_many_kernel<D>), dim3((unsigned)blocks), dim3(kManyThreads), 0, stream, a, v);
+    if (p.many.splits > 1)
+        hipLaunchKernelGGL((attention_join_kernel<D, Take::kLarge>), dim3((unsigned)((p.many.rows + 3) / 4)), dim3(256), 0,
+                           stream, a, v, p.many.rows, kManyRows);
     return hipGetLastError();
 }
 
