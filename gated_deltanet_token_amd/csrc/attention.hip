@@ -56,14 +56,15 @@ __device__ __forceinline__ void key_range(const AttentionArgs &a, const Request 
     jb = a.window > 0 && upto > a.window ? upto - a.window : 0;
 }
 
-// Row tiles: request s owns the tile numbers from floor(query_start_loc[s] * G
-// / rows) + s on, G rows per token: at least as many as it needs, found
-// without a list.  Returns the last request whose first tile is at or before
-// `tile` (64 candidates per step), and the tile's number within it.
-__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int &within) {
+// Row tiles without a list: request s owns the tile numbers from
+// floor(query_start_loc[s] * G / rows) + s * each on, G rows per token.  With
+// each = 1 that is as many as it needs or more, with each = 0 as many as it
+// needs behind its first one.  Returns the last request whose first number is at
+// or before `tile` (64 candidates per step), and the tile's place in it.
+__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, int &within) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = a.num_seqs;
-    auto first = [&](int s) { return (long long)max(a.qsl[s], 0) * group / rows + s; };
+    auto first = [&](int s) { return (long long)max(a.qsl[s], 0) * group / rows + s * each; };
     while (n > 1) {
         const int step = (n + 63) / 64;
         const bool in = lane * step < n && first(lo + lane * step) <= tile;
@@ -79,22 +80,37 @@ __device__ __forceinline__ int find_request(const AttentionArgs &a, long long ti
 
 __device__ __forceinline__ float max_over(float x, int lanes_apart) { return fmaxf(x, __shfl_xor(x, lanes_apart, 64)); }
 
-// 16 codes -> 16 bf16 values
-__device__ __forceinline__ void codes_to_bf16(const uint4 &w, bf16x8 &lo, bf16x8 &hi) {
-    const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-    uint32_t r[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d[i], 1.0f, false));
-        r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d[i], 1.0f, true));
-    }
-    const i32x4 a = {(int)r[0], (int)r[1], (int)r[2], (int)r[3]}, b = {(int)r[4], (int)r[5], (int)r[6], (int)r[7]};
-    lo = __builtin_bit_cast(bf16x8, a);
-    hi = __builtin_bit_cast(bf16x8, b);
+// 8 codes -> 8 bf16 values
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w0, uint32_t w1) {
+    const i32x4 v = {__builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false)),
+                     __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true)),
+                     __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false)),
+                     __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true))};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// 8 bf16 from packed pairs
+__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const i32x4 v = {(int)a, (int)b, (int)c, (int)d};
+    return __builtin_bit_cast(bf16x8, v);
 }
 
 // per byte: 0x80 where an e4m3 code is NaN (0x7f or 0xff)
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// a word's NaN codes become zero; returned: whether there were any
+__device__ __forceinline__ uint32_t take_nan(uint32_t &w) {
+    const uint32_t b = nan_codes(w) >> 7;
+    w &= ~(b * 0xffu);
+    return b;
+}
+// the bytes of a word of keys j .. j + 3 that lie in [lo, hi)
+__device__ __forceinline__ uint32_t key_bytes(int j, int lo, int hi) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (j + b >= lo && j + b < hi) m |= 0xffu << (8 * b);
+    return m;
+}
 
 // The splits of a row tile's keys [lo, hi): split i takes the keys of [i C,
 // (i + 1) C), the last one all that follow.
@@ -106,6 +122,29 @@ __device__ __forceinline__ Splits splits_of(int lo, int hi, int chunk, int n) {
     s.first = min(lo / chunk, n - 1);
     s.last = hi > lo ? min((hi - 1) / chunk, n - 1) : s.first - 1;
     return s;
+}
+
+// A tile that some of a wave's rows see and others do not cannot pass NaN codes
+// of its values through the matrix cores: they would reach all rows.  They go
+// in as zeros there, and this pass, for a wave that met any, finds the sums
+// that they belong to: bit i of `bits` for the lane's sum i, element `element(i)`
+// of the row that sees [jb, je).  `late(j0)`: whether the tile at j0 went in so.
+template <int N, typename Late, typename Element, typename Page>
+__device__ __forceinline__ void find_nan(const AttentionArgs &a, int hk, int j0, int end, int step, int tile, int jb, int je,
+                                         unsigned long long (&bits)[(N + 63) / 64], Late late, Element element, Page page_at) {
+#pragma unroll 1
+    for (; j0 < end; j0 += step) {
+        if (!late(j0)) continue;
+#pragma unroll 1
+        for (int j = j0; j < min(j0 + tile, end); ++j) {
+            const int page = page_at(j);
+            if ((unsigned)page >= (unsigned)a.num_pages || j < jb || j >= je) continue;
+            const uint8_t *v = a.v_cache + ((long long)page * a.num_kv_heads + hk) * a.d * a.page + (j & (a.page - 1));
+#pragma unroll 1
+            for (int i = 0; i < N; ++i)
+                if ((v[(long long)element(i) * a.page] & 0x7f) == 0x7f) bits[N > 64 ? i / 64 : 0] |= 1ull << (i & 63);
+        }
+    }
 }
 
 // Which requests a launch takes: all, those of at most kSmallRows rows per kv
@@ -151,20 +190,27 @@ __device__ __forceinline__ void split4(const float *f, float up, int &hi, int &l
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: one workgroup of W waves per (16 rows of one request that share a
-// kv head, split of its keys).  Bound by reading the cache: each wave takes
-// every W-th tile of 64 keys straight from HBM into registers in the order of
-// the matrix operands (16-byte loads, whole 64-byte sectors), with the next
-// tile's keys and values on their way while it works on this one.  The waves'
-// sums are joined in the LDS.
+// Few rows: one workgroup of eight waves per (16 rows of one request that
+// share a kv head, split of its keys).  Bound by reading the cache: each wave
+// takes every eighth tile of TK keys straight from HBM into registers in the
+// order of the matrix operands (16-byte loads, whole 64-byte sectors), with
+// the next tile's keys and values on their way while it works on this one.
+// The waves' sums are joined in the LDS.
 //
-// Lanes: with c = lane % 16 and g = lane / 16, a lane holds row c and the keys
-// 16 g .. 16 g + 15 of the tile, which lie in one page: one page number and
-// one pair of scales per lane.  For that, row i of the a-th K operand is key
-// 16 (i / 4) + 4 a + i % 4.
+// Lanes: with c = lane % 16 and g = lane / 16, a lane holds row c and the NK =
+// TK / 4 keys from NK g on, which lie in one page: one page number and one pair
+// of scales per lane.  For that, row i of the t-th K operand is key NK (i / 4) +
+// 4 t + i % 4.
+// TK is 64; at D = 256, 32, so that two tiles and the sums fit a lane's 256
+// registers (with 64 keys and no tile ahead a decode step of 32 requests took
+// 25.0 us).
 // ---------------------------------------------------------------------------
-template <int D, int W, Take TAKE>
-__global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionArgs a, Division v) {
+constexpr int kFewWaves = 8;
+constexpr int few_keys(int d) { return d == 256 ? 32 : 64; }
+
+template <int D, Take TAKE>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(AttentionArgs a, Division v) {
+    constexpr int W = kFewWaves, TK = few_keys(D), NK = TK / 4, NT = TK / 16, NV = TK / 16;
     constexpr int KS = D >= 128 ? D / 128 : 1;       // contraction steps of 128
     constexpr int KL = D / 64;                       // 16-byte loads per key operand
     constexpr int DT = D / 16;                       // operands of 16 value elements
@@ -187,8 +233,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
     if constexpr (TAKE == Take::kSmall) {
         s = (int)(tile / (kSmallRows / kTileRows));
         within = (int)(tile % (kSmallRows / kTileRows));
+    } else if (tile < a.num_seqs) {
+        s = (int)tile;                               // every request's first tile: no search
+        within = 0;
     } else {
-        s = find_request(a, tile, G, kTileRows, within);
+        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, within);
+        ++within;
     }
     const Request rq = request_of(a, s);
     const long long row0 = (long long)within * kTileRows, n_rows = (long long)rq.n * G;
@@ -271,40 +321,55 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
     };
     auto good = [&](int p) { return (unsigned)p < (unsigned)a.num_pages; };
 
-    uint4 kr[4][KL], vr[DT];
+    uint4 kr[NT][KL];
+    uint32_t vr[DT][NV];
     float ks = 0.f, vs = 0.f;
     auto load_k = [&](int j0, int page) {
-        const int j = j0 + 16 * kg;
+        const int j = j0 + NK * kg;
         const uint8_t *p = a.k_cache + (((long long)(good(page) ? page : 0) * a.num_kv_heads + hk) * a.page + (j & in_page) + (c & 3)) * D + 16 * g;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int l = 0; l < KL; ++l) kr[t][l] = *reinterpret_cast<const uint4 *>(p + 4 * t * D + 64 * l);
     };
     auto load_v = [&](int j0, int page) {
-        const int j = j0 + 16 * g;
+        const int j = j0 + NK * g;
         const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
         const uint8_t *p = a.v_cache + (ph * D + c) * a.page + (j & in_page);
 #pragma unroll
-        for (int t = 0; t < DT; ++t) vr[t] = *reinterpret_cast<const uint4 *>(p + (long long)16 * t * a.page);
+        for (int t = 0; t < DT; ++t) {
+            if constexpr (NV == 4) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(p + (long long)16 * t * a.page);
+                vr[t][0] = w.x;
+                vr[t][1] = w.y;
+                vr[t][2] = w.z;
+                vr[t][3] = w.w;
+            } else {
+                const uint2 w = *reinterpret_cast<const uint2 *>(p + (long long)16 * t * a.page);
+                vr[t][0] = w.x;
+                vr[t][1] = w.y;
+            }
+        }
         ks = a.k_scale[ph];
         vs = a.v_scale[ph];
     };
 
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
-    const int step = W * kTileKeys;
-    int j0 = (k_lo & ~(kTileKeys - 1)) + wave * kTileKeys;
-    int pk = page_at(j0 + 16 * kg), pv = page_at(j0 + 16 * g);
+    uint32_t met_nan = 0;
+    constexpr int step = W * TK;
+    int j0 = (k_lo & ~(TK - 1)) + wave * TK;
+    int pk = page_at(j0 + NK * kg), pv = page_at(j0 + NK * g);
     if (j0 < k_hi) {
         load_k(j0, pk);
         load_v(j0, pv);
     }
     for (; j0 < k_hi; j0 += step) {
         const int jn = j0 + step;
-        const int pk_n = page_at(jn + 16 * kg), pv_n = page_at(jn + 16 * g);
-        // X^T: keys 16 g + 4 t + r of row c
-        f32x4 x[4] = {};
+        pk = page_at(jn + NK * kg);
+        const int pv_n = page_at(jn + NK * g);
+        // X^T: keys NK g + 4 t + r of row c
+        f32x4 x[NT] = {};
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
             i32x8 hi8 = qh[st], lo8 = ql[st];
@@ -315,7 +380,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
                 lo8 = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
+            for (int t = 0; t < NT; ++t) {
                 const uint4 u = kr[t][D == 64 ? 0 : 2 * st], w = kr[t][D == 64 ? 0 : 2 * st + 1];
                 const i32x8 k8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
                 x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, hi8, x[t], 0, 0, 0, 0, 0, 0);
@@ -323,25 +388,30 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
                     x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, lo8, x[t], 0, 0, 0, 0, 0, 0);
             }
         }
-        if (jn < k_hi) load_k(jn, pk_n);
+        if (jn < k_hi) load_k(jn, pk);
         asm volatile("" ::: "memory");
 
         const float factor = to_log2 * ks;
-        const int jg = j0 + 16 * g;
+        const int jg = j0 + NK * g;
         const bool seen_page = good(pv);
-        const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + kTileKeys > min(x1, k_hi);
+        const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + TK > min(x1, k_hi);
         float mx = kNegInf;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[t][r] *= factor;
-                if (masked) {
+            for (int r = 0; r < 4; ++r) x[t][r] *= factor;
+        if (masked)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
                     const int j = jg + 4 * t + r;
                     if (!(seen_page && j >= jb && j < je)) x[t][r] = kNegInf;
                 }
-                mx = fmaxf(mx, x[t][r]);
-            }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
         mx = max_over(max_over(mx, 16), 32);
         if (__any(mx > m)) {
             const float m_new = fmaxf(m, mx);
@@ -352,92 +422,55 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
             for (int t = 0; t < DT; ++t) o[t] *= f;
         }
         const float at = m == kNegInf ? 0.f : m;
-        bf16x8 p[2];
-        {
-            uint32_t pw[8];
+        uint32_t pw[2 * NT];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float e[4];
+        for (int t = 0; t < NT; ++t) {
+            float e[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
-                    l += e[r];
-                    // a masked key's scale may be anything
-                    e[r] = masked && x[t][r] == kNegInf ? 0.f : e[r] * vs;
-                }
-                pw[2 * t] = pack_bf16x2(e[0], e[1]);
-                pw[2 * t + 1] = pack_bf16x2(e[2], e[3]);
+            for (int r = 0; r < 4; ++r) {
+                e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
+                l += e[r];
+                // a masked key's scale may be anything
+                e[r] = masked && x[t][r] == kNegInf ? 0.f : e[r] * vs;
             }
-            const i32x4 u = {(int)pw[0], (int)pw[1], (int)pw[2], (int)pw[3]}, w = {(int)pw[4], (int)pw[5], (int)pw[6], (int)pw[7]};
-            p[0] = __builtin_bit_cast(bf16x8, u);
-            p[1] = __builtin_bit_cast(bf16x8, w);
+            pw[2 * t] = pack_bf16x2(e[0], e[1]);
+            pw[2 * t + 1] = pack_bf16x2(e[2], e[3]);
         }
         if (masked) {
-            // Values that no row sees may be anything: zero.  NaN among those
-            // that some rows see must reach those rows only: its codes are
-            // zeroed too, and rows that see it get their NaN from a count.
-            uint32_t keep[4], any_nan = 0;
+            // values that no row sees may be anything: zero; NaN: find_nan
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                keep[w] = 0;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int j = jg + 4 * w + b;
-                    if (seen_page && j >= max(lo, k_lo) && j < k_hi) keep[w] |= 0xffu << (8 * b);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                vr[t].x &= keep[0];
-                vr[t].y &= keep[1];
-                vr[t].z &= keep[2];
-                vr[t].w &= keep[3];
-                any_nan |= nan_codes(vr[t].x) | nan_codes(vr[t].y) | nan_codes(vr[t].z) | nan_codes(vr[t].w);
-            }
-            if (__any(any_nan != 0)) {
-                bf16x8 sees[2];
-                uint32_t pw[8];
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; r += 2) {
-                        const int j = jg + 4 * t + r;
-                        pw[2 * t + r / 2] = (j >= jb && j < je ? 0x3f80u : 0u) | (j + 1 >= jb && j + 1 < je ? 0x3f800000u : 0u);
-                    }
-                const i32x4 u = {(int)pw[0], (int)pw[1], (int)pw[2], (int)pw[3]}, w = {(int)pw[4], (int)pw[5], (int)pw[6], (int)pw[7]};
-                sees[0] = __builtin_bit_cast(bf16x8, u);
-                sees[1] = __builtin_bit_cast(bf16x8, w);
+            for (int w = 0; w < NV; ++w) {
+                const uint32_t keep = seen_page ? key_bytes(jg + 4 * w, max(lo, k_lo), k_hi) : 0u;
 #pragma unroll
                 for (int t = 0; t < DT; ++t) {
-                    uint32_t d[4] = {vr[t].x, vr[t].y, vr[t].z, vr[t].w}, ones[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bad = nan_codes(d[i]) >> 7;       // 1 per NaN byte
-                        d[i] &= ~(bad * 0xffu);
-                        ones[i] = bad * 0x38u;                           // e4m3 1.0
-                    }
-                    vr[t] = make_uint4(d[0], d[1], d[2], d[3]);
-                    bf16x8 lo8, hi8;
-                    codes_to_bf16(make_uint4(ones[0], ones[1], ones[2], ones[3]), lo8, hi8);
-                    f32x4 count = {0.f, 0.f, 0.f, 0.f};
-                    count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo8, sees[0], count, 0, 0, 0);
-                    count = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi8, sees[1], count, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (count[r] > 0.f) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
+                    vr[t][w] &= keep;
+                    met_nan |= take_nan(vr[t][w]);
                 }
             }
         }
 #pragma unroll
-        for (int t = 0; t < DT; ++t) {
-            bf16x8 lo8, hi8;
-            codes_to_bf16(vr[t], lo8, hi8);
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo8, p[0], o[t], 0, 0, 0);
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi8, p[1], o[t], 0, 0, 0);
+        for (int u = 0; u < NV / 2; ++u) {
+            const bf16x8 p = as_bf16x8(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]);
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vr[t][2 * u], vr[t][2 * u + 1]), p, o[t], 0, 0, 0);
         }
         if (jn < k_hi) load_v(jn, pv_n);
         asm volatile("" ::: "memory");
         pv = pv_n;
+    }
+
+    if (__any(met_nan != 0)) {
+        unsigned long long bits[1] = {0};
+        find_nan<4 * DT>(
+            a, hk, (k_lo & ~(TK - 1)) + wave * TK, k_hi, step, TK, jb, je, bits,
+            [&](int j) { return __any(!good(page_at(j + NK * g))) || j < max(x0, k_lo) || j + TK > min(x1, k_hi); },
+            [&](int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }, page_at);
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (bits[0] >> (4 * t + r) & 1) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
     }
 
     // join the waves: maxima, then each wave's sums at the common maximum
@@ -502,6 +535,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void attention_few_kernel(AttentionA
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 128, kManyThreads = 256;
 
+// 16 bytes per lane from `src` to 64 consecutive places of the LDS, of which
+// `dst` is the wave's first
+__device__ __forceinline__ void to_lds(const uint8_t *src, uint4 *dst) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
 template <int D>
 struct ManyLds {
     uint4 k[2][kTileKeys * D / 16], v[2][kTileKeys * D / 16];
@@ -533,7 +573,7 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
     const long long tile = units / a.num_kv_heads - 1 - unit / a.num_kv_heads;
     const int hk = (int)(unit % a.num_kv_heads);
     int within;
-    const int s = find_request(a, tile, G, kManyRows, within);
+    const int s = find_request(a, tile, G, kManyRows, 1, within);
     const Request rq = request_of(a, s);
     const long long row0 = (long long)within * kManyRows, n_rows = (long long)rq.n * G;
     if (within < 0 || row0 >= n_rows || n_rows <= kSmallRows) return;
@@ -599,7 +639,9 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
             }
     }
 
-    // staging: a thread's 16-byte pieces of a tile
+    // staging: the tile's pieces go from memory to the LDS without registers
+    // between.  A wave's load fills 64 consecutive places; a lane's place says
+    // which piece it fetches.
     const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
     const int32_t *bt = a.block_table + s * a.block_table_stride;
     auto page_at = [&](int j) {
@@ -608,96 +650,75 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
         return (unsigned)id < (unsigned)a.num_pages ? id : -1;
     };
     constexpr int PPK = D / 16, KEYS = kManyThreads / PPK;      // pieces per key; keys per load
-    const int k_key = tid / PPK, k_p = tid % PPK, v_g = tid & 3, v_d = tid >> 2;
-    uint4 kr[NL], vr[NL];
+    const int k_key = tid / PPK, v_d = tid >> 2, v_g = (tid & 3) ^ (v_d >> 2 & 3);
+    int idk[NL], idv, ids, s_ok = 0;
     float s_ks = 0.f, s_vs = 0.f;
-    int idk[NL], idv;
     auto load_ids = [&](int j0) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + i * KEYS + k_key);
         idv = page_at(j0 + 16 * v_g);
+        ids = page_at(j0 + 16 * (tid & 3));
     };
-    int ok_next = 0;
-    auto load_tile = [&](int j0) {
+    auto load_tile = [&](int j0, int buf) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int j = j0 + i * KEYS + k_key;
-            kr[i] = *reinterpret_cast<const uint4 *>(
-                a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + (j & in_page)) * D + 16 * k_p);
+            const int key = i * KEYS + k_key, p = k_piece<D>(key, tid % PPK) - key * PPK;
+            to_lds(a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + ((j0 + key) & in_page)) * D + 16 * p,
+                   &lds.k[buf][i * kManyThreads + 64 * wave]);
         }
-        const int jv = j0 + 16 * v_g;
-        const long long ph = (long long)max(idv, 0) * a.num_kv_heads + hk;
-        const uint8_t *p = a.v_cache + (ph * D + v_d) * a.page + (jv & in_page);
+        const uint8_t *p = a.v_cache + (((long long)max(idv, 0) * a.num_kv_heads + hk) * D + v_d) * a.page +
+                           ((j0 + 16 * v_g) & in_page);
 #pragma unroll
-        for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const uint4 *>(p + (long long)64 * i * a.page);
+        for (int i = 0; i < NL; ++i) to_lds(p + (long long)64 * i * a.page, &lds.v[buf][i * kManyThreads + 64 * wave]);
         if (tid < 4) {
+            const long long ph = (long long)max(ids, 0) * a.num_kv_heads + hk;
             s_ks = a.k_scale[ph];
             s_vs = a.v_scale[ph];
-        }
-        ok_next = idv >= 0;
-    };
-    auto put_tile = [&](int j0, int buf) {
-        // values that no row of the workgroup sees may be anything: zero
-        if (j0 < k_lo || j0 + kTileKeys > k_hi || !ok_next) {
-            uint32_t keep[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                keep[w] = 0;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int j = j0 + 16 * v_g + 4 * w + b;
-                    if (ok_next && j >= k_lo && j < k_hi) keep[w] |= 0xffu << (8 * b);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NL; ++i) {
-                vr[i].x &= keep[0];
-                vr[i].y &= keep[1];
-                vr[i].z &= keep[2];
-                vr[i].w &= keep[3];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            lds.k[buf][k_piece<D>(i * KEYS + k_key, k_p)] = kr[i];
-            lds.v[buf][v_piece(64 * i + v_d, v_g)] = vr[i];
-        }
-        if (tid < 4) {
-            lds.ks[buf][tid] = s_ks;
-            lds.vs[buf][tid] = s_vs;
-            lds.ok[buf][tid] = ok_next;
+            s_ok = ids >= 0;
         }
     };
 
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
+    uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
     if (j0 < k_hi) {
         load_ids(j0);
-        load_tile(j0);
+        load_tile(j0, 0);
         load_ids(j0 + kTileKeys);
-        put_tile(j0, 0);
     }
-    __syncthreads();
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
+        // this tile has arrived, for all waves, and the other buffer is free
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (tid < 4) {
+            lds.ks[buf][tid] = s_ks;
+            lds.vs[buf][tid] = s_vs;
+            lds.ok[buf][tid] = s_ok;
+        }
+        __syncthreads();
         if (jn < k_hi) {
-            load_tile(jn);
+            load_tile(jn, buf ^ 1);
             load_ids(jn + kTileKeys);
         }
         if (j0 < w_hi && j0 + kTileKeys > w_lo) {
             f32x16 x[2] = {};
+            // (operands are read one step ahead of their products; left alone the
+            // compiler reads many steps ahead and runs out of registers)
+            auto k_operand = [&](int i) {
+                const int t = i / KS, st = i % KS, key = 32 * (c >> 2 & 1) + 16 * t + 4 * (c >> 3) + (c & 3);
+                const uint4 u = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2)];
+                const uint4 w = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2 + 1)];
+                return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
+            };
+            i32x8 k8 = k_operand(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int key = 32 * (c >> 2 & 1) + 16 * t + 4 * (c >> 3) + (c & 3);
-#pragma unroll
-                for (int st = 0; st < KS; ++st) {
-                    const uint4 u = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2)];
-                    const uint4 w = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2 + 1)];
-                    const i32x8 k8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
-                    x[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[st], x[t], 0, 0, 0, 0, 0, 0);
-                    x[t] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x[t], 0, 0, 0, 0, 0, 0);
-                }
+            for (int i = 0; i < 2 * KS; ++i) {
+                const i32x8 next = k_operand(min(i + 1, 2 * KS - 1));
+                asm volatile("" ::: "memory");
+                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+                k8 = next;
             }
             const int ok0 = lds.ok[buf][2 * h2], ok1 = lds.ok[buf][2 * h2 + 1];
             const bool masked = j0 < w_all0 || jn > w_all1 || __any(!(ok0 && ok1));
@@ -747,70 +768,55 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
                     }
                     pw[r / 2] = pack_bf16x2(e0, e1);
                 }
-                const i32x4 u = {(int)pw[0], (int)pw[1], (int)pw[2], (int)pw[3]};
-                const i32x4 w = {(int)pw[4], (int)pw[5], (int)pw[6], (int)pw[7]};
-                p[2 * t] = __builtin_bit_cast(bf16x8, u);
-                p[2 * t + 1] = __builtin_bit_cast(bf16x8, w);
+                p[2 * t] = as_bf16x8(pw[0], pw[1], pw[2], pw[3]);
+                p[2 * t + 1] = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
             }
-            // NaN among the values that some rows see must reach those only
-            bool bad = false;
-            if (masked) {
-                uint32_t any = 0;
+            // values that no row of the wave sees may be anything: zero; NaN: find_nan
+            uint32_t keep[2][4];
+            if (masked)
 #pragma unroll
-                for (int t = 0; t < DT; ++t)
+                for (int g = 0; g < 2; ++g)
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const uint4 w = lds.v[buf][v_piece(32 * t + c, 2 * h2 + g)];
-                        any |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
-                    }
-                bad = __any(any != 0);
-            }
+                    for (int w = 0; w < 4; ++w)
+                        keep[g][w] = (g ? ok1 : ok0) ? key_bytes(j0 + 32 * h2 + 16 * g + 4 * w, w_lo, w_hi) : 0u;
+            uint4 vw = lds.v[buf][v_piece(c, 2 * h2)];
 #pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint4 w = lds.v[buf][v_piece(32 * t + c, 2 * h2 + g)];
-                    if (bad) {
-                        // zeroed here; the rows that see them get theirs from a count
-                        uint32_t d[4] = {w.x, w.y, w.z, w.w}, ones[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t b = nan_codes(d[i]) >> 7;
-                            d[i] &= ~(b * 0xffu);
-                            ones[i] = b * 0x38u;                     // e4m3 1.0
-                        }
-                        w = make_uint4(d[0], d[1], d[2], d[3]);
-                        bf16x8 n0, n1;
-                        codes_to_bf16(make_uint4(ones[0], ones[1], ones[2], ones[3]), n0, n1);
-                        uint32_t see[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int j = j0 + 32 * h2 + 16 * g + 2 * i;
-                            see[i] = (j >= jb && j < je ? 0x3f80u : 0u) | (j + 1 >= jb && j + 1 < je ? 0x3f800000u : 0u);
-                        }
-                        const i32x4 s0 = {(int)see[0], (int)see[1], (int)see[2], (int)see[3]};
-                        const i32x4 s1 = {(int)see[4], (int)see[5], (int)see[6], (int)see[7]};
-                        f32x16 count = {};
-                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n0, __builtin_bit_cast(bf16x8, s0), count, 0, 0, 0);
-                        count = __builtin_amdgcn_mfma_f32_32x32x16_bf16(n1, __builtin_bit_cast(bf16x8, s1), count, 0, 0, 0);
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (count[r] > 0.f) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
-                    }
-                    bf16x8 v0, v1;
-                    codes_to_bf16(w, v0, v1);
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, p[2 * g], o[t], 0, 0, 0);
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, p[2 * g + 1], o[t], 0, 0, 0);
+            for (int i = 0; i < 2 * DT; ++i) {
+                const int t = i / 2, g = i % 2, n = min(i + 1, 2 * DT - 1);
+                const uint4 next = lds.v[buf][v_piece(32 * (n / 2) + c, 2 * h2 + n % 2)];
+                asm volatile("" ::: "memory");
+                if (masked) {
+                    vw.x &= keep[g][0];
+                    vw.y &= keep[g][1];
+                    vw.z &= keep[g][2];
+                    vw.w &= keep[g][3];
+                    met_nan |= take_nan(vw.x) | take_nan(vw.y) | take_nan(vw.z) | take_nan(vw.w);
                 }
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.x, vw.y), p[2 * g], o[t], 0, 0, 0);
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.z, vw.w), p[2 * g + 1], o[t], 0, 0, 0);
+                vw = next;
+            }
         }
-        if (jn < k_hi) put_tile(jn, buf ^ 1);
-        __syncthreads();
     }
 
     l += __shfl_xor(l, 32, 64);
-    if (!live) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
+    if (__any(met_nan != 0)) {
+        unsigned long long bits[(16 * DT + 63) / 64] = {};
+        find_nan<16 * DT>(
+            a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
+            [&](int j) {
+                return j < w_all0 || j + kTileKeys > w_all1 || __any(page_at(j + 32 * h2) < 0 || page_at(j + 32 * h2 + 16) < 0);
+            },
+            [&](int i) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * h2 + (i & 3); }, page_at);
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (bits[t / 4] >> (16 * (t & 3) + r) & 1) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
+    }
+    if (!live) return;
     // element 32 t + 8 q + 4 h2 + r of row c is o[t][4 q + r]
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -903,11 +909,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // few-rows kernel takes everything; else it takes the requests of up to
 // kSmallRows rows, and the many-rows kernel the others (16 rows of a wave cost
 // it as much as 32, and it reads a key once for 128 rows).  Keys are split
-// until there is a workgroup for every CU, each with at least kMinChunk keys.
+// until there is a workgroup for every CU, each with at least kMinChunk keys
+// (joining costs a launch: 32 decode rows of 1,100 keys take 23.0 us in one part
+// and 23.8 in two; five of 40,000 to 131,000 take 206 us in parts for 240 CUs and
+// 321 for 120).
 // ---------------------------------------------------------------------------
-constexpr int few_waves(int d) { return d == 256 ? 4 : 8; }
 constexpr int kCUs = 256;
-constexpr int kMinChunk = 8 * kTileKeys;
+constexpr int kMinChunk = 1024;
 
 struct Launch {
     long long units;        // (row tile, kv head) pairs, upper bound; 0: none
@@ -921,7 +929,7 @@ static Launch divide(long long tiles, long long busy, long long rows, int kv_hea
     Launch p{tiles * kv_heads, rows, 0x40000000, 1, 0};
     busy *= kv_heads;
     long long want = busy > 0 ? kCUs / busy : 1;
-    const long long most = (max_seq_len + (long long)kMinChunk - 1) / kMinChunk;
+    const long long most = max_seq_len / kMinChunk;
     if (want > most) want = most;
     if (want > 1) {
         const long long chunk = ((max_seq_len + want - 1) / want + kTileKeys - 1) / kTileKeys * kTileKeys;
@@ -965,8 +973,7 @@ static hipError_t launch_few(const AttentionArgs &a, const Launch &p, float *ws,
     const long long blocks = p.units * p.splits;
     if (blocks > 0x7fffffffLL || p.rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     const Division v{p.chunk, p.splits, ws, ws + p.rows * p.splits * D};
-    hipLaunchKernelGGL((attention_few_kernel<D, few_waves(D), TAKE>), dim3((unsigned)blocks), dim3(64 * few_waves(D)), 0,
-                       stream, a, v);
+    hipLaunchKernelGGL((attention_few_kernel<D, TAKE>), dim3((unsigned)blocks), dim3(64 * kFewWaves), 0, stream, a, v);
     if (p.splits > 1)
         hipLaunchKernelGGL((attention_join_kernel<D, TAKE>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, a, v,
                            p.rows, kTileRows);
