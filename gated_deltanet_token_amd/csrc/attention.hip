@@ -124,6 +124,110 @@ __device__ __forceinline__ Splits splits_of(int lo, int hi, int chunk, int n) {
     return s;
 }
 
+// The largest finite magnitude m of a row of q, brought to [128, 256): the
+// power of two for it, within [2^-120, 2^126].
+__device__ __forceinline__ float split_factor(float m) {
+    const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
+    return __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
+}
+// four elements' two parts
+__device__ __forceinline__ void split4(const float *f, float up, int &hi, int &lo) {
+    float v[4], b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = f[e] * up;           // infinities and NaN: NaN codes
+    const uint32_t w = e4m3x4(v[0], v[1], v[2], v[3]);
+    e4m3_values(w, b);
+    hi = (int)w;
+    lo = (int)e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
+}
+
+// One row's parts for lanes of 16 rows, in the order of the key operands: bytes
+// 16 m + e of step s are elements 128 s + 64 m + 16 g + e (for D = 64 the upper
+// 16 bytes are lo).  Returns what the products are to be multiplied by.
+template <int D>
+__device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
+                                           i32x8 (&ql)[D >= 128 ? D / 128 : 1]) {
+    constexpr int KL = D / 64;
+    float f[KL][16], m = 0.f;
+#pragma unroll
+    for (int l = 0; l < KL; ++l) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float t[8];
+            unpack8(*reinterpret_cast<const uint4 *>(q + 64 * l + 16 * g + 8 * b), t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[l][8 * b + e] = t[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = is_finite(f[l][e]) ? fmaxf(m, fabsf(f[l][e])) : m;
+    }
+    m = max_over(max_over(m, 16), 32);
+    const float up = split_factor(m);
+#pragma unroll
+    for (int l = 0; l < KL; ++l)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            int hw, lw;
+            split4(&f[l][4 * w], up, hw, lw);
+            if constexpr (D == 64) {
+                qh[0][w] = hw;
+                qh[0][4 + w] = lw;
+            } else {
+                qh[l / 2][4 * (l & 1) + w] = hw;
+                ql[l / 2][4 * (l & 1) + w] = lw;
+            }
+        }
+    return 1.f / up;
+}
+
+// One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
+// row) become weights, packed to bf16 pairs with the values' scale in them;
+// the running maximum m, the lane's sum l and the sums o follow.
+template <int NT, int DT>
+__device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool masked, bool seen_page, int jg, int jb, int je,
+                                      float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
+    float mx = kNegInf;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[t][r] *= factor;
+    if (masked)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = jg + 4 * t + r;
+                if (!(seen_page && j >= jb && j < je)) x[t][r] = kNegInf;
+            }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
+    mx = max_over(max_over(mx, 16), 32);
+    if (__any(mx > m)) {
+        const float m_new = fmaxf(m, mx);
+        const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+        m = m_new;
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) o[t] *= f;
+    }
+    const float at = m == kNegInf ? 0.f : m;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float e[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
+            l += e[r];
+            // a masked key's scale may be anything
+            e[r] = masked && x[t][r] == kNegInf ? 0.f : e[r] * vs;
+        }
+        pw[2 * t] = pack_bf16x2(e[0], e[1]);
+        pw[2 * t + 1] = pack_bf16x2(e[2], e[3]);
+    }
+}
+
 // A tile that some of a wave's rows see and others do not cannot pass NaN codes
 // of its values through the matrix cores: they would reach all rows.  They go
 // in as zeros there, and this pass, for a wave that met any, finds the sums
@@ -172,27 +276,10 @@ __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int
                                 : (long long)t * a.num_q_heads + h;
 }
 
-// The largest finite magnitude m of a row of q, brought to [128, 256): the
-// power of two for it, within [2^-120, 2^126].
-__device__ __forceinline__ float split_factor(float m) {
-    const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
-    return __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
-}
-// four elements' two parts
-__device__ __forceinline__ void split4(const float *f, float up, int &hi, int &lo) {
-    float v[4], b[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = f[e] * up;           // infinities and NaN: NaN codes
-    const uint32_t w = e4m3x4(v[0], v[1], v[2], v[3]);
-    e4m3_values(w, b);
-    hi = (int)w;
-    lo = (int)e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
-}
-
 // ---------------------------------------------------------------------------
-// Few rows: one workgroup of eight waves per (16 rows of one request that
+// Few rows: one workgroup of W waves per (16 rows of one request that
 // share a kv head, split of its keys).  Bound by reading the cache: each wave
-// takes every eighth tile of TK keys straight from HBM into registers in the
+// takes every W-th tile of TK keys straight from HBM into registers in the
 // order of the matrix operands (16-byte loads, whole 64-byte sectors), with
 // the next tile's keys and values on their way while it works on this one.
 // The waves' sums are joined in the LDS.
@@ -205,12 +292,11 @@ __device__ __forceinline__ void split4(const float *f, float up, int &hi, int &l
 // registers (with 64 keys and no tile ahead a decode step of 32 requests took
 // 25.0 us).
 // ---------------------------------------------------------------------------
-constexpr int kFewWaves = 8;
 constexpr int few_keys(int d) { return d == 256 ? 32 : 64; }
 
-template <int D, Take TAKE>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(AttentionArgs a, Division v) {
-    constexpr int W = kFewWaves, TK = few_keys(D), NK = TK / 4, NT = TK / 16, NV = TK / 16;
+template <int D, int W, Take TAKE>
+__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block) {
+    constexpr int TK = few_keys(D), NK = TK / 4, NT = TK / 16, NV = TK / 16;
     constexpr int KS = D >= 128 ? D / 128 : 1;       // contraction steps of 128
     constexpr int KL = D / 64;                       // 16-byte loads per key operand
     constexpr int DT = D / 16;                       // operands of 16 value elements
@@ -225,8 +311,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4, kg = c >> 2;
     const int G = a.num_q_heads / a.num_kv_heads;
-    const long long unit = blockIdx.x / v.splits;
-    const int split = blockIdx.x - (int)(unit * v.splits);
+    const long long unit = block / v.splits;
+    const int split = block - (int)(unit * v.splits);
     const long long tile = unit / a.num_kv_heads;
     const int hk = (int)(unit - tile * a.num_kv_heads);
     int within, s;
@@ -261,45 +347,10 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
     jb = max(jb, k_lo);
     je = min(je, k_hi);
 
-    // q's two parts, in the order of the key loads: bytes 16 m + e of step s
-    // are elements 128 s + 64 m + 16 g + e (for D = 64 the upper 16 bytes are lo)
     i32x8 qh[KS], ql[KS];
-    float unscale;
-    {
-        const uint16_t *qp = a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D;
-        float f[KL][16];
-        float m = 0.f;
-#pragma unroll
-        for (int l = 0; l < KL; ++l) {
-            float t[8];
-            unpack8(*reinterpret_cast<const uint4 *>(qp + 64 * l + 16 * g), t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[l][e] = t[e];
-            unpack8(*reinterpret_cast<const uint4 *>(qp + 64 * l + 16 * g + 8), t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[l][8 + e] = t[e];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) m = is_finite(f[l][e]) ? fmaxf(m, fabsf(f[l][e])) : m;
-        }
-        m = max_over(max_over(m, 16), 32);
-        const float up = split_factor(m);
-        unscale = 1.f / up;
-#pragma unroll
-        for (int l = 0; l < KL; ++l)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                int hw, lw;
-                split4(&f[l][4 * w], up, hw, lw);
-                if constexpr (D == 64) {
-                    qh[0][w] = hw;
-                    qh[0][4 + w] = lw;
-                } else {
-                    qh[l / 2][4 * (l & 1) + w] = hw;
-                    ql[l / 2][4 * (l & 1) + w] = lw;
-                }
-            }
-    }
-    const float to_log2 = a.scale * kLog2e * unscale;
+    const float to_log2 =
+        a.scale * kLog2e *
+        split_q16<D>(a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D, g, qh, ql);
     if constexpr (QLDS) {
         if (wave == 0) {
 #pragma unroll
@@ -391,51 +442,11 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
         if (jn < k_hi) load_k(jn, pk);
         asm volatile("" ::: "memory");
 
-        const float factor = to_log2 * ks;
         const int jg = j0 + NK * g;
         const bool seen_page = good(pv);
         const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + TK > min(x1, k_hi);
-        float mx = kNegInf;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[t][r] *= factor;
-        if (masked)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = jg + 4 * t + r;
-                    if (!(seen_page && j >= jb && j < je)) x[t][r] = kNegInf;
-                }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
-        mx = max_over(max_over(mx, 16), 32);
-        if (__any(mx > m)) {
-            const float m_new = fmaxf(m, mx);
-            const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
-            m = m_new;
-            l *= f;
-#pragma unroll
-            for (int t = 0; t < DT; ++t) o[t] *= f;
-        }
-        const float at = m == kNegInf ? 0.f : m;
         uint32_t pw[2 * NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float e[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
-                l += e[r];
-                // a masked key's scale may be anything
-                e[r] = masked && x[t][r] == kNegInf ? 0.f : e[r] * vs;
-            }
-            pw[2 * t] = pack_bf16x2(e[0], e[1]);
-            pw[2 * t + 1] = pack_bf16x2(e[2], e[3]);
-        }
+        weigh(x, to_log2 * ks, vs, masked, seen_page, jg, jb, je, m, l, o, pw);
         if (masked) {
             // values that no row sees may be anything: zero; NaN: find_nan
 #pragma unroll
@@ -533,7 +544,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attention_few_kernel(Attent
 // bits of the row's number) so that 16 lanes that read the same piece of their
 // rows find it in 16 different places of the 256 bytes that the banks span.
 // ---------------------------------------------------------------------------
-constexpr int kManyRows = 128, kManyThreads = 256;
+constexpr int kManyRows = 128;
+constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
 
 // 16 bytes per lane from `src` to 64 consecutive places of the LDS, of which
 // `dst` is the wave's first
@@ -549,6 +561,121 @@ struct ManyLds {
     int ok[2][4];
 };
 
+// A workgroup's share of a many-rows launch.
+struct ManyShare {
+    int s, hk, split;
+    Request rq;
+    long long row0, n_rows;
+    int k_lo, k_hi;        // its keys
+    bool whole;            // no other split has any
+};
+// The last tiles see the most keys and go first; a kv head's workgroups are
+// num_kv_heads apart, so that with eight heads an XCD keeps to one.
+__device__ __forceinline__ bool many_share(const AttentionArgs &a, const Division &v, int block, int blocks, ManyShare &w) {
+    const int G = a.num_q_heads / a.num_kv_heads;
+    const long long units = blocks / v.splits, unit = block / v.splits;
+    w.split = block - (int)(unit * v.splits);
+    const long long tile = units / a.num_kv_heads - 1 - unit / a.num_kv_heads;
+    w.hk = (int)(unit % a.num_kv_heads);
+    int within;
+    w.s = find_request(a, tile, G, kManyRows, 1, within);
+    w.rq = request_of(a, w.s);
+    w.row0 = (long long)within * kManyRows;
+    w.n_rows = (long long)w.rq.n * G;
+    if (within < 0 || w.row0 >= w.n_rows || w.n_rows <= kSmallRows) return false;
+    int lo, hi, x;
+    key_range(a, w.rq, (int)(w.row0 / G), lo, x);
+    key_range(a, w.rq, (int)(min(w.row0 + kManyRows, w.n_rows) - 1) / G, x, hi);
+    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
+    if (w.split != sp.first && (w.split < sp.first || w.split > sp.last)) return false;
+    w.whole = sp.last <= sp.first;
+    w.k_lo = max(lo, w.split * v.chunk);
+    w.k_hi = w.split == v.splits - 1 ? hi : min(hi, (w.split + 1) * v.chunk);
+    return true;
+}
+
+// The keys [lo, hi) of [k_lo, k_hi) that some of `rows` rows from `row` on see,
+// and those [all0, all1) that each of them sees.
+struct WaveKeys {
+    int lo, hi, all0, all1;
+};
+__device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const ManyShare &w, long long row, int rows) {
+    const int G = a.num_q_heads / a.num_kv_heads;
+    WaveKeys k{0, 0, 0, 0};
+    if (row < w.n_rows) {
+        key_range(a, w.rq, (int)(row / G), k.lo, k.all1);
+        key_range(a, w.rq, (int)((min(row + rows, w.n_rows) - 1) / G), k.all0, k.hi);
+        k.lo = max(k.lo, w.k_lo);
+        k.hi = min(k.hi, w.k_hi);
+        k.all0 = max(k.all0, w.k_lo);
+        k.all1 = min(k.all1, w.k_hi);
+    }
+    return k;
+}
+
+// Staging of a workgroup of THREADS threads: a tile's pieces go from memory to
+// the LDS without registers between.  A wave's load fills 64 consecutive
+// places; a lane's place says which piece it fetches (PLACE: the place of a
+// key's piece).
+template <int D, int THREADS, int (*PLACE)(int, int)>
+struct Staging {
+    static constexpr int NL = 64 * D / 16 / THREADS;             // loads of a thread, of keys and of values
+    static constexpr int PPK = D / 16, KEYS = THREADS / PPK;     // pieces per key; keys per load
+    const AttentionArgs &a;
+    ManyLds<D> &lds;
+    const int32_t *bt;
+    int hk, k_hi, shift, wave, k_key, v_d, v_g;
+    int idk[NL], idv, ids, s_ok;
+    float s_ks, s_vs;
+
+    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
+        : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), hk(w.hk), k_hi(w.k_hi),
+          shift(__builtin_ctz(a_.page)), wave(wave_), k_key(threadIdx.x / PPK), v_d(threadIdx.x >> 2),
+          v_g((threadIdx.x & 3) ^ (v_d >> 2 & 3)), s_ok(0), s_ks(0.f), s_vs(0.f) {}
+    // the page of key j, -1: none
+    __device__ __forceinline__ int page_at(int j) const {
+        const int p = j >> shift;
+        const int id = j < k_hi && p < a.max_pages ? bt[p] : -1;
+        return (unsigned)id < (unsigned)a.num_pages ? id : -1;
+    }
+    __device__ __forceinline__ void pages(int j0) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + i * KEYS + k_key);
+        idv = page_at(j0 + 16 * v_g);
+        ids = page_at(j0 + 16 * (threadIdx.x & 3));
+    }
+    __device__ __forceinline__ void load(int j0, int buf) {
+        const int tid = threadIdx.x, in_page = a.page - 1;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int key = i * KEYS + k_key, p = PLACE(key, tid % PPK) - key * PPK;
+            to_lds(a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + ((j0 + key) & in_page)) * D + 16 * p,
+                   &lds.k[buf][i * THREADS + 64 * wave]);
+        }
+        const uint8_t *p = a.v_cache + (((long long)max(idv, 0) * a.num_kv_heads + hk) * D + v_d) * a.page +
+                           ((j0 + 16 * v_g) & in_page);
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            to_lds(p + (long long)(THREADS / 4) * i * a.page, &lds.v[buf][i * THREADS + 64 * wave]);
+        if (tid < 4) {
+            const long long ph = (long long)max(ids, 0) * a.num_kv_heads + hk;
+            s_ks = a.k_scale[ph];
+            s_vs = a.v_scale[ph];
+            s_ok = ids >= 0;
+        }
+    }
+    // the tile has arrived, for all waves, and the other buffer is free
+    __device__ __forceinline__ void arrive(int buf) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (threadIdx.x < 4) {
+            lds.ks[buf][threadIdx.x] = s_ks;
+            lds.vs[buf][threadIdx.x] = s_vs;
+            lds.ok[buf][threadIdx.x] = s_ok;
+        }
+        __syncthreads();
+    }
+};
+
 template <int D>
 __device__ __forceinline__ int k_piece(int key, int p) {
     constexpr int shift = D == 256 ? 0 : D == 128 ? 1 : 2;
@@ -557,53 +684,28 @@ __device__ __forceinline__ int k_piece(int key, int p) {
 __device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (d >> 2 & 3)); }
 
 template <int D>
-__global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many_kernel(AttentionArgs a, Division v) {
+__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks) {
     constexpr int KS = D / 64;                       // contraction steps of 64
     constexpr int DT = D / 32;                       // operands of 32 value elements
-    constexpr int NL = D / 64;                       // 16-byte loads of a thread, of keys and of values
     __shared__ ManyLds<D> lds;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, h2 = lane >> 5;
     const int G = a.num_q_heads / a.num_kv_heads;
-    // the last tiles see the most keys and go first; a kv head's workgroups are
-    // num_kv_heads apart, so that with eight heads an XCD keeps to one
-    const long long units = gridDim.x / v.splits, unit = blockIdx.x / v.splits;
-    const int split = blockIdx.x - (int)(unit * v.splits);
-    const long long tile = units / a.num_kv_heads - 1 - unit / a.num_kv_heads;
-    const int hk = (int)(unit % a.num_kv_heads);
-    int within;
-    const int s = find_request(a, tile, G, kManyRows, 1, within);
-    const Request rq = request_of(a, s);
-    const long long row0 = (long long)within * kManyRows, n_rows = (long long)rq.n * G;
-    if (within < 0 || row0 >= n_rows || n_rows <= kSmallRows) return;
-    int lo, hi, x0, x1;
-    key_range(a, rq, (int)(row0 / G), lo, x1);
-    key_range(a, rq, (int)(min(row0 + kManyRows, n_rows) - 1) / G, x0, hi);
-    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
-    if (split != sp.first && (split < sp.first || split > sp.last)) return;
-    const bool whole = sp.last <= sp.first;
-    const int k_lo = max(lo, split * v.chunk);
-    const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
+    ManyShare w;
+    if (!many_share(a, v, block, blocks, w)) return;
+    const Request &rq = w.rq;
+    const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
 
     // this wave's rows
-    const long long wrow = row0 + 32 * wave, row = wrow + c;
-    const bool live = row < n_rows;
+    const long long wrow = w.row0 + 32 * wave, row = wrow + c;
+    const bool live = row < w.n_rows;
     const int i_row = live ? (int)(row / G) : 0, h = hk * G + (live ? (int)(row - (long long)i_row * G) : 0);
     int jb = 0, je = 0;
     if (live) key_range(a, rq, i_row, jb, je);
     jb = max(jb, k_lo);
     je = min(je, k_hi);
-    // keys that some row of the wave sees [w_lo, w_hi), that all do [w_all0, w_all1)
-    int w_lo = 0, w_hi = 0, w_all0 = 0, w_all1 = 0;
-    if (wrow < n_rows) {
-        key_range(a, rq, (int)(wrow / G), w_lo, w_all1);
-        key_range(a, rq, (int)((min(wrow + 32, n_rows) - 1) / G), w_all0, w_hi);
-        w_lo = max(w_lo, k_lo);
-        w_hi = min(w_hi, k_hi);
-        w_all0 = max(w_all0, k_lo);
-        w_all1 = min(w_all1, k_hi);
-    }
+    const WaveKeys wk = wave_keys(a, w, wrow, 32);
 
     // q's two parts: bytes 16 m + e of step st are elements 64 st + 32 h2 + 16 m + e
     i32x8 qh[KS], ql[KS];
@@ -639,69 +741,24 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
             }
     }
 
-    // staging: the tile's pieces go from memory to the LDS without registers
-    // between.  A wave's load fills 64 consecutive places; a lane's place says
-    // which piece it fetches.
-    const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
-    const int32_t *bt = a.block_table + s * a.block_table_stride;
-    auto page_at = [&](int j) {
-        const int p = j >> shift;
-        const int id = j < k_hi && p < a.max_pages ? bt[p] : -1;
-        return (unsigned)id < (unsigned)a.num_pages ? id : -1;
-    };
-    constexpr int PPK = D / 16, KEYS = kManyThreads / PPK;      // pieces per key; keys per load
-    const int k_key = tid / PPK, v_d = tid >> 2, v_g = (tid & 3) ^ (v_d >> 2 & 3);
-    int idk[NL], idv, ids, s_ok = 0;
-    float s_ks = 0.f, s_vs = 0.f;
-    auto load_ids = [&](int j0) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + i * KEYS + k_key);
-        idv = page_at(j0 + 16 * v_g);
-        ids = page_at(j0 + 16 * (tid & 3));
-    };
-    auto load_tile = [&](int j0, int buf) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int key = i * KEYS + k_key, p = k_piece<D>(key, tid % PPK) - key * PPK;
-            to_lds(a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + ((j0 + key) & in_page)) * D + 16 * p,
-                   &lds.k[buf][i * kManyThreads + 64 * wave]);
-        }
-        const uint8_t *p = a.v_cache + (((long long)max(idv, 0) * a.num_kv_heads + hk) * D + v_d) * a.page +
-                           ((j0 + 16 * v_g) & in_page);
-#pragma unroll
-        for (int i = 0; i < NL; ++i) to_lds(p + (long long)64 * i * a.page, &lds.v[buf][i * kManyThreads + 64 * wave]);
-        if (tid < 4) {
-            const long long ph = (long long)max(ids, 0) * a.num_kv_heads + hk;
-            s_ks = a.k_scale[ph];
-            s_vs = a.v_scale[ph];
-            s_ok = ids >= 0;
-        }
-    };
-
+    Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w, wave);
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
     uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
     if (j0 < k_hi) {
-        load_ids(j0);
-        load_tile(j0, 0);
-        load_ids(j0 + kTileKeys);
+        stage.pages(j0);
+        stage.load(j0, 0);
+        stage.pages(j0 + kTileKeys);
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        // this tile has arrived, for all waves, and the other buffer is free
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (tid < 4) {
-            lds.ks[buf][tid] = s_ks;
-            lds.vs[buf][tid] = s_vs;
-            lds.ok[buf][tid] = s_ok;
-        }
-        __syncthreads();
+        stage.arrive(buf);
         if (jn < k_hi) {
-            load_tile(jn, buf ^ 1);
-            load_ids(jn + kTileKeys);
+            stage.load(jn, buf ^ 1);
+            stage.pages(jn + kTileKeys);
         }
-        if (j0 < w_hi && j0 + kTileKeys > w_lo) {
+        if (j0 < wk.hi && jn > wk.lo) {
             f32x16 x[2] = {};
             // (operands are read one step ahead of their products; left alone the
             // compiler reads many steps ahead and runs out of registers)
@@ -721,7 +778,7 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
                 k8 = next;
             }
             const int ok0 = lds.ok[buf][2 * h2], ok1 = lds.ok[buf][2 * h2 + 1];
-            const bool masked = j0 < w_all0 || jn > w_all1 || __any(!(ok0 && ok1));
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1));
             float mx = kNegInf;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -778,7 +835,7 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
-                        keep[g][w] = (g ? ok1 : ok0) ? key_bytes(j0 + 32 * h2 + 16 * g + 4 * w, w_lo, w_hi) : 0u;
+                        keep[g][w] = (g ? ok1 : ok0) ? key_bytes(j0 + 32 * h2 + 16 * g + 4 * w, wk.lo, wk.hi) : 0u;
             uint4 vw = lds.v[buf][v_piece(c, 2 * h2)];
 #pragma unroll
             for (int i = 0; i < 2 * DT; ++i) {
@@ -807,9 +864,9 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
         find_nan<16 * DT>(
             a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
             [&](int j) {
-                return j < w_all0 || j + kTileKeys > w_all1 || __any(page_at(j + 32 * h2) < 0 || page_at(j + 32 * h2 + 16) < 0);
+                return j < wk.all0 || j + kTileKeys > wk.all1 || __any(stage.page_at(j + 32 * h2) < 0 || stage.page_at(j + 32 * h2 + 16) < 0);
             },
-            [&](int i) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * h2 + (i & 3); }, page_at);
+            [&](int i) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * h2 + (i & 3); }, [&](int j) { return stage.page_at(j); });
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -823,21 +880,181 @@ __global__ __launch_bounds__(kManyThreads, D == 256 ? 1 : 2) void attention_many
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int d = 32 * t + 8 * q + 4 * h2;
-            if (whole) {
-                uint2 w;
-                w.x = pack_bf16x2(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
-                w.y = pack_bf16x2(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
-                *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = w;
+            if (w.whole) {
+                uint2 b;
+                b.x = pack_bf16x2(o[t][4 * q] * inv, o[t][4 * q + 1] * inv);
+                b.y = pack_bf16x2(o[t][4 * q + 2] * inv, o[t][4 * q + 3] * inv);
+                *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = b;
             } else {
-                *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, split) + d) =
+                *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, w.split) + d) =
                     f32x4{o[t][4 * q], o[t][4 * q + 1], o[t][4 * q + 2], o[t][4 * q + 3]};
             }
         }
-    if (!whole && h2 == 0) {
-        float *ml = part_ml(v, out_row, split);
+    if (!w.whole && h2 == 0) {
+        float *ml = part_ml(v, out_row, w.split);
         ml[0] = m;
         ml[1] = l;
     }
+}
+
+// ---------------------------------------------------------------------------
+// The same with 16 rows per wave and eight waves, for D = 256: 32 rows' sums
+// and q parts leave room for one wave per SIMD only (360 registers), and a
+// lone wave issues every other slot and overlaps nothing (a mixed step of
+// 2,048 tokens: 71 us).  Lanes as in the few-rows kernel with 64 keys, operands
+// from the LDS.
+// ---------------------------------------------------------------------------
+constexpr int kNarrowThreads = 512;
+
+// 16 lanes read the same piece of keys 16 (i / 4) + 4 t + i % 4
+template <int D>
+__device__ __forceinline__ int k_piece_narrow(int key, int p) {
+    static_assert(D == 256, "16 pieces per key");
+    return key * 16 + (p ^ ((key & 3) | (key >> 4 & 3) << 2));
+}
+
+template <int D>
+__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks) {
+    constexpr int KS = D / 128, DT = D / 16;
+    __shared__ ManyLds<D> lds;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    ManyShare w;
+    if (!many_share(a, v, block, blocks, w)) return;
+    const Request &rq = w.rq;
+    const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
+    const long long wrow = w.row0 + 16 * wave, row = wrow + c;
+    const bool live = row < w.n_rows;
+    const int i_row = live ? (int)(row / G) : 0, h = hk * G + (live ? (int)(row - (long long)i_row * G) : 0);
+    int jb = 0, je = 0;
+    if (live) key_range(a, rq, i_row, jb, je);
+    jb = max(jb, k_lo);
+    je = min(je, k_hi);
+    const WaveKeys wk = wave_keys(a, w, wrow, 16);
+    i32x8 qh[KS], ql[KS];
+    const float to_log2 = a.scale * kLog2e *
+                          split_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, qh, ql);
+    Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
+
+    f32x4 o[DT] = {};
+    float m = kNegInf, l = 0.f;
+    uint32_t met_nan = 0;
+    int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
+    if (j0 < k_hi) {
+        stage.pages(j0);
+        stage.load(j0, 0);
+        stage.pages(j0 + kTileKeys);
+    }
+    for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
+        const int jn = j0 + kTileKeys;
+        stage.arrive(buf);
+        if (jn < k_hi) {
+            stage.load(jn, buf ^ 1);
+            stage.pages(jn + kTileKeys);
+        }
+        if (j0 >= wk.hi || jn <= wk.lo) continue;
+        f32x4 x[4] = {};
+        // (operands are read one step ahead of their products)
+        auto k_operand = [&](int i) {
+            const int t = i / KS, st = i % KS, key = 16 * (c >> 2) + 4 * t + (c & 3);
+            const uint4 u = lds.k[buf][k_piece_narrow<D>(key, 8 * st + g)];
+            const uint4 b = lds.k[buf][k_piece_narrow<D>(key, 8 * st + 4 + g)];
+            return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+        };
+        i32x8 k8 = k_operand(0);
+#pragma unroll
+        for (int i = 0; i < 4 * KS; ++i) {
+            const i32x8 next = k_operand(min(i + 1, 4 * KS - 1));
+            asm volatile("" ::: "memory");
+            x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+            x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+            k8 = next;
+        }
+        const int jg = j0 + 16 * g, ok = lds.ok[buf][g];
+        const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
+        uint32_t pw[8];
+        weigh(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], masked, ok, jg, jb, je, m, l, o, pw);
+        uint32_t keep[4];
+        if (masked)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
+        const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+        uint4 vw = lds.v[buf][v_piece(c, g)];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            const uint4 next = lds.v[buf][v_piece(16 * min(t + 1, DT - 1) + c, g)];
+            asm volatile("" ::: "memory");
+            if (masked) {
+                vw.x &= keep[0];
+                vw.y &= keep[1];
+                vw.z &= keep[2];
+                vw.w &= keep[3];
+                met_nan |= take_nan(vw.x) | take_nan(vw.y) | take_nan(vw.z) | take_nan(vw.w);
+            }
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.x, vw.y), p0, o[t], 0, 0, 0);
+            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.z, vw.w), p1, o[t], 0, 0, 0);
+            vw = next;
+        }
+    }
+
+    if (__any(met_nan != 0)) {
+        unsigned long long bits[1] = {0};
+        find_nan<4 * DT>(
+            a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
+            [&](int j) { return j < wk.all0 || j + kTileKeys > wk.all1 || __any(stage.page_at(j + 16 * g) < 0); },
+            [&](int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }, [&](int j) { return stage.page_at(j); });
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (bits[0] >> (4 * t + r) & 1) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+        const int d = 16 * t + 4 * g;
+        if (w.whole) {
+            uint2 b;
+            b.x = pack_bf16x2(o[t].x * inv, o[t].y * inv);
+            b.y = pack_bf16x2(o[t].z * inv, o[t].w * inv);
+            *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = b;
+        } else {
+            *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, w.split) + d) = o[t];
+        }
+    }
+    if (!w.whole && g == 0) {
+        float *ml = part_ml(v, out_row, w.split);
+        ml[0] = m;
+        ml[1] = l;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The kernels: a token per request at most on average (few rows alone, eight
+// waves), and else both kinds of requests in one grid -- the large ones'
+// workgroups first, those of the small ones (decode rows) take the CUs that
+// are left and each that becomes free.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(512, 2) void attention_few_kernel(AttentionArgs a, Division v) {
+    few_rows<D, 8, Take::kAll>(a, v, blockIdx.x);
+}
+
+constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThreads; }
+
+template <int D>
+__global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kernel(AttentionArgs a, Division few, Division many,
+                                                                              int many_blocks) {
+    const int block = blockIdx.x;
+    if (block >= many_blocks) few_rows<D, mixed_threads(D) / 64, Take::kSmall>(a, few, block - many_blocks);
+    else if constexpr (D == 256) many_rows_narrow<D>(a, many, block, many_blocks);
+    else many_rows_wide<D>(a, many, block, many_blocks);
 }
 
 // ---------------------------------------------------------------------------
@@ -968,32 +1185,33 @@ int64_t attention_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads,
     return (p.few.floats + p.many.floats) * 4;
 }
 
+// the partial results of a launch at `ws`
+static Division division(const Launch &p, int d, float *ws) { return {p.chunk, p.splits, ws, ws + p.rows * p.splits * d}; }
+
 template <int D, Take TAKE>
-static hipError_t launch_few(const AttentionArgs &a, const Launch &p, float *ws, hipStream_t stream) {
-    const long long blocks = p.units * p.splits;
-    if (blocks > 0x7fffffffLL || p.rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    const Division v{p.chunk, p.splits, ws, ws + p.rows * p.splits * D};
-    hipLaunchKernelGGL((attention_few_kernel<D, TAKE>), dim3((unsigned)blocks), dim3(64 * kFewWaves), 0, stream, a, v);
+static void launch_join(const AttentionArgs &a, const Launch &p, const Division &v, int tile_rows, hipStream_t stream) {
     if (p.splits > 1)
         hipLaunchKernelGGL((attention_join_kernel<D, TAKE>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, a, v,
-                           p.rows, kTileRows);
-    return hipGetLastError();
+                           p.rows, tile_rows);
 }
 
 template <int D>
 static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
     const Plan p = plan_of(a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
-    if (p.few_takes == Take::kAll) return launch_few<D, Take::kAll>(a, p.few, a.workspace, stream);
-    const long long blocks = p.many.units * p.many.splits;
-    if (blocks > 0x7fffffffLL || p.many.rows > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    const hipError_t e = launch_few<D, Take::kSmall>(a, p.few, a.workspace, stream);
-    if (e != hipSuccess) return e;
-    float *ws = a.workspace + p.few.floats;
-    const Division v{p.many.chunk, p.many.splits, ws, ws + p.many.rows * p.many.splits * D};
-    hipLaunchKernelGGL((attention_many_kernel<D>), dim3((unsigned)blocks), dim3(kManyThreads), 0, stream, a, v);
-    if (p.many.splits > 1)
-        hipLaunchKernelGGL((attention_join_kernel<D, Take::kLarge>), dim3((unsigned)((p.many.rows + 3) / 4)), dim3(256), 0,
-                           stream, a, v, p.many.rows, kManyRows);
+    const long long few = p.few.units * p.few.splits, many = p.many.units * p.many.splits;
+    if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
+        return hipErrorInvalidConfiguration;
+    const Division vf = division(p.few, D, a.workspace);
+    if (p.few_takes == Take::kAll) {
+        hipLaunchKernelGGL((attention_few_kernel<D>), dim3((unsigned)few), dim3(512), 0, stream, a, vf);
+        launch_join<D, Take::kAll>(a, p.few, vf, kTileRows, stream);
+        return hipGetLastError();
+    }
+    const Division vm = division(p.many, D, a.workspace + p.few.floats);
+    hipLaunchKernelGGL((attention_mixed_kernel<D>), dim3((unsigned)(few + many)), dim3(mixed_threads(D)), 0, stream, a, vf, vm,
+                       (int)many);
+    launch_join<D, Take::kSmall>(a, p.few, vf, kTileRows, stream);
+    launch_join<D, Take::kLarge>(a, p.many, vm, kManyRows, stream);
     return hipGetLastError();
 }
 
