@@ -78,7 +78,22 @@ __device__ __forceinline__ int find_request(const AttentionArgs &a, long long ti
     return lo;
 }
 
-__device__ __forceinline__ float max_over(float x, int lanes_apart) { return fmaxf(x, __shfl_xor(x, lanes_apart, 64)); }
+// The larger of a lane's value and that of the lane 32 (16) further or back: the
+// swap of half-waves (of neighbouring rows of 16) between two copies leaves both
+// lanes' values in each.  (The compiler must not see that they are copies: it
+// then takes the two results for equal.)
+__device__ __forceinline__ float max_over32(float x) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x), v = u;
+    asm("" : "+v"(v));
+    const auto r = __builtin_amdgcn_permlane32_swap(u, v, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float max_over16(float x) {
+    uint32_t u = __builtin_bit_cast(uint32_t, x), v = u;
+    asm("" : "+v"(v));
+    const auto r = __builtin_amdgcn_permlane16_swap(u, v, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
 
 // 8 codes -> 8 bf16 values
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w0, uint32_t w1) {
@@ -102,6 +117,15 @@ __device__ __forceinline__ uint32_t take_nan(uint32_t &w) {
     const uint32_t b = nan_codes(w) >> 7;
     w &= ~(b * 0xffu);
     return b;
+}
+// four words of values, those of no key in `keep` and NaN codes zeroed; returned:
+// whether there were any of the latter
+__device__ __forceinline__ uint32_t masked_values(uint4 &w, const uint32_t (&keep)[4]) {
+    w.x &= keep[0];
+    w.y &= keep[1];
+    w.z &= keep[2];
+    w.w &= keep[3];
+    return take_nan(w.x) | take_nan(w.y) | take_nan(w.z) | take_nan(w.w);
 }
 // the bytes of a word of keys j .. j + 3 that lie in [lo, hi)
 __device__ __forceinline__ uint32_t key_bytes(int j, int lo, int hi) {
@@ -161,7 +185,7 @@ __device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)
 #pragma unroll
         for (int e = 0; e < 16; ++e) m = is_finite(f[l][e]) ? fmaxf(m, fabsf(f[l][e])) : m;
     }
-    m = max_over(max_over(m, 16), 32);
+    m = max_over32(max_over16(m));
     const float up = split_factor(m);
 #pragma unroll
     for (int l = 0; l < KL; ++l)
@@ -191,19 +215,22 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[t][r] *= factor;
-    if (masked)
+    if (masked) {
+        // from the row's first and past its last key of these, none of a missing page
+        const int from = seen_page ? jb - jg : 4 * NT, to = je - jg;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int j = jg + 4 * t + r;
-                if (!(seen_page && j >= jb && j < je)) x[t][r] = kNegInf;
-            }
+            for (int r = 0; r < 4; ++r)
+                if (4 * t + r < from || 4 * t + r >= to) x[t][r] = kNegInf;
+        // the scale of values that the row does not see may be anything
+        if (max(from, 0) >= min(to, 4 * NT)) vs = 0.f;
+    }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
-    mx = max_over(max_over(mx, 16), 32);
+    mx = max_over32(max_over16(mx));
     if (__any(mx > m)) {
         const float m_new = fmaxf(m, mx);
         const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -220,11 +247,9 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
         for (int r = 0; r < 4; ++r) {
             e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
             l += e[r];
-            // a masked key's scale may be anything
-            e[r] = masked && x[t][r] == kNegInf ? 0.f : e[r] * vs;
         }
-        pw[2 * t] = pack_bf16x2(e[0], e[1]);
-        pw[2 * t + 1] = pack_bf16x2(e[2], e[3]);
+        pw[2 * t] = pack_bf16x2(e[0] * vs, e[1] * vs);
+        pw[2 * t + 1] = pack_bf16x2(e[2] * vs, e[3] * vs);
     }
 }
 
@@ -546,12 +571,28 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 128;
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
+constexpr int kWideAhead = 2;
 
 // 16 bytes per lane from `src` to 64 consecutive places of the LDS, of which
 // `dst` is the wave's first
 __device__ __forceinline__ void to_lds(const uint8_t *src, uint4 *dst) {
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
                                      (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// use(i, read(i)) for i < N, each read A steps before its use and, left alone
+// by the compiler, not earlier: it would read until it runs out of registers.
+template <int N, int A, typename Read, typename Use>
+__device__ __forceinline__ void run_ahead(Read read, Use use) {
+    decltype(read(0)) w[N];          // all but A + 1 of them dead at any time
+#pragma unroll
+    for (int i = 0; i < (A < N ? A : N); ++i) w[i] = read(i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (i + A < N) w[i + A] = read(i + A);
+        asm volatile("" ::: "memory");
+        use(i, w[i]);
+    }
 }
 
 template <int D>
@@ -624,40 +665,52 @@ struct Staging {
     const AttentionArgs &a;
     ManyLds<D> &lds;
     const int32_t *bt;
-    int hk, k_hi, shift, wave, k_key, v_d, v_g;
+    int k_hi, shift, wave, hk;
+    uint32_t pitch;                // bytes of a page, all kv heads
+    // a tile begins at a multiple of 64 keys, so a piece's place in its page and
+    // its page's place in the tile's pages stay the same
+    uint32_t k_off[NL], v_off;
+    int k_page[NL], v_page, s_page;
     int idk[NL], idv, ids, s_ok;
     float s_ks, s_vs;
 
     __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
-        : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), hk(w.hk), k_hi(w.k_hi),
-          shift(__builtin_ctz(a_.page)), wave(wave_), k_key(threadIdx.x / PPK), v_d(threadIdx.x >> 2),
-          v_g((threadIdx.x & 3) ^ (v_d >> 2 & 3)), s_ok(0), s_ks(0.f), s_vs(0.f) {}
-    // the page of key j, -1: none
-    __device__ __forceinline__ int page_at(int j) const {
-        const int p = j >> shift;
-        const int id = j < k_hi && p < a.max_pages ? bt[p] : -1;
-        return (unsigned)id < (unsigned)a.num_pages ? id : -1;
-    }
-    __device__ __forceinline__ void pages(int j0) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + i * KEYS + k_key);
-        idv = page_at(j0 + 16 * v_g);
-        ids = page_at(j0 + 16 * (threadIdx.x & 3));
-    }
-    __device__ __forceinline__ void load(int j0, int buf) {
+        : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
+          wave(wave_), hk(w.hk), pitch((uint32_t)a_.num_kv_heads * a_.page * D), s_ok(0), s_ks(0.f), s_vs(0.f) {
         const int tid = threadIdx.x, in_page = a.page - 1;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            const int key = i * KEYS + k_key, p = PLACE(key, tid % PPK) - key * PPK;
-            to_lds(a.k_cache + (((long long)max(idk[i], 0) * a.num_kv_heads + hk) * a.page + ((j0 + key) & in_page)) * D + 16 * p,
-                   &lds.k[buf][i * THREADS + 64 * wave]);
+            const int key = i * KEYS + tid / PPK, p = PLACE(key, tid % PPK) - key * PPK;
+            k_off[i] = (hk * a.page + (key & in_page)) * D + 16 * p;
+            k_page[i] = key >> shift;
         }
-        const uint8_t *p = a.v_cache + (((long long)max(idv, 0) * a.num_kv_heads + hk) * D + v_d) * a.page +
-                           ((j0 + 16 * v_g) & in_page);
+        const int v_d = tid >> 2, v_g = (tid & 3) ^ (v_d >> 2 & 3);
+        v_off = (hk * D + v_d) * a.page + (16 * v_g & in_page);
+        v_page = 16 * v_g >> shift;
+        s_page = 16 * (tid & 3) >> shift;
+    }
+    // the page of that number in the request's row, -1: none
+    __device__ __forceinline__ int page_number(int p) const {
+        const int id = p << shift < k_hi && p < a.max_pages ? bt[p] : -1;
+        return (unsigned)id < (unsigned)a.num_pages ? id : -1;
+    }
+    // the page of key j
+    __device__ __forceinline__ int page_at(int j) const { return j < k_hi ? page_number(j >> shift) : -1; }
+    __device__ __forceinline__ void pages(int j0) {
+        const int p0 = j0 >> shift;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) idk[i] = page_number(p0 + k_page[i]);
+        idv = page_number(p0 + v_page);
+        ids = page_number(p0 + s_page);
+    }
+    __device__ __forceinline__ void load(int buf) {
 #pragma unroll
         for (int i = 0; i < NL; ++i)
-            to_lds(p + (long long)(THREADS / 4) * i * a.page, &lds.v[buf][i * THREADS + 64 * wave]);
-        if (tid < 4) {
+            to_lds(a.k_cache + ((uint64_t)max(idk[i], 0) * pitch + k_off[i]), &lds.k[buf][i * THREADS + 64 * wave]);
+        const uint8_t *p = a.v_cache + ((uint64_t)max(idv, 0) * pitch + v_off);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) to_lds(p + i * (THREADS / 4) * a.page, &lds.v[buf][i * THREADS + 64 * wave]);
+        if (threadIdx.x < 4) {
             const long long ph = (long long)max(ids, 0) * a.num_kv_heads + hk;
             s_ks = a.k_scale[ph];
             s_vs = a.v_scale[ph];
@@ -722,7 +775,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m = is_finite(f[e]) ? fmaxf(m, fabsf(f[e])) : m;
             }
-        m = max_over(m, 32);
+        m = max_over32(m);
         const float up = split_factor(m);
         to_log2 = a.scale * kLog2e * (1.f / up);
 #pragma unroll
@@ -742,44 +795,42 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     }
 
     Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w, wave);
+    // this lane's operand rows: the t-th K operand's is 16 t keys further on, with
+    // its pieces in the same order, and so the t-th V operand's, 32 t elements
+    const int key = 32 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
+    const int k_row = key * (D / 16), k_swap = k_piece<D>(key, 2 * h2) - k_row, v_swap = v_piece(c, 2 * h2) - 4 * c;
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
     uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
     if (j0 < k_hi) {
         stage.pages(j0);
-        stage.load(j0, 0);
+        stage.load(0);
         stage.pages(j0 + kTileKeys);
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
         stage.arrive(buf);
         if (jn < k_hi) {
-            stage.load(jn, buf ^ 1);
+            stage.load(buf ^ 1);
             stage.pages(jn + kTileKeys);
         }
         if (j0 < wk.hi && jn > wk.lo) {
             f32x16 x[2] = {};
-            // (operands are read one step ahead of their products; left alone the
-            // compiler reads many steps ahead and runs out of registers)
+            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c;
             auto k_operand = [&](int i) {
-                const int t = i / KS, st = i % KS, key = 32 * (c >> 2 & 1) + 16 * t + 4 * (c >> 3) + (c & 3);
-                const uint4 u = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2)];
-                const uint4 w = lds.k[buf][k_piece<D>(key, 4 * st + 2 * h2 + 1)];
+                const int t = i / KS, st = i % KS;
+                const uint4 u = kt[16 * t * (D / 16) + (k_swap ^ 4 * st)], w = kt[16 * t * (D / 16) + (k_swap ^ (4 * st + 1))];
                 return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
             };
-            i32x8 k8 = k_operand(0);
-#pragma unroll
-            for (int i = 0; i < 2 * KS; ++i) {
-                const i32x8 next = k_operand(min(i + 1, 2 * KS - 1));
-                asm volatile("" ::: "memory");
+            auto v_operand = [&](int i) { return vt[32 * 4 * (i / 2) + (v_swap ^ i % 2)]; };
+            run_ahead<2 * KS, 1>(k_operand, [&](int i, const i32x8 &k8) {
                 x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
                 x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-                k8 = next;
-            }
+            });
             const int ok0 = lds.ok[buf][2 * h2], ok1 = lds.ok[buf][2 * h2 + 1];
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1));
-            float mx = kNegInf;
+            float mx = kNegInf, vs[2] = {lds.vs[buf][2 * h2], lds.vs[buf][2 * h2 + 1]};
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float factor = to_log2 * lds.ks[buf][2 * h2 + t];
@@ -788,17 +839,20 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             }
             if (masked)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t) {
+                    // from the row's first and past its last key of these 16, none of a missing page
+                    const int jg = j0 + 32 * h2 + 16 * t, from = (t ? ok1 : ok0) ? jb - jg : 16, to = je - jg;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int j = j0 + 32 * h2 + 16 * t + r;
-                        if (!((t ? ok1 : ok0) && j >= jb && j < je)) x[t][r] = kNegInf;
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        if (r < from || r >= to) x[t][r] = kNegInf;
+                    // the scale of values that the row does not see may be anything
+                    if (max(from, 0) >= min(to, 16)) vs[t] = 0.f;
+                }
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[t][r]);
-            mx = max_over(mx, 32);
+            mx = max_over32(mx);
             if (__any(mx > m)) {
                 const float m_new = fmaxf(m, mx);
                 const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -811,54 +865,40 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             bf16x8 p[4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const float vs = lds.vs[buf][2 * h2 + t];
                 uint32_t pw[8];
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
-                    float e0 = __builtin_amdgcn_exp2f(x[t][r] - at), e1 = __builtin_amdgcn_exp2f(x[t][r + 1] - at);
+                    const float e0 = __builtin_amdgcn_exp2f(x[t][r] - at), e1 = __builtin_amdgcn_exp2f(x[t][r + 1] - at);
                     l += e0 + e1;
-                    e0 *= vs;
-                    e1 *= vs;
-                    if (masked) {        // a masked key's scale may be anything
-                        if (x[t][r] == kNegInf) e0 = 0.f;
-                        if (x[t][r + 1] == kNegInf) e1 = 0.f;
-                    }
-                    pw[r / 2] = pack_bf16x2(e0, e1);
+                    pw[r / 2] = pack_bf16x2(e0 * vs[t], e1 * vs[t]);
                 }
                 p[2 * t] = as_bf16x8(pw[0], pw[1], pw[2], pw[3]);
                 p[2 * t + 1] = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
             }
-            // values that no row of the wave sees may be anything: zero; NaN: find_nan
-            uint32_t keep[2][4];
-            if (masked)
+            // `fix(w, g)`: what a masked tile does to four words of values of granule g
+            auto multiply = [&](auto fix) {
+                run_ahead<2 * DT, kWideAhead>(v_operand, [&](int i, uint4 vw) {
+                    const int t = i / 2, g = i % 2;
+                    fix(vw, g);
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.x, vw.y), p[2 * g], o[t], 0, 0, 0);
+                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.z, vw.w), p[2 * g + 1], o[t], 0, 0, 0);
+                });
+            };
+            if (masked) {
+                // values that no row of the wave sees may be anything: zero; NaN: find_nan
+                uint32_t keep[2][4];
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         keep[g][w] = (g ? ok1 : ok0) ? key_bytes(j0 + 32 * h2 + 16 * g + 4 * w, wk.lo, wk.hi) : 0u;
-            uint4 vw = lds.v[buf][v_piece(c, 2 * h2)];
-#pragma unroll
-            for (int i = 0; i < 2 * DT; ++i) {
-                const int t = i / 2, g = i % 2, n = min(i + 1, 2 * DT - 1);
-                const uint4 next = lds.v[buf][v_piece(32 * (n / 2) + c, 2 * h2 + n % 2)];
-                asm volatile("" ::: "memory");
-                if (masked) {
-                    vw.x &= keep[g][0];
-                    vw.y &= keep[g][1];
-                    vw.z &= keep[g][2];
-                    vw.w &= keep[g][3];
-                    met_nan |= take_nan(vw.x) | take_nan(vw.y) | take_nan(vw.z) | take_nan(vw.w);
-                }
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.x, vw.y), p[2 * g], o[t], 0, 0, 0);
-                o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.z, vw.w), p[2 * g + 1], o[t], 0, 0, 0);
-                vw = next;
+                multiply([&](uint4 &w, int g) { met_nan |= masked_values(w, keep[g]); });
+            } else {
+                multiply([](uint4 &, int) {});
             }
         }
     }
 
-    l += __shfl_xor(l, 32, 64);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
     if (__any(met_nan != 0)) {
         unsigned long long bits[(16 * DT + 63) / 64] = {};
         find_nan<16 * DT>(
@@ -873,7 +913,10 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             for (int r = 0; r < 16; ++r)
                 if (bits[t / 4] >> (16 * (t & 3) + r) & 1) o[t][r] = __builtin_bit_cast(float, 0x7fc00000u);
     }
+    l += __shfl_xor(l, 32, 64);
     if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long out_row = (long long)(rq.begin + i_row) * a.num_q_heads + h;
     // element 32 t + 8 q + 4 h2 + r of row c is o[t][4 q + r]
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -905,6 +948,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // from the LDS.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowThreads = 512;
+constexpr int kNarrowAhead = 3;
 
 // 16 lanes read the same piece of keys 16 (i / 4) + 4 t + i % 4
 template <int D>
@@ -937,6 +981,10 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     const float to_log2 = a.scale * kLog2e *
                           split_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, qh, ql);
     Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
+    // this lane's operand rows: the t-th K operand's is 4 t keys further on, with its
+    // pieces in the same order, and so the t-th V operand's, 16 t elements
+    const int key = 16 * (c >> 2) + (c & 3);
+    const int k_row = key * 16, k_swap = k_piece_narrow<D>(key, g) - k_row, v_swap = v_piece(c, g) - 4 * c;
 
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
@@ -944,58 +992,48 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
     if (j0 < k_hi) {
         stage.pages(j0);
-        stage.load(j0, 0);
+        stage.load(0);
         stage.pages(j0 + kTileKeys);
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
         stage.arrive(buf);
         if (jn < k_hi) {
-            stage.load(jn, buf ^ 1);
+            stage.load(buf ^ 1);
             stage.pages(jn + kTileKeys);
         }
         if (j0 >= wk.hi || jn <= wk.lo) continue;
         f32x4 x[4] = {};
-        // (operands are read one step ahead of their products)
+        const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c + v_swap;
         auto k_operand = [&](int i) {
-            const int t = i / KS, st = i % KS, key = 16 * (c >> 2) + 4 * t + (c & 3);
-            const uint4 u = lds.k[buf][k_piece_narrow<D>(key, 8 * st + g)];
-            const uint4 b = lds.k[buf][k_piece_narrow<D>(key, 8 * st + 4 + g)];
+            const int t = i / KS, st = i % KS;
+            const uint4 u = kt[4 * t * 16 + (k_swap ^ 8 * st)], b = kt[4 * t * 16 + (k_swap ^ (8 * st + 4))];
             return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
         };
-        i32x8 k8 = k_operand(0);
-#pragma unroll
-        for (int i = 0; i < 4 * KS; ++i) {
-            const i32x8 next = k_operand(min(i + 1, 4 * KS - 1));
-            asm volatile("" ::: "memory");
+        run_ahead<4 * KS, kNarrowAhead>(k_operand, [&](int i, const i32x8 &k8) {
             x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
             x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-            k8 = next;
-        }
+        });
         const int jg = j0 + 16 * g, ok = lds.ok[buf][g];
         const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
         uint32_t pw[8];
         weigh(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], masked, ok, jg, jb, je, m, l, o, pw);
-        uint32_t keep[4];
-        if (masked)
+        const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+        auto multiply = [&](auto fix) {
+            run_ahead<DT, kNarrowAhead>([&](int t) { return vt[16 * 4 * t]; }, [&](int t, uint4 vw) {
+                fix(vw);
+                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.x, vw.y), p0, o[t], 0, 0, 0);
+                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.z, vw.w), p1, o[t], 0, 0, 0);
+            });
+        };
+        if (masked) {
+            // values that no row of the wave sees may be anything: zero; NaN: find_nan
+            uint32_t keep[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
-        const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
-        uint4 vw = lds.v[buf][v_piece(c, g)];
-#pragma unroll
-        for (int t = 0; t < DT; ++t) {
-            const uint4 next = lds.v[buf][v_piece(16 * min(t + 1, DT - 1) + c, g)];
-            asm volatile("" ::: "memory");
-            if (masked) {
-                vw.x &= keep[0];
-                vw.y &= keep[1];
-                vw.z &= keep[2];
-                vw.w &= keep[3];
-                met_nan |= take_nan(vw.x) | take_nan(vw.y) | take_nan(vw.z) | take_nan(vw.w);
-            }
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.x, vw.y), p0, o[t], 0, 0, 0);
-            o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.z, vw.w), p1, o[t], 0, 0, 0);
-            vw = next;
+            multiply([&](uint4 &w) { met_nan |= masked_values(w, keep); });
+        } else {
+            multiply([](uint4 &) {});
         }
     }
 
