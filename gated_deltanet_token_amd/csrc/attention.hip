@@ -319,19 +319,23 @@ __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int
 // ---------------------------------------------------------------------------
 constexpr int few_keys(int d) { return d == 256 ? 32 : 64; }
 
+template <int D, int W>
+struct FewLds {
+    f32x4 red[W][D >= 128 ? 8 : D / 16][64];
+    float red_m[W][16], red_l[W][16];
+    // at D = 256 q's parts wait in the LDS: with sums, keys and values they
+    // would pass a lane's 256 registers
+    i32x4 q[D == 256 ? 8 : 1][64];
+};
+
 template <int D, int W, Take TAKE>
-__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block) {
+__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block, FewLds<D, W> &lds) {
     constexpr int TK = few_keys(D), NK = TK / 4, NT = TK / 16, NV = TK / 16;
     constexpr int KS = D >= 128 ? D / 128 : 1;       // contraction steps of 128
     constexpr int KL = D / 64;                       // 16-byte loads per key operand
     constexpr int DT = D / 16;                       // operands of 16 value elements
     constexpr int DTH = DT < 8 ? DT : 8;             // of which joined at once
-    __shared__ f32x4 red[W][DTH][64];
-    __shared__ float red_m[W][16], red_l[W][16];
-    // at D = 256 q's parts wait in the LDS: with sums, keys and values they
-    // would pass a lane's 256 registers
     constexpr bool QLDS = D == 256;
-    __shared__ i32x4 q_lds[QLDS ? 4 * KS : 1][64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4, kg = c >> 2;
@@ -380,10 +384,10 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         if (wave == 0) {
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                q_lds[4 * st][lane] = i32x4{qh[st][0], qh[st][1], qh[st][2], qh[st][3]};
-                q_lds[4 * st + 1][lane] = i32x4{qh[st][4], qh[st][5], qh[st][6], qh[st][7]};
-                q_lds[4 * st + 2][lane] = i32x4{ql[st][0], ql[st][1], ql[st][2], ql[st][3]};
-                q_lds[4 * st + 3][lane] = i32x4{ql[st][4], ql[st][5], ql[st][6], ql[st][7]};
+                lds.q[4 * st][lane] = i32x4{qh[st][0], qh[st][1], qh[st][2], qh[st][3]};
+                lds.q[4 * st + 1][lane] = i32x4{qh[st][4], qh[st][5], qh[st][6], qh[st][7]};
+                lds.q[4 * st + 2][lane] = i32x4{ql[st][0], ql[st][1], ql[st][2], ql[st][3]};
+                lds.q[4 * st + 3][lane] = i32x4{ql[st][4], ql[st][5], ql[st][6], ql[st][7]};
             }
         }
         __syncthreads();
@@ -450,8 +454,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         for (int st = 0; st < KS; ++st) {
             i32x8 hi8 = qh[st], lo8 = ql[st];
             if constexpr (QLDS) {
-                const i32x4 a0 = q_lds[4 * st][lane], a1 = q_lds[4 * st + 1][lane];
-                const i32x4 b0 = q_lds[4 * st + 2][lane], b1 = q_lds[4 * st + 3][lane];
+                const i32x4 a0 = lds.q[4 * st][lane], a1 = lds.q[4 * st + 1][lane];
+                const i32x4 b0 = lds.q[4 * st + 2][lane], b1 = lds.q[4 * st + 3][lane];
                 hi8 = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
                 lo8 = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
             }
@@ -513,16 +517,16 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     if (g == 0) {
-        red_m[wave][c] = m;
-        red_l[wave][c] = l;
+        lds.red_m[wave][c] = m;
+        lds.red_l[wave][c] = l;
     }
     __syncthreads();
     float m_all = kNegInf, l_all = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, red_m[w][c]);
+    for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, lds.red_m[w][c]);
     const float at = m_all == kNegInf ? 0.f : m_all;
 #pragma unroll
-    for (int w = 0; w < W; ++w) l_all += red_l[w][c] * __builtin_amdgcn_exp2f(red_m[w][c] - at);
+    for (int w = 0; w < W; ++w) l_all += lds.red_l[w][c] * __builtin_amdgcn_exp2f(lds.red_m[w][c] - at);
     const float f = __builtin_amdgcn_exp2f(m - at);
     const long long out_row = part_row<TAKE>(a, s, rq.begin + i_row, h, row, hk);
     const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
@@ -530,12 +534,12 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     for (int t0 = 0; t0 < DT; t0 += DTH) {
         if (t0) __syncthreads();
 #pragma unroll
-        for (int t = 0; t < DTH; ++t) red[wave][t][lane] = o[t0 + t] * f;
+        for (int t = 0; t < DTH; ++t) lds.red[wave][t][lane] = o[t0 + t] * f;
         __syncthreads();
         for (int t = wave; t < DTH; t += W) {
-            f32x4 sum = red[0][t][lane];
+            f32x4 sum = lds.red[0][t][lane];
 #pragma unroll
-            for (int w = 1; w < W; ++w) sum += red[w][t][lane];
+            for (int w = 1; w < W; ++w) sum += lds.red[w][t][lane];
             if (!live) continue;
             const int d = 16 * (t0 + t) + 4 * g;
             if (whole) {
@@ -573,13 +577,6 @@ constexpr int kManyRows = 128;
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
 constexpr int kWideAhead = 2;
 
-// 16 bytes per lane from `src` to 64 consecutive places of the LDS, of which
-// `dst` is the wave's first
-__device__ __forceinline__ void to_lds(const uint8_t *src, uint4 *dst) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-}
-
 // use(i, read(i)) for i < N, each read A steps before its use and, left alone
 // by the compiler, not earlier: it would read until it runs out of registers.
 template <int N, int A, typename Read, typename Use>
@@ -598,6 +595,7 @@ __device__ __forceinline__ void run_ahead(Read read, Use use) {
 template <int D>
 struct ManyLds {
     uint4 k[2][kTileKeys * D / 16], v[2][kTileKeys * D / 16];
+    // of the tile's four granules of 16 keys: scales, and whether there is a page
     float ks[2][4], vs[2][4];
     int ok[2][4];
 };
@@ -654,10 +652,16 @@ __device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const Many
     return k;
 }
 
-// Staging of a workgroup of THREADS threads: a tile's pieces go from memory to
-// the LDS without registers between.  A wave's load fills 64 consecutive
-// places; a lane's place says which piece it fetches (PLACE: the place of a
-// key's piece).
+// the LDS place of piece p of element row d of a tile's values
+__device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (d >> 2 & 3)); }
+
+// Staging of a workgroup of THREADS threads: the next tile's pieces are loaded
+// into registers before the work on this one and put into the other LDS buffer
+// after it, and the page numbers of the one behind with them.  (Loads from
+// memory straight to the LDS need no registers, but the compiler waits for all
+// of them before any read of the LDS: with them every tile waited out a round
+// trip to memory, and a prompt of 8,192 tokens took 660 us.)  PLACE: the LDS
+// place of a key's piece.
 template <int D, int THREADS, int (*PLACE)(int, int)>
 struct Staging {
     static constexpr int NL = 64 * D / 16 / THREADS;             // loads of a thread, of keys and of values
@@ -665,66 +669,82 @@ struct Staging {
     const AttentionArgs &a;
     ManyLds<D> &lds;
     const int32_t *bt;
-    int k_hi, shift, wave, hk;
+    int k_hi, shift, hk;
     uint32_t pitch;                // bytes of a page, all kv heads
-    // a tile begins at a multiple of 64 keys, so a piece's place in its page and
-    // its page's place in the tile's pages stay the same
+    // a tile begins at a multiple of 64 keys, so a piece's place in its page
+    // stays the same
     uint32_t k_off[NL], v_off;
-    int k_page[NL], v_page, s_page;
-    int idk[NL], idv, ids, s_ok;
-    float s_ks, s_vs;
+    int idk[NL], idv;              // pages of the tile to load next, -1: none
+    uint4 kr[NL], vr[NL];
+    float s_ks, s_vs;              // of granule tid % 4, whose page idv is
+    int s_ok;
 
-    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
+    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w)
         : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
-          wave(wave_), hk(w.hk), pitch((uint32_t)a_.num_kv_heads * a_.page * D), s_ok(0), s_ks(0.f), s_vs(0.f) {
+          hk(w.hk), pitch((uint32_t)a_.num_kv_heads * a_.page * D), s_ks(0.f), s_vs(0.f), s_ok(0) {
         const int tid = threadIdx.x, in_page = a.page - 1;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int key = i * KEYS + tid / PPK, p = PLACE(key, tid % PPK) - key * PPK;
-            k_off[i] = (hk * a.page + (key & in_page)) * D + 16 * p;
-            k_page[i] = key >> shift;
-        }
-        const int v_d = tid >> 2, v_g = (tid & 3) ^ (v_d >> 2 & 3);
-        v_off = (hk * D + v_d) * a.page + (16 * v_g & in_page);
-        v_page = 16 * v_g >> shift;
-        s_page = 16 * (tid & 3) >> shift;
+        for (int i = 0; i < NL; ++i) k_off[i] = (hk * a.page + (i * KEYS + tid / PPK & in_page)) * D + 16 * (tid % PPK);
+        v_off = (hk * D + (tid >> 2)) * a.page + (16 * (tid & 3) & in_page);
     }
-    // the page of that number in the request's row, -1: none
-    __device__ __forceinline__ int page_number(int p) const {
-        const int id = p << shift < k_hi && p < a.max_pages ? bt[p] : -1;
+    // the page of key j, -1: none
+    __device__ __forceinline__ int page_at(int j) const {
+        const int p = j >> shift, id = j < k_hi && p < a.max_pages ? bt[p] : -1;
         return (unsigned)id < (unsigned)a.num_pages ? id : -1;
     }
-    // the page of key j
-    __device__ __forceinline__ int page_at(int j) const { return j < k_hi ? page_number(j >> shift) : -1; }
     __device__ __forceinline__ void pages(int j0) {
-        const int p0 = j0 >> shift;
+        // (a key past the end has no page, but a piece of its granule is loaded with
+        // the keys before it: the granule's first key decides)
 #pragma unroll
-        for (int i = 0; i < NL; ++i) idk[i] = page_number(p0 + k_page[i]);
-        idv = page_number(p0 + v_page);
-        ids = page_number(p0 + s_page);
+        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + (i * KEYS + threadIdx.x / PPK & ~15));
+        idv = page_at(j0 + 16 * (threadIdx.x & 3));
     }
-    __device__ __forceinline__ void load(int buf) {
+    __device__ __forceinline__ void load() {
 #pragma unroll
         for (int i = 0; i < NL; ++i)
-            to_lds(a.k_cache + ((uint64_t)max(idk[i], 0) * pitch + k_off[i]), &lds.k[buf][i * THREADS + 64 * wave]);
-        const uint8_t *p = a.v_cache + ((uint64_t)max(idv, 0) * pitch + v_off);
+            kr[i] = *reinterpret_cast<const uint4 *>(a.k_cache + ((uint64_t)max(idk[i], 0) * pitch + k_off[i]));
+        const uint8_t *v = a.v_cache + ((uint64_t)max(idv, 0) * pitch + v_off);
 #pragma unroll
-        for (int i = 0; i < NL; ++i) to_lds(p + i * (THREADS / 4) * a.page, &lds.v[buf][i * THREADS + 64 * wave]);
+        for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const uint4 *>(v + i * (THREADS / 4) * a.page);
         if (threadIdx.x < 4) {
-            const long long ph = (long long)max(ids, 0) * a.num_kv_heads + hk;
+            const long long ph = (long long)max(idv, 0) * a.num_kv_heads + hk;
             s_ks = a.k_scale[ph];
             s_vs = a.v_scale[ph];
-            s_ok = ids >= 0;
+            s_ok = idv >= 0;
         }
     }
-    // the tile has arrived, for all waves, and the other buffer is free
-    __device__ __forceinline__ void arrive(int buf) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        if (threadIdx.x < 4) {
-            lds.ks[buf][threadIdx.x] = s_ks;
-            lds.vs[buf][threadIdx.x] = s_vs;
-            lds.ok[buf][threadIdx.x] = s_ok;
+    __device__ __forceinline__ void put(int buf) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            lds.k[buf][PLACE(i * KEYS + tid / PPK, tid % PPK)] = kr[i];
+            lds.v[buf][v_piece(i * (THREADS / 4) + (tid >> 2), tid & 3)] = vr[i];
         }
+        if (tid < 4) {
+            lds.ks[buf][tid] = s_ks;
+            lds.vs[buf][tid] = s_vs;
+            lds.ok[buf][tid] = s_ok;
+        }
+    }
+    __device__ __forceinline__ void begin(int j0) {
+        pages(j0);
+        load();
+        pages(j0 + kTileKeys);
+        put(0);
+        __syncthreads();
+    }
+    // before the work on the tile at j0: the next one's loads go out
+    __device__ __forceinline__ void ahead(int j0) {
+        if (j0 + kTileKeys < k_hi) {
+            load();
+            pages(j0 + 2 * kTileKeys);
+        }
+        asm volatile("" ::: "memory");
+    }
+    // after it: into the other buffer
+    __device__ __forceinline__ void next(int j0, int buf) {
+        asm volatile("" ::: "memory");
+        if (j0 + kTileKeys < k_hi) put(buf ^ 1);
         __syncthreads();
     }
 };
@@ -734,13 +754,11 @@ __device__ __forceinline__ int k_piece(int key, int p) {
     constexpr int shift = D == 256 ? 0 : D == 128 ? 1 : 2;
     return key * (D / 16) + (p ^ (((key & 7) | (key >> 5 & 1) << 3) >> shift));
 }
-__device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (d >> 2 & 3)); }
 
 template <int D>
-__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks) {
+__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
     constexpr int KS = D / 64;                       // contraction steps of 64
     constexpr int DT = D / 32;                       // operands of 32 value elements
-    __shared__ ManyLds<D> lds;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 31, h2 = lane >> 5;
@@ -794,7 +812,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             }
     }
 
-    Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w, wave);
+    Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w);
     // this lane's operand rows: the t-th K operand's is 16 t keys further on, with
     // its pieces in the same order, and so the t-th V operand's, 32 t elements
     const int key = 32 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
@@ -803,100 +821,83 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     float m = kNegInf, l = 0.f;
     uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
-    if (j0 < k_hi) {
-        stage.pages(j0);
-        stage.load(0);
-        stage.pages(j0 + kTileKeys);
-    }
+    if (j0 < k_hi) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.arrive(buf);
-        if (jn < k_hi) {
-            stage.load(buf ^ 1);
-            stage.pages(jn + kTileKeys);
-        }
+        stage.ahead(j0);
         if (j0 < wk.hi && jn > wk.lo) {
-            f32x16 x[2] = {};
+            const bool ok01[2] = {lds.ok[buf][2 * h2] != 0, lds.ok[buf][2 * h2 + 1] != 0};
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok01[0] && ok01[1]));
             const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c;
-            auto k_operand = [&](int i) {
-                const int t = i / KS, st = i % KS;
-                const uint4 u = kt[16 * t * (D / 16) + (k_swap ^ 4 * st)], w = kt[16 * t * (D / 16) + (k_swap ^ (4 * st + 1))];
-                return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
-            };
-            auto v_operand = [&](int i) { return vt[32 * 4 * (i / 2) + (v_swap ^ i % 2)]; };
-            run_ahead<2 * KS, 1>(k_operand, [&](int i, const i32x8 &k8) {
-                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-            });
-            const int ok0 = lds.ok[buf][2 * h2], ok1 = lds.ok[buf][2 * h2 + 1];
-            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1));
-            float mx = kNegInf, vs[2] = {lds.vs[buf][2 * h2], lds.vs[buf][2 * h2 + 1]};
+            // half of the tile at a time: keys 16 t .. 16 t + 15 of each of its halves
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
+                f32x16 x = {};
+                run_ahead<KS, 1>(
+                    [&](int st) {
+                        const uint4 u = kt[16 * t * (D / 16) + (k_swap ^ 4 * st)];
+                        const uint4 b = kt[16 * t * (D / 16) + (k_swap ^ (4 * st + 1))];
+                        return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+                    },
+                    [&](int st, const i32x8 &k8) {
+                        x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[st], x, 0, 0, 0, 0, 0, 0);
+                        x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x, 0, 0, 0, 0, 0, 0);
+                    });
+                const bool ok = ok01[t];
                 const float factor = to_log2 * lds.ks[buf][2 * h2 + t];
+                float mx = kNegInf, vs = lds.vs[buf][2 * h2 + t];
+                const int jg = j0 + 32 * h2 + 16 * t;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[t][r] *= factor;
-            }
-            if (masked)
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int r = 0; r < 16; ++r) x[r] *= factor;
+                if (masked) {
                     // from the row's first and past its last key of these 16, none of a missing page
-                    const int jg = j0 + 32 * h2 + 16 * t, from = (t ? ok1 : ok0) ? jb - jg : 16, to = je - jg;
+                    const int from = ok ? jb - jg : 16, to = je - jg;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        if (r < from || r >= to) x[t][r] = kNegInf;
+                        if (r < from || r >= to) x[r] = kNegInf;
                     // the scale of values that the row does not see may be anything
-                    if (max(from, 0) >= min(to, 16)) vs[t] = 0.f;
+                    if (max(from, 0) >= min(to, 16)) vs = 0.f;
                 }
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[r]);
+                mx = max_over32(mx);
+                if (__any(mx > m)) {
+                    const float m_new = fmaxf(m, mx);
+                    const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+                    m = m_new;
+                    l *= f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[t][r]);
-            mx = max_over32(mx);
-            if (__any(mx > m)) {
-                const float m_new = fmaxf(m, mx);
-                const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
-                m = m_new;
-                l *= f;
-#pragma unroll
-                for (int t = 0; t < DT; ++t) o[t] *= f;
-            }
-            const float at = m == kNegInf ? 0.f : m;
-            bf16x8 p[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
+                    for (int i = 0; i < DT; ++i) o[i] *= f;
+                }
+                const float at = m == kNegInf ? 0.f : m;
                 uint32_t pw[8];
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
-                    const float e0 = __builtin_amdgcn_exp2f(x[t][r] - at), e1 = __builtin_amdgcn_exp2f(x[t][r + 1] - at);
+                    const float e0 = __builtin_amdgcn_exp2f(x[r] - at), e1 = __builtin_amdgcn_exp2f(x[r + 1] - at);
                     l += e0 + e1;
-                    pw[r / 2] = pack_bf16x2(e0 * vs[t], e1 * vs[t]);
+                    pw[r / 2] = pack_bf16x2(e0 * vs, e1 * vs);
                 }
-                p[2 * t] = as_bf16x8(pw[0], pw[1], pw[2], pw[3]);
-                p[2 * t + 1] = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
-            }
-            // `fix(w, g)`: what a masked tile does to four words of values of granule g
-            auto multiply = [&](auto fix) {
-                run_ahead<2 * DT, kWideAhead>(v_operand, [&](int i, uint4 vw) {
-                    const int t = i / 2, g = i % 2;
-                    fix(vw, g);
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.x, vw.y), p[2 * g], o[t], 0, 0, 0);
-                    o[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(vw.z, vw.w), p[2 * g + 1], o[t], 0, 0, 0);
-                });
-            };
-            if (masked) {
-                // values that no row of the wave sees may be anything: zero; NaN: find_nan
-                uint32_t keep[2][4];
+                const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+                // `fix(w)`: what a masked tile does to four words of values
+                auto multiply = [&](auto fix) {
+                    run_ahead<DT, kWideAhead>([&](int i) { return vt[32 * 4 * i + (v_swap ^ t)]; }, [&](int i, uint4 w) {
+                        fix(w);
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.x, w.y), p0, o[i], 0, 0, 0);
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.z, w.w), p1, o[i], 0, 0, 0);
+                    });
+                };
+                if (masked) {
+                    // values that no row of the wave sees may be anything: zero; NaN: find_nan
+                    uint32_t keep[4];
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        keep[g][w] = (g ? ok1 : ok0) ? key_bytes(j0 + 32 * h2 + 16 * g + 4 * w, wk.lo, wk.hi) : 0u;
-                multiply([&](uint4 &w, int g) { met_nan |= masked_values(w, keep[g]); });
-            } else {
-                multiply([](uint4 &, int) {});
+                    for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
+                    multiply([&](uint4 &w) { met_nan |= masked_values(w, keep); });
+                } else {
+                    multiply([](uint4 &) {});
+                }
             }
         }
+        stage.next(j0, buf);
     }
 
     if (__any(met_nan != 0)) {
@@ -958,9 +959,8 @@ __device__ __forceinline__ int k_piece_narrow(int key, int p) {
 }
 
 template <int D>
-__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks) {
+__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
     constexpr int KS = D / 128, DT = D / 16;
-    __shared__ ManyLds<D> lds;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -980,7 +980,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     i32x8 qh[KS], ql[KS];
     const float to_log2 = a.scale * kLog2e *
                           split_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, qh, ql);
-    Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
+    Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w);
     // this lane's operand rows: the t-th K operand's is 4 t keys further on, with its
     // pieces in the same order, and so the t-th V operand's, 16 t elements
     const int key = 16 * (c >> 2) + (c & 3);
@@ -990,51 +990,46 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     float m = kNegInf, l = 0.f;
     uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
-    if (j0 < k_hi) {
-        stage.pages(j0);
-        stage.load(0);
-        stage.pages(j0 + kTileKeys);
-    }
+    if (j0 < k_hi) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.arrive(buf);
-        if (jn < k_hi) {
-            stage.load(buf ^ 1);
-            stage.pages(jn + kTileKeys);
-        }
-        if (j0 >= wk.hi || jn <= wk.lo) continue;
-        f32x4 x[4] = {};
-        const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c + v_swap;
-        auto k_operand = [&](int i) {
-            const int t = i / KS, st = i % KS;
-            const uint4 u = kt[4 * t * 16 + (k_swap ^ 8 * st)], b = kt[4 * t * 16 + (k_swap ^ (8 * st + 4))];
-            return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-        };
-        run_ahead<4 * KS, kNarrowAhead>(k_operand, [&](int i, const i32x8 &k8) {
-            x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-            x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-        });
-        const int jg = j0 + 16 * g, ok = lds.ok[buf][g];
-        const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
-        uint32_t pw[8];
-        weigh(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], masked, ok, jg, jb, je, m, l, o, pw);
-        const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
-        auto multiply = [&](auto fix) {
-            run_ahead<DT, kNarrowAhead>([&](int t) { return vt[16 * 4 * t]; }, [&](int t, uint4 vw) {
-                fix(vw);
-                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.x, vw.y), p0, o[t], 0, 0, 0);
-                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.z, vw.w), p1, o[t], 0, 0, 0);
+        stage.ahead(j0);
+        if (j0 < wk.hi && jn > wk.lo) {
+            f32x4 x[4] = {};
+            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c + v_swap;
+            auto k_operand = [&](int i) {
+                const int t = i / KS, st = i % KS;
+                const uint4 u = kt[4 * t * 16 + (k_swap ^ 8 * st)], b = kt[4 * t * 16 + (k_swap ^ (8 * st + 4))];
+                return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+            };
+            run_ahead<4 * KS, kNarrowAhead>(k_operand, [&](int i, const i32x8 &k8) {
+                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
             });
-        };
-        if (masked) {
-            // values that no row of the wave sees may be anything: zero; NaN: find_nan
-            uint32_t keep[4];
+            const int jg = j0 + 16 * g;
+            const bool ok = lds.ok[buf][g] != 0;
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
+            uint32_t pw[8];
+            weigh(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], masked, ok, jg, jb, je, m, l, o, pw);
+            const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+            auto multiply = [&](auto fix) {
+                run_ahead<DT, kNarrowAhead>([&](int t) { return vt[16 * 4 * t]; }, [&](int t, uint4 vw) {
+                    fix(vw);
+                    o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.x, vw.y), p0, o[t], 0, 0, 0);
+                    o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(vw.z, vw.w), p1, o[t], 0, 0, 0);
+                });
+            };
+            if (masked) {
+                // values that no row of the wave sees may be anything: zero; NaN: find_nan
+                uint32_t keep[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
-            multiply([&](uint4 &w) { met_nan |= masked_values(w, keep); });
-        } else {
-            multiply([](uint4 &) {});
+                for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
+                multiply([&](uint4 &w) { met_nan |= masked_values(w, keep); });
+            } else {
+                multiply([](uint4 &) {});
+            }
         }
+        stage.next(j0, buf);
     }
 
     if (__any(met_nan != 0)) {
@@ -1081,7 +1076,8 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ __launch_bounds__(512, 2) void attention_few_kernel(AttentionArgs a, Division v) {
-    few_rows<D, 8, Take::kAll>(a, v, blockIdx.x);
+    __shared__ FewLds<D, 8> lds;
+    few_rows<D, 8, Take::kAll>(a, v, blockIdx.x, lds);
 }
 
 constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThreads; }
@@ -1089,10 +1085,15 @@ constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThr
 template <int D>
 __global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kernel(AttentionArgs a, Division few, Division many,
                                                                               int many_blocks) {
+    constexpr int W = mixed_threads(D) / 64;
+    __shared__ union {
+        FewLds<D, W> few;
+        ManyLds<D> many;
+    } lds;
     const int block = blockIdx.x;
-    if (block >= many_blocks) few_rows<D, mixed_threads(D) / 64, Take::kSmall>(a, few, block - many_blocks);
-    else if constexpr (D == 256) many_rows_narrow<D>(a, many, block, many_blocks);
-    else many_rows_wide<D>(a, many, block, many_blocks);
+    if (block >= many_blocks) few_rows<D, W, Take::kSmall>(a, few, block - many_blocks, lds.few);
+    else if constexpr (D == 256) many_rows_narrow<D>(a, many, block, many_blocks, lds.many);
+    else many_rows_wide<D>(a, many, block, many_blocks, lds.many);
 }
 
 // ---------------------------------------------------------------------------
