@@ -204,17 +204,16 @@ __device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)
     return 1.f / up;
 }
 
+// A factor for scores whose signs were turned where it is negative: not zero,
+// so that it keeps a masked score at -infinity.
+__device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0x1p-126f : factor < 0.f ? -factor : factor; }
+
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
 // row) become weights, packed to bf16 pairs with the values' scale in them;
 // the running maximum m, the lane's sum l and the sums o follow.
 template <int NT, int DT>
 __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool masked, bool seen_page, int jg, int jb, int je,
                                       float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
-    float mx = kNegInf;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[t][r] *= factor;
     if (masked) {
         // from the row's first and past its last key of these, none of a missing page
         const int from = seen_page ? jb - jg : 4 * NT, to = je - jg;
@@ -223,14 +222,27 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 if (4 * t + r < from || 4 * t + r >= to) x[t][r] = kNegInf;
-        // the scale of values that the row does not see may be anything
-        if (max(from, 0) >= min(to, 4 * NT)) vs = 0.f;
+        // scales of a page that the row does not see may be anything
+        if (max(from, 0) >= min(to, 4 * NT)) {
+            vs = 0.f;
+            factor = 1.f;
+        }
     }
+    if (__any(!(factor > 0.f))) {              // zero, below it or NaN
+        if (factor < 0.f)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (x[t][r] != kNegInf) x[t][r] = -x[t][r];
+        factor = usable(factor);
+    }
+    float mx = kNegInf;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
-    mx = max_over32(max_over16(mx));
+    mx = max_over32(max_over16(mx * factor));
     if (__any(mx > m)) {
         const float m_new = fmaxf(m, mx);
         const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -245,7 +257,7 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
         float e[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            e[r] = __builtin_amdgcn_exp2f(x[t][r] - at);
+            e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], factor, -at));
             l += e[r];
         }
         pw[2 * t] = pack_bf16x2(e[0] * vs, e[1] * vs);
@@ -669,19 +681,23 @@ struct Staging {
     const AttentionArgs &a;
     ManyLds<D> &lds;
     const int32_t *bt;
-    int k_hi, shift, hk;
+    int k_hi, shift, hk, wave;
     uint32_t pitch;                // bytes of a page, all kv heads
     // a tile begins at a multiple of 64 keys, so a piece's place in its page
     // stays the same
     uint32_t k_off[NL], v_off;
-    int idk[NL], idv;              // pages of the tile to load next, -1: none
+    // the block table's entry for granule tid % 4 of the tile to load next, as it
+    // came (looking at it here would wait for it and all loads before it)
+    int entry, tile;
     uint4 kr[NL], vr[NL];
     float s_ks, s_vs;              // of granule tid % 4, whose page idv is
     int s_ok;
 
-    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w)
+    static_assert(64 / PPK <= 16, "");
+
+    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
         : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
-          hk(w.hk), pitch((uint32_t)a_.num_kv_heads * a_.page * D), s_ks(0.f), s_vs(0.f), s_ok(0) {
+          hk(w.hk), wave(wave_), pitch((uint32_t)a_.num_kv_heads * a_.page * D), entry(-1), tile(0), s_ks(0.f), s_vs(0.f), s_ok(0) {
         const int tid = threadIdx.x, in_page = a.page - 1;
 #pragma unroll
         for (int i = 0; i < NL; ++i) k_off[i] = (hk * a.page + (i * KEYS + tid / PPK & in_page)) * D + 16 * (tid % PPK);
@@ -693,24 +709,27 @@ struct Staging {
         return (unsigned)id < (unsigned)a.num_pages ? id : -1;
     }
     __device__ __forceinline__ void pages(int j0) {
-        // (a key past the end has no page, but a piece of its granule is loaded with
-        // the keys before it: the granule's first key decides)
-#pragma unroll
-        for (int i = 0; i < NL; ++i) idk[i] = page_at(j0 + (i * KEYS + threadIdx.x / PPK & ~15));
-        idv = page_at(j0 + 16 * (threadIdx.x & 3));
+        tile = j0;
+        entry = bt[min((j0 + 16 * (int)(threadIdx.x & 3)) >> shift, a.max_pages - 1)];
     }
     __device__ __forceinline__ void load() {
+        const int j = tile + 16 * (threadIdx.x & 3);
+        const int own = j < k_hi && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
 #pragma unroll
-        for (int i = 0; i < NL; ++i)
-            kr[i] = *reinterpret_cast<const uint4 *>(a.k_cache + ((uint64_t)max(idk[i], 0) * pitch + k_off[i]));
-        const uint8_t *v = a.v_cache + ((uint64_t)max(idv, 0) * pitch + v_off);
+        for (int i = 0; i < NL; ++i) {
+            // a wave's keys lie in one granule: a scalar address
+            const int granule = (i * KEYS + wave * (64 / PPK)) >> 4, page = __builtin_amdgcn_readlane(own, granule);
+            const uint8_t *k = a.k_cache + (uint64_t)max(page, 0) * pitch;
+            kr[i] = *reinterpret_cast<const uint4 *>(k + k_off[i]);
+        }
+        const uint8_t *v = a.v_cache + ((uint64_t)max(own, 0) * pitch + v_off);
 #pragma unroll
         for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const uint4 *>(v + i * (THREADS / 4) * a.page);
         if (threadIdx.x < 4) {
-            const long long ph = (long long)max(idv, 0) * a.num_kv_heads + hk;
+            const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk;
             s_ks = a.k_scale[ph];
             s_vs = a.v_scale[ph];
-            s_ok = idv >= 0;
+            s_ok = own >= 0;
         }
     }
     __device__ __forceinline__ void put(int buf) {
@@ -812,7 +831,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             }
     }
 
-    Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w);
+    Staging<D, kWideThreads, k_piece<D>> stage(a, lds, w, wave);
     // this lane's operand rows: the t-th K operand's is 16 t keys further on, with
     // its pieces in the same order, and so the t-th V operand's, 32 t elements
     const int key = 32 * (c >> 2 & 1) + 4 * (c >> 3) + (c & 3);
@@ -844,23 +863,30 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                         x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x, 0, 0, 0, 0, 0, 0);
                     });
                 const bool ok = ok01[t];
-                const float factor = to_log2 * lds.ks[buf][2 * h2 + t];
-                float mx = kNegInf, vs = lds.vs[buf][2 * h2 + t];
+                float mx = kNegInf, factor = to_log2 * lds.ks[buf][2 * h2 + t], vs = lds.vs[buf][2 * h2 + t];
                 const int jg = j0 + 32 * h2 + 16 * t;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] *= factor;
                 if (masked) {
                     // from the row's first and past its last key of these 16, none of a missing page
                     const int from = ok ? jb - jg : 16, to = je - jg;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         if (r < from || r >= to) x[r] = kNegInf;
-                    // the scale of values that the row does not see may be anything
-                    if (max(from, 0) >= min(to, 16)) vs = 0.f;
+                    // scales of a page that the row does not see may be anything
+                    if (max(from, 0) >= min(to, 16)) {
+                        vs = 0.f;
+                        factor = 1.f;
+                    }
+                }
+                if (__any(!(factor > 0.f))) {              // zero, below it or NaN
+                    if (factor < 0.f)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (x[r] != kNegInf) x[r] = -x[r];
+                    factor = usable(factor);
                 }
 #pragma unroll
                 for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[r]);
-                mx = max_over32(mx);
+                mx = max_over32(mx * factor);
                 if (__any(mx > m)) {
                     const float m_new = fmaxf(m, mx);
                     const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -873,7 +899,8 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 uint32_t pw[8];
 #pragma unroll
                 for (int r = 0; r < 16; r += 2) {
-                    const float e0 = __builtin_amdgcn_exp2f(x[r] - at), e1 = __builtin_amdgcn_exp2f(x[r + 1] - at);
+                    const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], factor, -at));
+                    const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r + 1], factor, -at));
                     l += e0 + e1;
                     pw[r / 2] = pack_bf16x2(e0 * vs, e1 * vs);
                 }
@@ -954,8 +981,9 @@ constexpr int kNarrowAhead = 3;
 // 16 lanes read the same piece of keys 16 (i / 4) + 4 t + i % 4
 template <int D>
 __device__ __forceinline__ int k_piece_narrow(int key, int p) {
-    static_assert(D == 256, "16 pieces per key");
-    return key * 16 + (p ^ ((key & 3) | (key >> 4 & 3) << 2));
+    static_assert(D >= 128, "");
+    constexpr int shift = D == 256 ? 0 : 1;
+    return key * (D / 16) + (p ^ (((key & 3) | (key >> 4 & 3) << 2) >> shift));
 }
 
 template <int D>
@@ -980,11 +1008,11 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     i32x8 qh[KS], ql[KS];
     const float to_log2 = a.scale * kLog2e *
                           split_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, qh, ql);
-    Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w);
+    Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
     // this lane's operand rows: the t-th K operand's is 4 t keys further on, with its
     // pieces in the same order, and so the t-th V operand's, 16 t elements
     const int key = 16 * (c >> 2) + (c & 3);
-    const int k_row = key * 16, k_swap = k_piece_narrow<D>(key, g) - k_row, v_swap = v_piece(c, g) - 4 * c;
+    const int k_row = key * (D / 16), k_swap = k_piece_narrow<D>(key, g) - k_row, v_swap = v_piece(c, g) - 4 * c;
 
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
@@ -999,7 +1027,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c + v_swap;
             auto k_operand = [&](int i) {
                 const int t = i / KS, st = i % KS;
-                const uint4 u = kt[4 * t * 16 + (k_swap ^ 8 * st)], b = kt[4 * t * 16 + (k_swap ^ (8 * st + 4))];
+                const uint4 u = kt[4 * t * (D / 16) + (k_swap ^ 8 * st)], b = kt[4 * t * (D / 16) + (k_swap ^ (8 * st + 4))];
                 return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
             };
             run_ahead<4 * KS, kNarrowAhead>(k_operand, [&](int i, const i32x8 &k8) {
