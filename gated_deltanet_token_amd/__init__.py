@@ -162,16 +162,24 @@ def _stream(stream):
 
 def _rows(t, name):
     """Token stride (elements) of a 2-D tensor with a contiguous last dim."""
-    if t.dim() != 2 or (t.size(1) > 1 and t.stride(1) != 1):
+    return _row_stride(t.shape, t.stride(), name)
+
+
+def _row_stride(shape, strides, name):
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError("%s must be 2-D with contiguous rows" % name)
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1))
+    return strides[0] if shape[0] > 1 else max(strides[0], shape[1])
 
 
 def _heads(t, name):
     """Token stride of a [T][H][d] tensor whose heads are packed."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.size(1) > 1 and t.stride(1) != t.size(2)):
+    return _head_stride(t.shape, t.stride(), name)
+
+
+def _head_stride(shape, strides, name):
+    if len(shape) != 3 or strides[2] != 1 or (strides[1] != shape[2] and shape[1] > 1):
         raise ValueError("%s must be [T][H][d] with packed heads" % name)
-    return t.stride(0) if t.size(0) > 1 else max(t.stride(0), t.size(1) * t.size(2))
+    return strides[0] if shape[0] > 1 else max(strides[0], shape[1] * shape[2])
 
 
 def _dtype(t, dt, name):
@@ -527,28 +535,39 @@ def gdn_chunk_rule_and_fused_decode_noalloc(q, k, v, g, beta, state_indices, o, 
 # the attention layers' operators and the block norms
 # ---------------------------------------------------------------------------
 
+# Host time counts here: a decode step's calls take the GPU a few microseconds.
+# So each tensor's shape, strides and device are asked for once.
+
 def _vector(t, dt, n, name):
     """A packed 1-D operand of n entries."""
     if t.dtype != dt:
         raise TypeError("%s must be %s, got %s" % (name, dt, t.dtype))
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be packed with %d entries, got shape %s" % (name, n, tuple(t.shape)))
     return t.data_ptr()
 
 
-def _current(*named):
-    """Every (name, tensor or None) on the current GPU."""
+def _on_current(names, *tensors):
+    """Every tensor (None: not given) on the current GPU, whose number is
+    returned."""
     cur = None
-    for name, t in named:
+    for i, t in enumerate(tensors):
         if t is None:
             continue
         at = t.get_device()
-        if at < 0:
-            raise ValueError("%s must be a GPU tensor, got one on %s" % (name, t.device))
-        if cur is None:
-            cur = torch.cuda.current_device()
         if at != cur:
-            raise ValueError("%s is on cuda:%d but the current device is cuda:%d" % (name, at, cur))
+            name = names.split()[i]
+            if at < 0:
+                raise ValueError("%s must be a GPU tensor, got one on %s" % (name, t.device))
+            if at != torch.cuda.current_device():
+                raise ValueError("%s is on cuda:%d but the current device is cuda:%d"
+                                 % (name, at, torch.cuda.current_device()))
+            cur = at
+    return cur
+
+
+def _stream_on(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def gdn_build_step_tables(context_lens, query_lens, free_pages, num_free, block_table, page_size, query_start_loc,
@@ -581,11 +600,10 @@ def gdn_build_step_tables(context_lens, query_lens, free_pages, num_free, block_
             _vector(query_start_loc, i32, S + 1, "query_start_loc"), _vector(seq_lens, i32, S, "seq_lens"),
             _vector(positions, i32, T, "positions"), _vector(slot_mapping, torch.int64, T, "slot_mapping"), T,
             chunks.data_ptr() if n else None, n, _vector(counts, i32, 4, "counts"))
-    _current(("context_lens", context_lens), ("query_lens", query_lens), ("free_pages", free_pages),
-             ("num_free", num_free), ("block_table", block_table), ("query_start_loc", query_start_loc),
-             ("seq_lens", seq_lens), ("positions", positions), ("slot_mapping", slot_mapping), ("counts", counts),
-             ("chunks", chunks))
-    _check(lib.gdn_build_step_tables(*args, _stream(stream)), "gdn_build_step_tables")
+    dev = _on_current("context_lens query_lens free_pages num_free block_table query_start_loc seq_lens positions "
+                      "slot_mapping counts chunks", context_lens, query_lens, free_pages, num_free, block_table,
+                      query_start_loc, seq_lens, positions, slot_mapping, counts, chunks)
+    _check(lib.gdn_build_step_tables(*args, _stream_on(stream, dev)), "gdn_build_step_tables")
 
 
 def gdn_rope_frequencies(rotary_dim, base, scaling="plain", factor=1.0, original_context=0.0, beta_fast=32.0,
@@ -625,9 +643,10 @@ def _bf16_heads(t, T, H, d, name):
     """Token stride of a bf16 [T][H][d] operand with packed heads."""
     if t.dtype != torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.shape != (T, H, d):
-        raise ValueError("%s must have shape %s, got %s" % (name, (T, H, d), tuple(t.shape)))
-    return _heads(t, name)
+    shape = (T, H, d)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    return _head_stride(shape, t.stride(), name)
 
 
 def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale,
@@ -661,10 +680,9 @@ def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_
             _vector(frequencies, torch.float64, rot // 2, "frequencies") if rot else None, rot, 1 if interleaved else 0,
             rope_scale, _ptr(q_out), os_, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             n, page, T, hq, hk, d)
-    _current(("k", k), ("v", v), ("positions", positions), ("slot_mapping", slot_mapping), ("frequencies", frequencies),
-             ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("q", q),
-             ("q_out", q_out))
-    _check(lib.gdn_rope_append_kv8(*args, _stream(stream)), "gdn_rope_append_kv8")
+    dev = _on_current("k v positions slot_mapping frequencies k_cache v_cache k_scale v_scale q q_out", k, v, positions,
+                      slot_mapping, frequencies, k_cache, v_cache, k_scale, v_scale, q, q_out)
+    _check(lib.gdn_rope_append_kv8(*args, _stream_on(stream, dev)), "gdn_rope_append_kv8")
 
 
 def gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -700,14 +718,13 @@ def gdn_paged_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
             _vector(seq_lens, torch.int32, S, "seq_lens"),
             _vector(query_start_loc, torch.int32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
             d, scale, 1 if causal else 0, window)
-    _current(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-             ("block_table", block_table), ("seq_lens", seq_lens), ("query_start_loc", query_start_loc), ("o", o),
-             ("workspace", workspace))
+    dev = _on_current("q k_cache v_cache k_scale v_scale block_table seq_lens query_start_loc o workspace", q, k_cache,
+                      v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o, workspace)
     need = lib.gdn_paged_attention_kv8_workspace_size(T, S, hq, hk, d, max_seq_len)
     if need or workspace is not None:
         workspace = _workspace(workspace, need, q.device, stream)
     _check(lib.gdn_paged_attention_kv8(*args, _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                       _stream(stream)), "gdn_paged_attention_kv8")
+                                       _stream_on(stream, dev)), "gdn_paged_attention_kv8")
 
 
 def gdn_gated_rms_norm(x, weight, y, gate=None, eps=1e-6, weight_offset=0.0, stream=None):
@@ -719,9 +736,9 @@ def gdn_gated_rms_norm(x, weight, y, gate=None, eps=1e-6, weight_offset=0.0, str
     xs, ys = _bf16_heads(x, T, H, d, "x"), _bf16_heads(y, T, H, d, "y")
     gs = 0 if gate is None else _bf16_heads(gate, T, H, d, "gate")
     w = _vector(weight, torch.bfloat16, d, "weight")
-    _current(("x", x), ("weight", weight), ("y", y), ("gate", gate))
+    dev = _on_current("x weight y gate", x, weight, y, gate)
     _check(lib.gdn_gated_rms_norm(x.data_ptr(), xs, _ptr(gate), gs, w, y.data_ptr(), ys, T, H, d, eps, weight_offset,
-                                  _stream(stream)), "gdn_gated_rms_norm")
+                                  _stream_on(stream, dev)), "gdn_gated_rms_norm")
 
 
 def gdn_residual_rms_norm(x, residual, weight, new_residual, y, post_weight=None, gate=None, residual_scale=1.0,
@@ -743,11 +760,12 @@ def gdn_residual_rms_norm(x, residual, weight, new_residual, y, post_weight=None
             raise TypeError("%s must be %s, got %s" % (name, bf16, t.dtype))
         if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        strides.append(_rows(t, name))
+        strides.append(_row_stride(shape, t.stride(), name))
     w = _vector(weight, bf16, D, "weight")
     pw = None if post_weight is None else _vector(post_weight, bf16, D, "post_weight")
-    _current(("x", x), ("residual", residual), ("weight", weight), ("new_residual", new_residual), ("y", y),
-             ("post_weight", post_weight), ("gate", gate))
+    dev = _on_current("x residual weight new_residual y post_weight gate", x, residual, weight, new_residual, y,
+                      post_weight, gate)
     _check(lib.gdn_residual_rms_norm(x.data_ptr(), strides[0], residual.data_ptr(), strides[1], pw, _ptr(gate),
                                      strides[2], w, new_residual.data_ptr(), strides[3], y.data_ptr(), strides[4], R, D,
-                                     residual_scale, eps, weight_offset, _stream(stream)), "gdn_residual_rms_norm")
+                                     residual_scale, eps, weight_offset, _stream_on(stream, dev)),
+           "gdn_residual_rms_norm")
