@@ -670,7 +670,11 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * no influence whatever their codes and scales hold, NaN included; cache
  * bytes past L are free to hold anything.
  *
- * Products, softmax statistics and sums are fp32; o is rounded to bf16.
+ * Scores are products of the cache's codes with q in two 8-bit parts (exact
+ * for elements of at least 2^-10 of their head's largest, within 2^-18 of that
+ * largest for smaller ones), summed in fp32; softmax statistics and sums are
+ * fp32.  Weights are rounded to bf16 for their products with the values, and o
+ * to bf16.  Results do not change from call to call (no atomics).
  *
  *   q            bf16, token t head h at q + t*q_stride + h*head_dim
  *   block_table  int32 [num_seqs][block_table_stride], max_pages entries used

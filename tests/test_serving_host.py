@@ -114,6 +114,12 @@ def test_rope_append_refusals(kw, code):
     assert gdn.lib.gdn_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(ks=1 << 24), dict(vs=1 << 24), dict(ks=(1 << 24) + 8, vs=(1 << 24) + 8)])
+def test_rope_append_refuses_far_strides(kw):
+    # a page's rows are addressed with 32-bit offsets
+    assert rope(**kw) == UNS and b"2^24" in gdn.lib.gdn_last_error()
+
+
 def attn(**kw):
     a = dict(q=P[0], qs=4096, kc=P[1], vc=P[2], ksc=P[3], vsc=P[4], n=64, page=16, bt=P[5], bts=32, cols=32, seq=P[6], qsl=P[7],
              longest=500, o=P[8], os=4096, S=2, T=8, HQ=16, HK=4, D=256, scale=1.0, causal=1, window=0, ws=P[9], wsn=1 << 28)
