@@ -208,6 +208,13 @@ __device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)
 // so that it keeps a masked score at -infinity.
 __device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0x1p-126f : factor < 0.f ? -factor : factor; }
 
+// The sums are brought to a row's new maximum only where that is more than this
+// above the maximum m that they are relative to (in units of log2): weights up
+// to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
+// row of a wave, hardly any such a one.  None is let through where the values'
+// scale is so large that weight times scale or their sum could pass fp32's end.
+__device__ __forceinline__ float slack(float vs) { return fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
+
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
 // row) become weights, packed to bf16 pairs with the values' scale in them;
 // the running maximum m, the lane's sum l and the sums o follow.
@@ -243,7 +250,7 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
 #pragma unroll
         for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
     mx = max_over32(max_over16(mx * factor));
-    if (__any(mx > m)) {
+    if (__any(mx > m + slack(vs))) {
         const float m_new = fmaxf(m, mx);
         const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
         m = m_new;
@@ -887,7 +894,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 #pragma unroll
                 for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[r]);
                 mx = max_over32(mx * factor);
-                if (__any(mx > m)) {
+                if (__any(mx > m + slack(vs))) {
                     const float m_new = fmaxf(m, mx);
                     const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
                     m = m_new;
