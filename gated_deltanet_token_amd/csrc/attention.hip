@@ -589,8 +589,10 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // 32 h .. 32 h + 31 of the tile, x[a][r] being key 32 h + 16 a + r.  For that,
 // row i of the a-th K operand is key 32 (i / 4 % 2) + 16 a + 4 (i / 8) + i % 4.
 // LDS rows are cut into 16-byte pieces, piece p of a row kept at p ^ (a few
-// bits of the row's number) so that 16 lanes that read the same piece of their
-// rows find it in 16 different places of the 256 bytes that the banks span.
+// bits of the row's number) so that the 16 lanes that are served together find
+// theirs in 16 different places of the 256 bytes that the banks span.  Those are
+// lanes 0-3, 12-15 and 20-27 of a half-wave, or the other 16 of it (measured: a
+// read takes 4 cycles, and 5 with two of these lanes at the same banks).
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 128;
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
@@ -672,7 +674,7 @@ __device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const Many
 }
 
 // the LDS place of piece p of element row d of a tile's values
-__device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (d >> 2 & 3)); }
+__device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (-(d >> 2) & 3)); }
 
 // Staging of a workgroup of THREADS threads: the next tile's pieces are loaded
 // into registers before the work on this one and put into the other LDS buffer
