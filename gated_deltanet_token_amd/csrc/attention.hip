@@ -1261,14 +1261,22 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // How a call is split.  With at most a token per request on average the
 // few-rows kernel takes everything; else it takes the requests of up to
 // kSmallRows rows, and the many-rows kernel the others (16 rows of a wave cost
-// it as much as 32, and it reads a key once for 128 rows).  Keys are split
-// until there is a workgroup for every CU, each with at least kMinChunk keys
-// (joining costs a launch: 32 decode rows of 1,100 keys take 23.0 us in one part
-// and 23.8 in two; five of 40,000 to 131,000 take 206 us in parts for 240 CUs and
-// 321 for 120).
+// it as much as 32, and it reads a key once for 128 rows).
+//
+// Keys are split until there is a workgroup for every CU, two of the wide
+// kernel's, which fit a CU together.  A part has at least kMinChunk keys where
+// eight waves share them (joining costs a launch: 32 decode rows of 1,100 keys take
+// 23.0 us in one part and 23.8 in two; five of 40,000 to 131,000 take 206 us in
+// parts for 240 CUs and 321 for 120), and kManyChunk where each wave works on
+// them all: 300 tokens of three prompts of up to 1,100 tokens, 16/4 heads of 256,
+// take 31 us with 256, 38 with 512, 33 with 128 and 51 with 1,024; of 128, 27, 31,
+// 32 and 37.  (More workgroups than fit at once, to even out lengths: a mixed
+// step of 2,048 tokens took 100 us with two parts and 67 with one, as partial
+// sums cost more than the long rows' wait.)
 // ---------------------------------------------------------------------------
 constexpr int kCUs = 256;
 constexpr int kMinChunk = 1024;
+constexpr int kManyChunk = 256;
 
 struct Launch {
     long long units;        // (row tile, kv head) pairs, upper bound; 0: none
@@ -1278,11 +1286,12 @@ struct Launch {
 };
 
 // `busy`: row tiles that hold rows, as far as the host can tell
-static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len) {
+static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len, int aim,
+                     int min_chunk) {
     Launch p{tiles * kv_heads, rows, 0x40000000, 1, 0};
     busy *= kv_heads;
-    long long want = busy > 0 ? kCUs / busy : 1;
-    const long long most = max_seq_len / kMinChunk;
+    long long want = busy > 0 ? aim / busy : 1;
+    const long long most = max_seq_len / min_chunk;
     if (want > most) want = most;
     if (want > 1) {
         const long long chunk = ((max_seq_len + want - 1) / want + kTileKeys - 1) / kTileKeys * kTileKeys;
@@ -1306,12 +1315,13 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
     if (T <= S) {
         p.few_takes = Take::kAll;
         const long long full = T * G / kTileRows;
-        p.few = divide(full + S, full > T ? full : T, T * q_heads, kv_heads, d, max_seq_len);
+        p.few = divide(full + S, full > T ? full : T, T * q_heads, kv_heads, d, max_seq_len, kCUs, kMinChunk);
     } else {
         p.few_takes = Take::kSmall;
-        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len);
+        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs, kMinChunk);
         const long long full = T * G / kManyRows;
-        p.many = divide(full + S, full > 1 ? full : 1, T * q_heads, kv_heads, d, max_seq_len);
+        p.many = divide(full + S, full > 1 ? full : 1, T * q_heads, kv_heads, d, max_seq_len, d == 256 ? kCUs : 2 * kCUs,
+                        kManyChunk);
     }
     return p;
 }
