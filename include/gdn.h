@@ -673,8 +673,11 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * Scores are products of the cache's codes with q in two 8-bit parts (exact
  * for elements of at least 2^-10 of their head's largest, within 2^-18 of that
  * largest for smaller ones), summed in fp32; softmax statistics and sums are
- * fp32.  Weights are rounded to bf16 for their products with the values, and o
- * to bf16.  Results do not change from call to call (no atomics).
+ * fp32.  In its product with a value a weight is off by at most 2^-8 of itself
+ * (bf16) or, with the values' scale in it, by 2^-22 of the largest among 32
+ * neighbouring keys; o is rounded to bf16.  A token that sees a key of a page
+ * whose v_scale is infinite or NaN gets infinite or NaN elements there.
+ * Results do not change from call to call (no atomics).
  *
  *   q            bf16, token t head h at q + t*q_stride + h*head_dim
  *   block_table  int32 [num_seqs][block_table_stride], max_pages entries used

@@ -314,3 +314,31 @@ def test_on_a_stream_of_its_own_and_in_a_graph():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, o)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_value_scales_over_their_whole_range(d):
+    """Every page's scale another one from 2^-100 to 2^100, not powers of two, some zero or
+    negative: none passes fp32's end in a weight, none's rounding reaches another row."""
+    c = Case(19, [(300, 70), (90, 90), (500, 1), (64, 40)], 8, 2, d, 16, spread=2.0)
+    c.vs = (2.0 ** c.r.integers(-100, 101, c.vs.shape) * c.r.uniform(1, 2, c.vs.shape)).astype(np.float32)
+    c.vs[::7] = 0
+    c.vs[1::5] *= -1
+    c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("step", [1.0, 7.5, 8.5, 200.0])
+def test_scores_that_rise_or_fall_with_the_key(d, step):
+    """The running maximum moves by `step` powers of two per 16 keys, up in one kv head and
+    down in the other: sums follow it at once, late, or not at all."""
+    c = Case(20, [(200, 100), (330, 1), (150, 33)], 4, 2, d, 16, spread=0.0)
+    c.q[...] = 0
+    c.q[:, :, 0] = 1.0
+    c.kq[...] = 0
+    c.kq[:, :, :, 0] = 256.0
+    c.scale = 2.0 ** -8 * np.log(2.0)
+    for s in range(len(c.seq)):
+        for i in range(-(-int(c.seq[s]) // 16)):
+            c.ks[c.table[s, i]] = [step * (i + 1), step * (40 - i)]
+    c.check()
