@@ -1287,7 +1287,7 @@ struct Launch {
 
 // `busy`: row tiles that hold rows, as far as the host can tell
 static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len, int aim,
-                     int min_chunk) {
+                     long long min_chunk) {
     Launch p{tiles * kv_heads, rows, 0x40000000, 1, 0};
     busy *= kv_heads;
     long long want = busy > 0 ? aim / busy : 1;
@@ -1318,10 +1318,14 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
         p.few = divide(full + S, full > T ? full : T, T * q_heads, kv_heads, d, max_seq_len, kCUs, kMinChunk);
     } else {
         p.few_takes = Take::kSmall;
-        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs, kMinChunk);
-        const long long full = T * G / kManyRows;
-        p.many = divide(full + S, full > 1 ? full : 1, T * q_heads, kv_heads, d, max_seq_len, d == 256 ? kCUs : 2 * kCUs,
-                        kManyChunk);
+        const long long full = T * G / kManyRows, busy = full > 1 ? full : 1, room = d == 256 ? kCUs : 2 * kCUs;
+        // the small requests' parts need not be shorter than what the other
+        // workgroups take anyway: at least this many keys one after the other, where
+        // a small request's waves share theirs
+        const long long anyway = busy * kv_heads * (T / S) / 2 / room * (mixed_threads(d) / 64);
+        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
+                       anyway > kMinChunk ? anyway : kMinChunk);
+        p.many = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
     }
     return p;
 }
