@@ -213,16 +213,20 @@ __device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0
 // The sums are brought to a row's new maximum only where that is more than this
 // above the maximum m that they are relative to (in units of log2): weights up
 // to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
-// row of a wave, hardly any such a one.  None is let through where the values'
-// scale is so large that weight times scale or their sum could pass fp32's end.
-__device__ __forceinline__ float slack(float vs) { return fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
+// row of a wave, hardly any such a one (a prompt of 8,192 tokens, heads of 128: 589
+// us with none, 573).  None is let through where the values' scale is so large
+// that weight times scale or their sum could pass fp32's end, nor in a wave's first
+// kLateKeys keys: of few keys the heaviest often makes up the sum, and its weight
+// of 1 is exact.
+constexpr int kLateKeys = 256;
+__device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
 // row) are masked, and the running maximum m, the lane's sum l and the sums o
 // follow.  Returns the lane's own maximum.
 template <int NT, int DT>
-__device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs, bool masked, bool seen_page, int jg, int jb,
-                                        int je, float &m, float &l, f32x4 (&o)[DT]) {
+__device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs, bool late, bool masked, bool seen_page, int jg,
+                                        int jb, int je, float &m, float &l, f32x4 (&o)[DT]) {
     if (masked) {
         // from the row's first and past its last key of these, none of a missing page
         const int from = seen_page ? jb - jg : 4 * NT, to = je - jg;
@@ -253,7 +257,7 @@ __device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs
         for (int r = 0; r < 4; ++r) own = fmaxf(own, x[t][r]);
     own *= factor;
     const float mx = max_over32(max_over16(own));
-    if (__any(mx > m + slack(vs))) {
+    if (__any(mx > m + slack(vs, late))) {
         const float m_new = fmaxf(m, mx);
         const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
         m = m_new;
@@ -266,9 +270,9 @@ __device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs
 
 // The scores as weights, packed to bf16 pairs with the values' scale in them.
 template <int NT, int DT>
-__device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool masked, bool seen_page, int jg, int jb, int je,
-                                      float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
-    settle(x, factor, vs, masked, seen_page, jg, jb, je, m, l, o);
+__device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool late, bool masked, bool seen_page, int jg, int jb,
+                                      int je, float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
+    settle(x, factor, vs, late, masked, seen_page, jg, jb, je, m, l, o);
     const float at = m == kNegInf ? 0.f : m;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -291,9 +295,9 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
 // 32), and so do 2 and 3; groups 0 and 1 hold those of the first parts and groups
 // 2 and 3 those of the second ones (measured with one-hot operands).
 template <int DT>
-__device__ __forceinline__ int weigh8(f32x4 (&x)[4], float factor, float vs, bool masked, bool seen_page, int jg, int jb, int je,
-                                      float &m, float &l, f32x4 (&o)[DT], i32x8 &p) {
-    const float own = settle(x, factor, vs, masked, seen_page, jg, jb, je, m, l, o);
+__device__ __forceinline__ int weigh8(f32x4 (&x)[4], float factor, float vs, bool late, bool masked, bool seen_page, int jg, int jb,
+                                      int je, float &m, float &l, f32x4 (&o)[DT], i32x8 &p) {
+    const float own = settle(x, factor, vs, late, masked, seen_page, jg, jb, je, m, l, o);
     const float at = m == kNegInf ? 0.f : m;
     // weights are below 2^(floor(own - at) + 1), the scale's fraction below 1: their
     // product goes to below 2^8
@@ -547,7 +551,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         const bool seen_page = good(pv);
         const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + TK > min(x1, k_hi);
         uint32_t pw[2 * NT];
-        weigh(x, to_log2 * ks, vs, masked, seen_page, jg, jb, je, m, l, o, pw);
+        weigh(x, to_log2 * ks, vs, j0 - k_lo >= kLateKeys, masked, seen_page, jg, jb, je, m, l, o, pw);
         if (masked) {
             // values that no row sees may be anything: zero; NaN: find_nan
 #pragma unroll
@@ -914,7 +918,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
         stage.ahead(j0);
         if (j0 < wk.hi && jn > wk.lo) {
             const bool ok01[2] = {lds.ok[buf][2 * h2] != 0, lds.ok[buf][2 * h2 + 1] != 0};
-            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok01[0] && ok01[1]));
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok01[0] && ok01[1])), late = j0 - k_lo >= kLateKeys;
             const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c;
             // half of the tile at a time: keys 16 t .. 16 t + 15 of each of its halves
 #pragma unroll
@@ -955,7 +959,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 #pragma unroll
                 for (int r = 0; r < 16; ++r) mx = fmaxf(mx, x[r]);
                 mx = max_over32(mx * factor);
-                if (__any(mx > m + slack(vs))) {
+                if (__any(mx > m + slack(vs, late))) {
                     const float m_new = fmaxf(m, mx);
                     const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
                     m = m_new;
@@ -1110,7 +1114,8 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
             // keys 16 g ... 16 g + 15 of the values' operands twice: for the weights' two parts
             i32x8 p;
-            const int p_scale = weigh8(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], masked, ok, jg, jb, je, m, l, o, p);
+            const int p_scale = weigh8(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], j0 - k_lo >= kLateKeys, masked, ok,
+                                           jg, jb, je, m, l, o, p);
             auto multiply = [&](int t, const uint4 &u, const uint4 &b) {
                 const i32x8 v8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
                 o[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8, p, o[t], 0, 0, 0, 127, 0, p_scale);
