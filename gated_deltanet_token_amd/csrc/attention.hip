@@ -641,7 +641,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the matrix cores and the exponentials: tiles of 64 keys and values pass
 // through the LDS once for all four waves, the next one on its way from HBM
 // to registers meanwhile, with one barrier per tile between two buffers.
-// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 572 us, 960 TFLOP/s (4 D
+// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 575 us, 956 TFLOP/s (4 D
 // per row and key it sees).  Vector and matrix instructions hardly overlap here: an
 // operation takes 2.4 cycles of a SIMD, an exponential 8, a pair of values'
 // conversion 4, a matrix product 32 of which it hides 10; their sum over a tile is
