@@ -326,10 +326,10 @@ __device__ __forceinline__ int weigh8(f32x4 (&x)[4], float factor, float vs, boo
     return (int)(threadIdx.x & 16 ? r[1] : r[0]) - (threadIdx.x & 32 ? 4 : 0);
 }
 
-// A tile that some of a wave's rows see and others do not cannot pass NaN codes
-// of its values through the matrix cores: they would reach all rows.  They go
-// in as zeros there, and this pass, for a wave that met any, finds the sums
-// that they belong to: bit i of `bits` for the lane's sum i, element `element(i)`
+// A tile that some of the rows see and others do not cannot pass NaN codes of
+// its values through the matrix cores: they would reach all rows.  They go in
+// as zeros there, and this pass, where any was met, finds the sums that they
+// belong to: bit i of `bits` for the lane's sum i, element `element(i)`
 // of the row that sees [jb, je).  `late(j0)`: whether the tile at j0 went in so.
 template <int N, typename Late, typename Element, typename Page>
 __device__ __forceinline__ void find_nan(const AttentionArgs &a, int hk, int j0, int end, int step, int tile, int jb, int je,
@@ -659,7 +659,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // ---------------------------------------------------------------------------
 constexpr int kManyRows = 128;
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
-constexpr int kWideAhead = 2;
+constexpr int kWideAhead = 3;
 
 // use(i, read(i)) for i < N, each read A steps before its use and, left alone
 // by the compiler, not earlier: it would read until it runs out of registers.
@@ -682,6 +682,7 @@ struct ManyLds {
     // of the tile's four granules of 16 keys: scales, and whether there is a page
     float ks[2][4], vs[2][4];
     int ok[2][4];
+    int met_nan;
 };
 
 // A workgroup's share of a many-rows launch.
@@ -762,14 +763,20 @@ struct Staging {
     // came (looking at it here would wait for it and all loads before it)
     int entry, tile;
     uint4 kr[NL], vr[NL];
-    float s_ks, s_vs;              // of granule tid % 4, whose page idv is
-    int s_ok;
+    int own;                       // the page of granule tid % 4 of these
+    float s_ks, s_vs;              // its scales
+    int k_lo, all0, all1;          // the first key; the keys that all rows see
+    uint32_t met_nan;
 
     static_assert(64 / PPK <= 16, "");
 
     __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
         : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
-          hk(w.hk), wave(wave_), pitch((uint32_t)a_.num_kv_heads * a_.page * D), entry(-1), tile(0), s_ks(0.f), s_vs(0.f), s_ok(0) {
+          hk(w.hk), wave(wave_), pitch((uint32_t)a_.num_kv_heads * a_.page * D), entry(-1), tile(0), own(-1), s_ks(0.f), s_vs(0.f), k_lo(w.k_lo),
+          met_nan(0) {
+        const WaveKeys all = wave_keys(a, w, w.row0, kManyRows);
+        all0 = all.all0;
+        all1 = all.all1;
         const int tid = threadIdx.x, in_page = a.page - 1;
 #pragma unroll
         for (int i = 0; i < NL; ++i) k_off[i] = (hk * a.page + (i * KEYS + tid / PPK & in_page)) * D + 16 * (tid % PPK);
@@ -786,7 +793,7 @@ struct Staging {
     }
     __device__ __forceinline__ void load() {
         const int j = tile + 16 * (threadIdx.x & 3);
-        const int own = j < k_hi && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
+        own = j < k_hi && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             // a wave's keys lie in one granule: a scalar address
@@ -801,11 +808,23 @@ struct Staging {
             const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk;
             s_ks = a.k_scale[ph];
             s_vs = a.v_scale[ph];
-            s_ok = own >= 0;
         }
     }
-    __device__ __forceinline__ void put(int buf) {
+    // Whether some rows see keys of the tile at j0 and others do not.  Zero weights
+    // do not keep NaN codes of its values out of the sums: they go in as zeros, and so
+    // does what no row sees and may be anything; find_nan looks for them afterwards.
+    __device__ __forceinline__ bool late(int j0, int page) const {
+        return j0 < all0 || j0 + kTileKeys > all1 || __any(page < 0);
+    }
+    __device__ __forceinline__ void put(int buf, int j0) {
         const int tid = threadIdx.x;
+        if (late(j0, own)) {
+            uint32_t keep[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) keep[i] = own < 0 ? 0u : key_bytes(j0 + 16 * (tid & 3) + 4 * i, k_lo, k_hi);
+#pragma unroll
+            for (int i = 0; i < NL; ++i) met_nan |= masked_values(vr[i], keep);
+        }
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             lds.k[buf][PLACE(i * KEYS + tid / PPK, tid % PPK)] = kr[i];
@@ -814,14 +833,15 @@ struct Staging {
         if (tid < 4) {
             lds.ks[buf][tid] = s_ks;
             lds.vs[buf][tid] = s_vs;
-            lds.ok[buf][tid] = s_ok;
+            lds.ok[buf][tid] = own >= 0;
         }
     }
     __device__ __forceinline__ void begin(int j0) {
         pages(j0);
         load();
         pages(j0 + kTileKeys);
-        put(0);
+        put(0, j0);
+        if (threadIdx.x == 0) lds.met_nan = 0;
         __syncthreads();
     }
     // before the work on the tile at j0: the next one's loads go out
@@ -835,8 +855,14 @@ struct Staging {
     // after it: into the other buffer
     __device__ __forceinline__ void next(int j0, int buf) {
         asm volatile("" ::: "memory");
-        if (j0 + kTileKeys < k_hi) put(buf ^ 1);
+        if (j0 + kTileKeys < k_hi) put(buf ^ 1, j0 + kTileKeys);
         __syncthreads();
+    }
+    // after the last one, where there was one: whether a value was NaN and went in as zero
+    __device__ __forceinline__ bool nan_left_out() {
+        if (met_nan) lds.met_nan = 1;
+        __syncthreads();
+        return lds.met_nan != 0;
     }
 };
 
@@ -910,9 +936,9 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     const int k_row = key * (D / 16), k_swap = k_piece<D>(key, 2 * h2) - k_row, v_swap = v_piece(c, 2 * h2) - 4 * c;
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
-    uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
-    if (j0 < k_hi) stage.begin(j0);
+    const bool any = j0 < k_hi;
+    if (any) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
         stage.ahead(j0);
@@ -977,35 +1003,20 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                     pw[r / 2] = pack_bf16x2(e0 * vs, e1 * vs);
                 }
                 const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
-                // `fix(w)`: what a masked tile does to four words of values
-                auto multiply = [&](auto fix) {
-                    run_ahead<DT, kWideAhead>([&](int i) { return vt[32 * 4 * i + (v_swap ^ t)]; }, [&](int i, uint4 w) {
-                        fix(w);
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.x, w.y), p0, o[i], 0, 0, 0);
-                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.z, w.w), p1, o[i], 0, 0, 0);
-                    });
-                };
-                if (masked) {
-                    // values that no row of the wave sees may be anything: zero; NaN: find_nan
-                    uint32_t keep[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
-                    multiply([&](uint4 &w) { met_nan |= masked_values(w, keep); });
-                } else {
-                    multiply([](uint4 &) {});
-                }
+                run_ahead<DT, kWideAhead>([&](int i) { return vt[32 * 4 * i + (v_swap ^ t)]; }, [&](int i, const uint4 &w) {
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.x, w.y), p0, o[i], 0, 0, 0);
+                    o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(codes_to_bf16(w.z, w.w), p1, o[i], 0, 0, 0);
+                });
             }
         }
         stage.next(j0, buf);
     }
 
-    if (__any(met_nan != 0)) {
+    if (any && stage.nan_left_out()) {
         unsigned long long bits[(16 * DT + 63) / 64] = {};
         find_nan<16 * DT>(
             a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
-            [&](int j) {
-                return j < wk.all0 || j + kTileKeys > wk.all1 || __any(stage.page_at(j + 32 * h2) < 0 || stage.page_at(j + 32 * h2 + 16) < 0);
-            },
+            [&](int j) { return stage.late(j, stage.page_at(j + 16 * (lane & 3))); },
             [&](int i) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * h2 + (i & 3); }, [&](int j) { return stage.page_at(j); });
 #pragma unroll
         for (int t = 0; t < DT; ++t)
@@ -1091,9 +1102,9 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
-    uint32_t met_nan = 0;
     int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
-    if (j0 < k_hi) stage.begin(j0);
+    const bool any = j0 < k_hi;
+    if (any) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
         stage.ahead(j0);
@@ -1120,37 +1131,26 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 const i32x8 v8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
                 o[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8, p, o[t], 0, 0, 0, 127, 0, p_scale);
             };
-            if (masked) {
-                // values that no row of the wave sees may be anything: zero; NaN: find_nan
-                uint32_t keep[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) keep[i] = ok ? key_bytes(jg + 4 * i, wk.lo, wk.hi) : 0u;
-                run_ahead<DT, kNarrowAhead>([&](int t) { return vt[16 * 4 * t]; }, [&](int t, uint4 w) {
-                    met_nan |= masked_values(w, keep);
-                    multiply(t, w, w);
-                });
-            } else {
-                struct Twice {
-                    uint4 a, b;
-                };
-                run_ahead<DT, kNarrowAhead>(
-                    [&](int t) {
-                        // read twice: the LDS has time, copies would take the vector unit's
-                        const uint4 a = vt[16 * 4 * t];
-                        asm volatile("" ::: "memory");
-                        return Twice{a, vt[16 * 4 * t]};
-                    },
-                    [&](int t, const Twice &w) { multiply(t, w.a, w.b); });
-            }
+            struct Twice {
+                uint4 a, b;
+            };
+            run_ahead<DT, kNarrowAhead>(
+                [&](int t) {
+                    // read twice: the LDS has time, copies would take the vector unit's
+                    const uint4 a = vt[16 * 4 * t];
+                    asm volatile("" ::: "memory");
+                    return Twice{a, vt[16 * 4 * t]};
+                },
+                [&](int t, const Twice &w) { multiply(t, w.a, w.b); });
         }
         stage.next(j0, buf);
     }
 
-    if (__any(met_nan != 0)) {
+    if (any && stage.nan_left_out()) {
         unsigned long long bits[1] = {0};
         find_nan<4 * DT>(
             a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
-            [&](int j) { return j < wk.all0 || j + kTileKeys > wk.all1 || __any(stage.page_at(j + 16 * g) < 0); },
+            [&](int j) { return stage.late(j, stage.page_at(j + 16 * (lane & 3))); },
             [&](int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }, [&](int j) { return stage.page_at(j); });
 #pragma unroll
         for (int t = 0; t < DT; ++t)
