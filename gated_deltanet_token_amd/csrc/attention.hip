@@ -58,6 +58,11 @@ __device__ __forceinline__ void key_range(const AttentionArgs &a, const Request 
     jb = a.window > 0 && upto > a.window ? upto - a.window : 0;
 }
 
+// the token within its request of a row, and the last one of up to `rows` rows
+// from `row` on, of n
+__device__ __forceinline__ int token_of(int row, int G) { return (int)((unsigned)row / (unsigned)G); }
+__device__ __forceinline__ int last_row(int row, int rows, int n) { return (int)min((unsigned)row + rows, (unsigned)n) - 1; }
+
 // Row tiles without a list: request s owns the tile numbers from
 // floor(query_start_loc[s] * G / rows) + s * each on, G rows per token.  With
 // each = 1 that is as many as it needs or more, with each = 0 as many as it
@@ -66,7 +71,7 @@ __device__ __forceinline__ void key_range(const AttentionArgs &a, const Request 
 __device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, int &within) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = a.num_seqs;
-    auto first = [&](int s) { return (long long)max(a.qsl[s], 0) * group / rows + s * each; };
+    auto first = [&](int s) { return (long long)((unsigned long long)max(a.qsl[s], 0) * group / rows) + s * each; };
     while (n > 1) {
         const int step = (n + 63) / 64;
         const bool in = lane * step < n && first(lo + lane * step) <= tile;
@@ -416,25 +421,27 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4, kg = c >> 2;
     const int G = a.num_q_heads / a.num_kv_heads;
-    const long long unit = block / v.splits;
+    // rows and workgroups of a launch are fewer than 2^31 (launch_d): 32-bit
+    // divisions, in the registers of one lane or all
+    const unsigned unit = (unsigned)block / (unsigned)v.splits;
     const int split = block - (int)(unit * v.splits);
-    const long long tile = unit / a.num_kv_heads;
+    const int tile = (int)(unit / (unsigned)a.num_kv_heads);
     const int hk = (int)(unit - tile * a.num_kv_heads);
     int within, s;
     if constexpr (TAKE == Take::kSmall) {
-        s = (int)(tile / (kSmallRows / kTileRows));
-        within = (int)(tile % (kSmallRows / kTileRows));
+        s = tile / (kSmallRows / kTileRows);
+        within = tile % (kSmallRows / kTileRows);
     } else if (tile < a.num_seqs) {
-        s = (int)tile;                               // every request's first tile: no search
+        s = tile;                                    // every request's first tile: no search
         within = 0;
     } else {
         s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, within);
         ++within;
     }
     const Request rq = request_of(a, s);
-    const long long row0 = (long long)within * kTileRows, n_rows = (long long)rq.n * G;
-    if (within < 0 || row0 >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
-    const int i_first = (int)(row0 / G), i_last = (int)(min(row0 + kTileRows, n_rows) - 1) / G;
+    const int n_rows = rq.n * G;
+    if (within < 0 || (long long)within * kTileRows >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
+    const int row0 = within * kTileRows, i_first = token_of(row0, G), i_last = token_of(last_row(row0, kTileRows, n_rows), G);
     int lo, hi, x0, x1;                              // keys that some row sees, that every row sees
     key_range(a, rq, i_first, lo, x1);
     key_range(a, rq, i_last, x0, hi);
@@ -444,8 +451,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     const int k_lo = max(lo, split * v.chunk);
     const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
 
-    const long long row = row0 + c;
-    const int i_row = (int)(row / G), h = hk * G + (int)(row - (long long)i_row * G);
+    const int row = row0 + c, i_row = token_of(row, G), h = hk * G + row - i_row * G;
     const bool live = row < n_rows;
     int jb = 0, je = 0;
     if (live) key_range(a, rq, i_row, jb, je);
@@ -689,7 +695,7 @@ struct ManyLds {
 struct ManyShare {
     int s, hk, split;
     Request rq;
-    long long row0, n_rows;
+    int row0, n_rows;
     int k_lo, k_hi;        // its keys
     bool whole;            // no other split has any
 };
@@ -697,19 +703,19 @@ struct ManyShare {
 // num_kv_heads apart, so that with eight heads an XCD keeps to one.
 __device__ __forceinline__ bool many_share(const AttentionArgs &a, const Division &v, int block, int blocks, ManyShare &w) {
     const int G = a.num_q_heads / a.num_kv_heads;
-    const long long units = blocks / v.splits, unit = block / v.splits;
+    const unsigned units = (unsigned)blocks / (unsigned)v.splits, unit = (unsigned)block / (unsigned)v.splits, hks = a.num_kv_heads;
     w.split = block - (int)(unit * v.splits);
-    const long long tile = units / a.num_kv_heads - 1 - unit / a.num_kv_heads;
-    w.hk = (int)(unit % a.num_kv_heads);
+    const int tile = (int)(units / hks - 1 - unit / hks);
+    w.hk = (int)(unit % hks);
     int within;
     w.s = find_request(a, tile, G, kManyRows, 1, within);
     w.rq = request_of(a, w.s);
-    w.row0 = (long long)within * kManyRows;
-    w.n_rows = (long long)w.rq.n * G;
-    if (within < 0 || w.row0 >= w.n_rows || w.n_rows <= kSmallRows) return false;
+    w.n_rows = w.rq.n * G;
+    if (within < 0 || (long long)within * kManyRows >= w.n_rows || w.n_rows <= kSmallRows) return false;
+    w.row0 = within * kManyRows;
     int lo, hi, x;
-    key_range(a, w.rq, (int)(w.row0 / G), lo, x);
-    key_range(a, w.rq, (int)(min(w.row0 + kManyRows, w.n_rows) - 1) / G, x, hi);
+    key_range(a, w.rq, token_of(w.row0, G), lo, x);
+    key_range(a, w.rq, token_of(last_row(w.row0, kManyRows, w.n_rows), G), x, hi);
     const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
     if (w.split != sp.first && (w.split < sp.first || w.split > sp.last)) return false;
     w.whole = sp.last <= sp.first;
@@ -723,12 +729,12 @@ __device__ __forceinline__ bool many_share(const AttentionArgs &a, const Divisio
 struct WaveKeys {
     int lo, hi, all0, all1;
 };
-__device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const ManyShare &w, long long row, int rows) {
+__device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const ManyShare &w, int row, int rows) {
     const int G = a.num_q_heads / a.num_kv_heads;
     WaveKeys k{0, 0, 0, 0};
     if (row < w.n_rows) {
-        key_range(a, w.rq, (int)(row / G), k.lo, k.all1);
-        key_range(a, w.rq, (int)((min(row + rows, w.n_rows) - 1) / G), k.all0, k.hi);
+        key_range(a, w.rq, token_of(row, G), k.lo, k.all1);
+        key_range(a, w.rq, token_of(last_row(row, rows, w.n_rows), G), k.all0, k.hi);
         k.lo = max(k.lo, w.k_lo);
         k.hi = min(k.hi, w.k_hi);
         k.all0 = max(k.all0, w.k_lo);
@@ -886,9 +892,9 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
 
     // this wave's rows
-    const long long wrow = w.row0 + 32 * wave, row = wrow + c;
+    const int wrow = w.row0 + 32 * wave, row = wrow + c;
     const bool live = row < w.n_rows;
-    const int i_row = live ? (int)(row / G) : 0, h = hk * G + (live ? (int)(row - (long long)i_row * G) : 0);
+    const int i_row = live ? token_of(row, G) : 0, h = hk * G + (live ? row - i_row * G : 0);
     int jb = 0, je = 0;
     if (live) key_range(a, rq, i_row, jb, je);
     jb = max(jb, k_lo);
@@ -1083,9 +1089,9 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     if (!many_share(a, v, block, blocks, w)) return;
     const Request &rq = w.rq;
     const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
-    const long long wrow = w.row0 + 16 * wave, row = wrow + c;
+    const int wrow = w.row0 + 16 * wave, row = wrow + c;
     const bool live = row < w.n_rows;
-    const int i_row = live ? (int)(row / G) : 0, h = hk * G + (live ? (int)(row - (long long)i_row * G) : 0);
+    const int i_row = live ? token_of(row, G) : 0, h = hk * G + (live ? row - i_row * G : 0);
     int jb = 0, je = 0;
     if (live) key_range(a, rq, i_row, jb, je);
     jb = max(jb, k_lo);
@@ -1215,23 +1221,23 @@ __global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kernel(At
 // its splits' sums brought to the common maximum.
 // ---------------------------------------------------------------------------
 template <int D, Take TAKE>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Division v, long long rows, int tile_rows) {
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Division v, int rows, int tile_rows) {
     constexpr int E = D / 64;
     const int lane = threadIdx.x & 63;
-    const long long part = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (part >= rows) return;
+    const unsigned part = blockIdx.x * 4u + (threadIdx.x >> 6);
+    if (part >= (unsigned)rows) return;
     const int G = a.num_q_heads / a.num_kv_heads;
     int s, t, h;
-    long long r;                            // the row within its request and kv head
+    int r;                                  // the row within its request and kv head
     if constexpr (TAKE == Take::kSmall) {
-        const int hk = (int)(part % a.num_kv_heads);
-        r = part / a.num_kv_heads % kSmallRows;
-        s = (int)(part / a.num_kv_heads / kSmallRows);
-        h = hk * G + (int)(r % G);
+        const unsigned of = part / (unsigned)a.num_kv_heads;
+        r = (int)(of % kSmallRows);
+        s = (int)(of / kSmallRows);
+        h = (int)(part - of * a.num_kv_heads) * G + r % G;
         t = 0;
     } else {
-        t = (int)(part / a.num_q_heads);
-        h = (int)(part - (long long)t * a.num_q_heads);
+        t = (int)(part / (unsigned)a.num_q_heads);
+        h = (int)(part - (unsigned)t * a.num_q_heads);
         s = 0;
         int n = a.num_seqs;                 // the request of token t, 64 candidates per step
         while (n > 1) {
@@ -1243,19 +1249,19 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
         }
     }
     const Request rq = request_of(a, s);
-    const long long n_rows = (long long)rq.n * G;
+    const int n_rows = rq.n * G;
     if constexpr (TAKE == Take::kSmall) {
         if (n_rows > kSmallRows || r >= n_rows) return;
-        t = rq.begin + (int)(r / G);
+        t = rq.begin + token_of(r, G);
     } else {
         if (t < rq.begin || t >= rq.begin + rq.n || (TAKE == Take::kLarge && n_rows <= kSmallRows)) return;
-        r = (long long)(t - rq.begin) * G + h % G;
+        r = (t - rq.begin) * G + h % G;
     }
     // the keys of the row's tile decide which splits wrote
-    const long long r0 = r / tile_rows * tile_rows;
+    const int r0 = r - r % tile_rows;
     int k_lo, k_hi, x;
-    key_range(a, rq, (int)(r0 / G), k_lo, x);
-    key_range(a, rq, (int)((min(r0 + tile_rows, n_rows) - 1) / G), x, k_hi);
+    key_range(a, rq, token_of(r0, G), k_lo, x);
+    key_range(a, rq, token_of(last_row(r0, tile_rows, n_rows), G), x, k_hi);
     const Splits sp = splits_of(k_lo, k_hi, v.chunk, v.splits);
     if (sp.last <= sp.first) return;
     float m = kNegInf, l = 0.f, o[E] = {};
@@ -1359,7 +1365,7 @@ template <int D, Take TAKE>
 static void launch_join(const AttentionArgs &a, const Launch &p, const Division &v, int tile_rows, hipStream_t stream) {
     if (p.splits > 1)
         hipLaunchKernelGGL((attention_join_kernel<D, TAKE>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, a, v,
-                           p.rows, tile_rows);
+                           (int)p.rows, tile_rows);
 }
 
 template <int D>
