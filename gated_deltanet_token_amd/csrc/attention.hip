@@ -172,11 +172,26 @@ __device__ __forceinline__ void split4(const float *f, float up, int &hi, int &l
     lo = (int)e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
 }
 
-// One row's parts for lanes of 16 rows, in the order of the key operands: bytes
+// A lane's elements of one row, for lanes of 16 rows: 64 l + 16 g + e.
+template <int D>
+struct Row16 {
+    uint4 w[D / 64][2];
+};
+template <int D>
+__device__ __forceinline__ Row16<D> load_q16(const uint16_t *q, int g) {
+    Row16<D> r;
+#pragma unroll
+    for (int l = 0; l < D / 64; ++l)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) r.w[l][b] = *reinterpret_cast<const uint4 *>(q + 64 * l + 16 * g + 8 * b);
+    return r;
+}
+
+// Their two parts, in the order of the key operands: bytes
 // 16 m + e of step s are elements 128 s + 64 m + 16 g + e (for D = 64 the upper
 // 16 bytes are lo).  Returns what the products are to be multiplied by.
 template <int D>
-__device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
+__device__ __forceinline__ float split_q16(const Row16<D> &q, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
                                            i32x8 (&ql)[D >= 128 ? D / 128 : 1]) {
     constexpr int KL = D / 64;
     float f[KL][16], m = 0.f;
@@ -185,7 +200,7 @@ __device__ __forceinline__ float split_q16(const uint16_t *q, int g, i32x8 (&qh)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             float t[8];
-            unpack8(*reinterpret_cast<const uint4 *>(q + 64 * l + 16 * g + 8 * b), t);
+            unpack8(q.w[l][b], t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[l][8 * b + e] = t[e];
         }
@@ -458,23 +473,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     jb = max(jb, k_lo);
     je = min(je, k_hi);
 
-    i32x8 qh[KS], ql[KS];
-    const float to_log2 =
-        a.scale * kLog2e *
-        split_q16<D>(a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D, g, qh, ql);
-    if constexpr (QLDS) {
-        if (wave == 0) {
-#pragma unroll
-            for (int st = 0; st < KS; ++st) {
-                lds.q[4 * st][lane] = i32x4{qh[st][0], qh[st][1], qh[st][2], qh[st][3]};
-                lds.q[4 * st + 1][lane] = i32x4{qh[st][4], qh[st][5], qh[st][6], qh[st][7]};
-                lds.q[4 * st + 2][lane] = i32x4{ql[st][0], ql[st][1], ql[st][2], ql[st][3]};
-                lds.q[4 * st + 3][lane] = i32x4{ql[st][4], ql[st][5], ql[st][6], ql[st][7]};
-            }
-        }
-        __syncthreads();
-    }
-
+    const Row16<D> q =
+        load_q16<D>(a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D, g);
     const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
     const int32_t *bt = a.block_table + s * a.block_table_stride;
     auto page_at = [&](int j) {
@@ -482,6 +482,11 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         return j < k_hi && p < a.max_pages ? bt[p] : -1;
     };
     auto good = [&](int p) { return (unsigned)p < (unsigned)a.num_pages; };
+    // Page numbers are loaded a tile ahead of the loads that use them, and not
+    // looked at before: loads come back in order, so that looking at one that was
+    // asked for behind a tile waits for the tile.
+    auto entry_at = [&](int j) { return bt[min(j >> shift, a.max_pages - 1)]; };
+    auto page_of = [&](int entry, int j) { return j < k_hi && good(entry) ? entry : -1; };
 
     uint4 kr[NT][KL];
     uint32_t vr[DT][NV];
@@ -498,6 +503,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         const int j = j0 + NK * g;
         const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
         const uint8_t *p = a.v_cache + (ph * D + c) * a.page + (j & in_page);
+        ks = a.k_scale[ph];              // needed before the values
+        vs = a.v_scale[ph];
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
             if constexpr (NV == 4) {
@@ -512,8 +519,6 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
                 vr[t][1] = w.y;
             }
         }
-        ks = a.k_scale[ph];
-        vs = a.v_scale[ph];
     };
 
     f32x4 o[DT] = {};
@@ -521,15 +526,40 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     uint32_t met_nan = 0;
     constexpr int step = W * TK;
     int j0 = (k_lo & ~(TK - 1)) + wave * TK;
-    int pk = page_at(j0 + NK * kg), pv = page_at(j0 + NK * g);
+    int ek = entry_at(j0 + NK * kg), ev = entry_at(j0 + NK * g), pv = -1;
+    // the next tile's keys, and the entries behind it
+    auto turn = [&](int j) {
+        const int pk = page_of(ek, j + NK * kg), page = page_of(ev, j + NK * g);
+        load_k(j, pk);
+        ek = entry_at(j + step + NK * kg);
+        ev = entry_at(j + step + NK * g);
+        return page;
+    };
     if (j0 < k_hi) {
-        load_k(j0, pk);
+        pv = turn(j0);
+        asm volatile("" ::: "memory");
         load_v(j0, pv);
+        asm volatile("" ::: "memory");
     }
+    // q is split while the first tile is on its way
+    i32x8 qh[KS], ql[KS];
+    const float to_log2 = a.scale * kLog2e * split_q16<D>(q, qh, ql);
+    if constexpr (QLDS) {
+        if (wave == 0) {
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                lds.q[4 * st][lane] = i32x4{qh[st][0], qh[st][1], qh[st][2], qh[st][3]};
+                lds.q[4 * st + 1][lane] = i32x4{qh[st][4], qh[st][5], qh[st][6], qh[st][7]};
+                lds.q[4 * st + 2][lane] = i32x4{ql[st][0], ql[st][1], ql[st][2], ql[st][3]};
+                lds.q[4 * st + 3][lane] = i32x4{ql[st][4], ql[st][5], ql[st][6], ql[st][7]};
+            }
+        }
+        __syncthreads();
+    }
+
     for (; j0 < k_hi; j0 += step) {
         const int jn = j0 + step;
-        pk = page_at(jn + NK * kg);
-        const int pv_n = page_at(jn + NK * g);
+        int pv_n = -1;
         // X^T: keys NK g + 4 t + r of row c
         f32x4 x[NT] = {};
 #pragma unroll
@@ -550,7 +580,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
                     x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, lo8, x[t], 0, 0, 0, 0, 0, 0);
             }
         }
-        if (jn < k_hi) load_k(jn, pk);
+        if (jn < k_hi) pv_n = turn(jn);
         asm volatile("" ::: "memory");
 
         const int jg = j0 + NK * g;
@@ -1099,7 +1129,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     const WaveKeys wk = wave_keys(a, w, wrow, 16);
     i32x8 qh[KS], ql[KS];
     const float to_log2 = a.scale * kLog2e *
-                          split_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, qh, ql);
+                          split_q16<D>(load_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), qh, ql);
     Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
     // this lane's operand rows: the t-th K operand's is 4 t keys further on, with its
     // pieces in the same order, and so the t-th V operand's, 16 t elements
