@@ -155,8 +155,20 @@ __device__ __forceinline__ Splits splits_of(int lo, int hi, int chunk, int n) {
     return s;
 }
 
-// The largest finite magnitude m of a row of q, brought to [128, 256): the
-// power of two for it, within [2^-120, 2^126].
+// The larger of the magnitudes of two bf16 pairs, as integers in the same order
+// (an infinity or NaN among a row of q: its scores are NaN at any factor).
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t w) {
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                  __builtin_bit_cast(u16x2, w & 0x7fff7fffu)));
+}
+__device__ __forceinline__ uint32_t larger(uint32_t m, const uint4 &w) {
+    return larger(larger(larger(larger(m, w.x), w.y), w.z), w.w);
+}
+__device__ __forceinline__ float larger_half(uint32_t m) { return __builtin_bit_cast(float, max(m << 16, m & 0xffff0000u)); }
+
+// The largest magnitude m of a row of q, brought to [128, 256): the power of
+// two for it, within [2^-121, 2^126].
 __device__ __forceinline__ float split_factor(float m) {
     const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
     return __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
@@ -194,20 +206,19 @@ template <int D>
 __device__ __forceinline__ float split_q16(const Row16<D> &q, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
                                            i32x8 (&ql)[D >= 128 ? D / 128 : 1]) {
     constexpr int KL = D / 64;
-    float f[KL][16], m = 0.f;
+    float f[KL][16];
+    uint32_t mm = 0;
 #pragma unroll
-    for (int l = 0; l < KL; ++l) {
+    for (int l = 0; l < KL; ++l)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             float t[8];
             unpack8(q.w[l][b], t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[l][8 * b + e] = t[e];
+            mm = larger(mm, q.w[l][b]);
         }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) m = is_finite(f[l][e]) ? fmaxf(m, fabsf(f[l][e])) : m;
-    }
-    m = max_over32(max_over16(m));
+    const float m = max_over32(max_over16(larger_half(mm)));
     const float up = split_factor(m);
 #pragma unroll
     for (int l = 0; l < KL; ++l)
@@ -936,17 +947,12 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     float to_log2;
     {
         const uint16_t *qp = a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D + 32 * h2;
-        float m = 0.f;
+        uint32_t mm = 0;
 #pragma unroll
         for (int st = 0; st < KS; ++st)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float f[8];
-                unpack8(*reinterpret_cast<const uint4 *>(qp + 64 * st + 8 * b), f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) m = is_finite(f[e]) ? fmaxf(m, fabsf(f[e])) : m;
-            }
-        m = max_over32(m);
+            for (int b = 0; b < 4; ++b) mm = larger(mm, *reinterpret_cast<const uint4 *>(qp + 64 * st + 8 * b));
+        const float m = max_over32(larger_half(mm));
         const float up = split_factor(m);
         to_log2 = a.scale * kLog2e * (1.f / up);
 #pragma unroll
