@@ -199,42 +199,40 @@ __device__ __forceinline__ Row16<D> load_q16(const uint16_t *q, int g) {
     return r;
 }
 
-// Their two parts, in the order of the key operands: bytes
-// 16 m + e of step s are elements 128 s + 64 m + 16 g + e (for D = 64 the upper
-// 16 bytes are lo).  Returns what the products are to be multiplied by.
+// What brings the row to its parts' range.
 template <int D>
-__device__ __forceinline__ float split_q16(const Row16<D> &q, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
-                                           i32x8 (&ql)[D >= 128 ? D / 128 : 1]) {
-    constexpr int KL = D / 64;
-    float f[KL][16];
+__device__ __forceinline__ float factor_q16(const Row16<D> &q) {
     uint32_t mm = 0;
 #pragma unroll
-    for (int l = 0; l < KL; ++l)
+    for (int l = 0; l < D / 64; ++l) mm = larger(larger(mm, q.w[l][0]), q.w[l][1]);
+    return split_factor(max_over32(max_over16(larger_half(mm))));
+}
+
+// The row's two parts, in the order of the key operands: bytes
+// 16 m + e of step s are elements 128 s + 64 m + 16 g + e (for D = 64 the upper
+// 16 bytes are lo).
+template <int D>
+__device__ __forceinline__ void split_q16(const Row16<D> &q, float up, i32x8 (&qh)[D >= 128 ? D / 128 : 1],
+                                          i32x8 (&ql)[D >= 128 ? D / 128 : 1]) {
+#pragma unroll
+    for (int l = 0; l < D / 64; ++l)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            float t[8];
-            unpack8(q.w[l][b], t);
+            float f[8];
+            unpack8(q.w[l][b], f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[l][8 * b + e] = t[e];
-            mm = larger(mm, q.w[l][b]);
-        }
-    const float m = max_over32(max_over16(larger_half(mm)));
-    const float up = split_factor(m);
-#pragma unroll
-    for (int l = 0; l < KL; ++l)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            int hw, lw;
-            split4(&f[l][4 * w], up, hw, lw);
-            if constexpr (D == 64) {
-                qh[0][w] = hw;
-                qh[0][4 + w] = lw;
-            } else {
-                qh[l / 2][4 * (l & 1) + w] = hw;
-                ql[l / 2][4 * (l & 1) + w] = lw;
+            for (int w = 2 * b; w < 2 * b + 2; ++w) {
+                int hw, lw;
+                split4(&f[4 * (w & 1)], up, hw, lw);
+                if constexpr (D == 64) {
+                    qh[0][w] = hw;
+                    qh[0][4 + w] = lw;
+                } else {
+                    qh[l / 2][4 * (l & 1) + w] = hw;
+                    ql[l / 2][4 * (l & 1) + w] = lw;
+                }
             }
         }
-    return 1.f / up;
 }
 
 // A factor for scores whose signs were turned where it is negative: not zero,
@@ -554,9 +552,12 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     }
     // q is split while the first tile is on its way
     i32x8 qh[KS], ql[KS];
-    const float to_log2 = a.scale * kLog2e * split_q16<D>(q, qh, ql);
-    if constexpr (QLDS) {
+    const float up = factor_q16<D>(q), to_log2 = a.scale * kLog2e * (1.f / up);
+    if constexpr (!QLDS) {
+        split_q16<D>(q, up, qh, ql);
+    } else {
         if (wave == 0) {
+            split_q16<D>(q, up, qh, ql);
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
                 lds.q[4 * st][lane] = i32x4{qh[st][0], qh[st][1], qh[st][2], qh[st][3]};
@@ -1134,8 +1135,9 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     je = min(je, k_hi);
     const WaveKeys wk = wave_keys(a, w, wrow, 16);
     i32x8 qh[KS], ql[KS];
-    const float to_log2 = a.scale * kLog2e *
-                          split_q16<D>(load_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), qh, ql);
+    const Row16<D> q = load_q16<D>(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g);
+    const float up = factor_q16<D>(q), to_log2 = a.scale * kLog2e * (1.f / up);
+    split_q16<D>(q, up, qh, ql);
     Staging<D, kNarrowThreads, k_piece_narrow<D>> stage(a, lds, w, wave);
     // this lane's operand rows: the t-th K operand's is 4 t keys further on, with its
     // pieces in the same order, and so the t-th V operand's, 16 t elements
