@@ -374,7 +374,7 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
         auto load = [&](int i0, Raw (&r)[UNROLL]) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
-                const int i = min(i0 + u * step, rows - 1), t = i / a.num_q_heads, h = i - t * a.num_q_heads;
+                const int i = min(i0 + u * step, rows - 1), t = (unsigned)i / (unsigned)a.num_q_heads, h = i - t * a.num_q_heads;
                 r[u] = load_raw(a, a.q + (t0 + t) * a.q_stride + (long long)h * D, e0);
             }
         };
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
                 for (int u = 0; u < UNROLL; ++u) {
                     const int i = i0 + u * step;
                     if (i >= rows) continue;
-                    const int t = i / a.num_q_heads, h = i - t * a.num_q_heads;
+                    const int t = (unsigned)i / (unsigned)a.num_q_heads, h = i - t * a.num_q_heads;
                     float f[8];
                     rotated(a, now[u], e0, cs + t * half, f);
                     *reinterpret_cast<uint4 *>(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + e0) = pack8(f);
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
         if (a.q != a.q_out && c0 >= a.rot)
 #pragma unroll 4
             for (int i = wave * TPI + lane / LPT; i < rows; i += kAppendWaves * TPI) {
-                const int t = i / a.num_q_heads, h = i - t * a.num_q_heads;
+                const int t = (unsigned)i / (unsigned)a.num_q_heads, h = i - t * a.num_q_heads;
                 *reinterpret_cast<uint4 *>(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + c0) =
                     *reinterpret_cast<const uint4 *>(a.q + (t0 + t) * a.q_stride + (long long)h * D + c0);
             }
@@ -413,9 +413,11 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
     // the first of its new ones.  Rank 0 of all windows comes first, and ranks
     // are shifted against each other, so that the blocks with work are spread
     // over the XCDs and CUs whatever their spacing.
-    const int windows = (a.num_tokens + a.page - 1) / a.page;
-    const int unit = (int)blockIdx.x / (2 * groups), part = (int)blockIdx.x - unit * 2 * groups;
-    const int rank = unit / windows, w0 = (unit - rank * windows + 5 * rank) % windows;
+    const int shift = __builtin_ctz(a.page);
+    const unsigned windows = ((unsigned)a.num_tokens + a.page - 1) >> shift, parts = 2 * groups;
+    const unsigned unit = blockIdx.x / parts;
+    const int part = (int)(blockIdx.x - unit * parts), rank = (int)(unit / windows);
+    const int w0 = (int)((unit + 5 * rank) % windows);
     const long long slots = (long long)a.num_pages * a.page;
     const int first = w0 * a.page;
     // the slots of the window's tokens and of as many behind them (a page's run
@@ -430,7 +432,6 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
     const int item = (is_k ? part : part - groups) * kAppendWaves + wave;
     const bool live = item < a.num_kv_heads;
     const int head = live ? item : 0;
-    const int shift = __builtin_ctz(a.page);
     // the next page of the block: its new tokens t .. t + n, from offset off on
     int skip = rank, t, n, off;
     long long ph;
