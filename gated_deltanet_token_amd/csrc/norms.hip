@@ -42,7 +42,8 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a) {
     const long long n = (long long)a.num_tokens * a.num_heads;
     const long long row = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
     if (row >= n) return;
-    const long long t = row / a.num_heads, h = row - t * a.num_heads;
+    // (64-bit divisions take a hundred instructions: for more than 2^32 rows only)
+    const long long t = n <= 0xffffffffLL ? (unsigned)row / (unsigned)a.num_heads : row / a.num_heads, h = row - t * a.num_heads;
     float f[8] = {}, w[8] = {}, z[8] = {};
     if (live) {
         unpack8(load16(a.x + t * a.x_stride + h * a.d + e0), f);
