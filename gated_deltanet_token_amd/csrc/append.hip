@@ -18,8 +18,8 @@
 //
 // Bound by HBM for prompts (q in and out, k and v in, codes out) and by the
 // 64-bit sines, by latency for decode rows.  Measured: 32 decode rows, 16/4 heads
-// of 256 with 64 elements rotated: 7.5 us; 2,048 tokens, of prompts and decode
-// rows: 19.5 us, 2.4 TB/s; 16,384 tokens, 32/8 heads of 128, all rotated: 107 us, 3.5
+// of 256 with 64 elements rotated: 7.3 us; 2,048 tokens, of prompts and decode
+// rows: 19.4 us, 2.4 TB/s; 16,384 tokens, 32/8 heads of 128, all rotated: 104 us, 3.6
 // TB/s.
 #include "fp8.h"
 #include "serving_internal.h"

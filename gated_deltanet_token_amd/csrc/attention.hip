@@ -418,9 +418,9 @@ __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int
 // TK is 64; at D = 256, 32, so that two tiles and the sums fit a lane's 256
 // registers (with 64 keys and no tile ahead a decode step of 32 requests took
 // 25.0 us).
-// Measured: 32 requests of 1,100 tokens, 16/4 heads of 256: 22.0 us, 3.3 TB/s, most
-// of it start and end; five of 40,000 to 131,000, 32/8 heads of 128: 191 us, 5.8
-// TB/s, and 6 us to join the parts.
+// Measured: 32 requests of 1,100 tokens, 16/4 heads of 256: 20.8 us, half of it start
+// and end; five of 40,000 to 131,000, 32/8 heads of 128: 188 us, 5.9 TB/s, and 6 us to
+// join the parts.
 // ---------------------------------------------------------------------------
 constexpr int few_keys(int d) { return d == 256 ? 32 : 64; }
 
@@ -689,12 +689,12 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the matrix cores and the exponentials: tiles of 64 keys and values pass
 // through the LDS once for all four waves, the next one on its way from HBM
 // to registers meanwhile, with one barrier per tile between two buffers.
-// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 575 us, 956 TFLOP/s (4 D
-// per row and key it sees).  Vector and matrix instructions hardly overlap here: an
+// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 562 us on one card and 618
+// on another, 980 and 890 TFLOP/s (4 D per row and key it sees).  Vector and matrix instructions hardly overlap here: an
 // operation takes 2.4 cycles of a SIMD, an exponential 8, a pair of values'
 // conversion 4, a matrix product 32 of which it hides 10; their sum over a tile is
 // what a tile takes.  (Values converted once for the workgroup, on their way to the
-// LDS: 612 us, twice the LDS reads.)
+// LDS: 612 us against 573 then, twice the LDS reads.)
 //
 // Lanes: with c = lane % 32 and h = lane / 32, a lane holds row c and the keys
 // 32 h .. 32 h + 31 of the tile, x[a][r] being key 32 h + 16 a + r.  For that,
@@ -1101,8 +1101,9 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // 2,048 tokens: 71 us, 67 so; at D = 128, where both fit, a prompt of 8,192 tokens
 // took 948 us with 16 rows per wave and 583 with 32).  Lanes as in the few-rows
 // kernel with 64 keys, operands from the LDS.  A prompt of 8,192 tokens, 16/4
-// heads of 256: 623 us, 880 TFLOP/s; what bounds it are latencies within a tile,
-// which two waves per SIMD do not hide.
+// heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 62 us.  What bounds it
+// are latencies within a tile, which two waves per SIMD do not hide: a tile takes
+// 5,200 cycles, and 3,900 where one of the eight waves has rows.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowThreads = 512;
 constexpr int kNarrowAhead = 3;
