@@ -1326,9 +1326,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // it as much as 32, and it reads a key once for 128 rows).
 //
 // Keys are split until there is a workgroup for every CU, two of the wide
-// kernel's, which fit a CU together.  A part has at least kMinChunk keys where
-// eight waves share them (joining costs a launch: 32 decode rows of 1,100 keys take
-// 23.0 us in one part and 23.8 in two; five of 40,000 to 131,000 take 206 us in
+// kernel's, which fit a CU together.  Where eight waves share a part's keys it has
+// at least kMinChunk (joining costs a launch: 32 decode rows of 1,100 keys take 20.8
+// us in one part and 21.6 in two, 16 of 1,500 with heads of 128 15.7 and 17.4), or
+// kIdleChunk where three of four CUs had no work else (one row of 4,000 keys: 18.7
+// us with 512, 25.3 with 1,024; eight of 1,100: 18.1 and 20.3; four of 2,500 with heads
+// of 128: 15.1, 16.7, and 16.9 with 256; five of 40,000 to 131,000 take 206 us in
 // parts for 240 CUs and 321 for 120), and kManyChunk where each wave works on
 // them all: 300 tokens of three prompts of up to 1,100 tokens, 16/4 heads of 256,
 // take 31 us with 256, 38 with 512, 33 with 128 and 51 with 1,024; of 128, 27, 31,
@@ -1337,7 +1340,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // sums cost more than the long rows' wait.)
 // ---------------------------------------------------------------------------
 constexpr int kCUs = 256;
-constexpr int kMinChunk = 1024;
+constexpr int kMinChunk = 1024, kIdleChunk = 512;
 constexpr int kManyChunk = 256;
 
 struct Launch {
@@ -1346,6 +1349,9 @@ struct Launch {
     int chunk, splits;
     long long floats;       // of partial results
 };
+
+// the least keys of a part of the few-rows kernel's
+static long long few_chunk(long long busy, int kv_heads) { return busy * kv_heads * 4 <= kCUs ? kIdleChunk : kMinChunk; }
 
 // `busy`: row tiles that hold rows, as far as the host can tell
 static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len, int aim,
@@ -1377,7 +1383,8 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
     if (T <= S) {
         p.few_takes = Take::kAll;
         const long long full = T * G / kTileRows;
-        p.few = divide(full + S, full > T ? full : T, T * q_heads, kv_heads, d, max_seq_len, kCUs, kMinChunk);
+        const long long busy = full > T ? full : T;
+        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, kCUs, few_chunk(busy, kv_heads));
     } else {
         p.few_takes = Take::kSmall;
         const long long full = T * G / kManyRows, busy = full > 1 ? full : 1, room = d == 256 ? kCUs : 2 * kCUs;
@@ -1385,8 +1392,9 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
         // workgroups take anyway: at least this many keys one after the other, where
         // a small request's waves share theirs
         const long long anyway = busy * kv_heads * (T / S) / 2 / room * (mixed_threads(d) / 64);
+        const long long least = few_chunk(S, kv_heads);
         p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
-                       anyway > kMinChunk ? anyway : kMinChunk);
+                       anyway > least ? anyway : least);
         p.many = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
     }
     return p;
