@@ -66,12 +66,15 @@ __device__ __forceinline__ int last_row(int row, int rows, int n) { return (int)
 // Row tiles without a list: request s owns the tile numbers from
 // floor(query_start_loc[s] * G / rows) + s * each on, G rows per token.  With
 // each = 1 that is as many as it needs or more, with each = 0 as many as it
-// needs behind its first one.  Returns the last request whose first number is at
+// needs behind its first one.  `up` rounds the first number up: then, with each =
+// 0, a request of more than `rows` rows owns at least one number per `rows` of
+// them, and the others one at most.  Returns the last request whose first number is at
 // or before `tile` (64 candidates per step), and the tile's place in it.
-__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, int &within) {
+__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, bool up, int &within) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = a.num_seqs;
-    auto first = [&](int s) { return (long long)((unsigned long long)max(a.qsl[s], 0) * group / rows) + s * each; };
+    const int add = up ? rows - 1 : 0;
+    auto first = [&](int s) { return (long long)(((unsigned long long)max(a.qsl[s], 0) * group + add) / rows) + s * each; };
     while (n > 1) {
         const int step = (n + 63) / 64;
         const bool in = lane * step < n && first(lo + lane * step) <= tile;
@@ -389,6 +392,7 @@ constexpr int kSmallRows = 32;
 // (request, row of kSmallRows, kv head).
 struct Division {
     int chunk, splits;
+    bool by_rows;       // many rows: a tile number per kSmallRows rows, else one per kManyRows and one per request
     float *sums, *stats;
 };
 __device__ __forceinline__ float *part_o(const Division &v, int d, long long row, int split) {
@@ -453,13 +457,13 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     const int hk = (int)(unit - tile * a.num_kv_heads);
     int within, s;
     if constexpr (TAKE == Take::kSmall) {
-        s = tile / (kSmallRows / kTileRows);
-        within = tile % (kSmallRows / kTileRows);
+        within = (unsigned)tile / (unsigned)a.num_seqs;      // the first tiles, most of them the only ones, first
+        s = tile - within * a.num_seqs;
     } else if (tile < a.num_seqs) {
         s = tile;                                    // every request's first tile: no search
         within = 0;
     } else {
-        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, within);
+        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, false, within);
         ++within;
     }
     const Request rq = request_of(a, s);
@@ -750,7 +754,7 @@ __device__ __forceinline__ bool many_share(const AttentionArgs &a, const Divisio
     const int tile = (int)(units / hks - 1 - unit / hks);
     w.hk = (int)(unit % hks);
     int within;
-    w.s = find_request(a, tile, G, kManyRows, 1, within);
+    w.s = v.by_rows ? find_request(a, tile, G, kSmallRows, 0, true, within) : find_request(a, tile, G, kManyRows, 1, false, within);
     w.rq = request_of(a, w.s);
     w.n_rows = w.rq.n * G;
     if (within < 0 || (long long)within * kManyRows >= w.n_rows || w.n_rows <= kSmallRows) return false;
@@ -1374,6 +1378,7 @@ static Launch divide(long long tiles, long long busy, long long rows, int kv_hea
 
 struct Plan {
     Take few_takes;
+    bool by_rows;
     Launch few, many;
 };
 
@@ -1395,7 +1400,10 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
         const long long least = few_chunk(S, kv_heads);
         p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
                        anyway > least ? anyway : least);
-        p.many = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
+        // the least numbers that are enough: a request of many rows has more than kSmallRows
+        const long long by_rows = T * G / kSmallRows + 1;
+        p.by_rows = by_rows < full + S;
+        p.many = divide(p.by_rows ? by_rows : full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
     }
     return p;
 }
@@ -1406,7 +1414,9 @@ int64_t attention_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads,
 }
 
 // the partial results of a launch at `ws`
-static Division division(const Launch &p, int d, float *ws) { return {p.chunk, p.splits, ws, ws + p.rows * p.splits * d}; }
+static Division division(const Launch &p, bool by_rows, int d, float *ws) {
+    return {p.chunk, p.splits, by_rows, ws, ws + p.rows * p.splits * d};
+}
 
 template <int D, Take TAKE>
 static void launch_join(const AttentionArgs &a, const Launch &p, const Division &v, int tile_rows, hipStream_t stream) {
@@ -1421,13 +1431,13 @@ static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
     const long long few = p.few.units * p.few.splits, many = p.many.units * p.many.splits;
     if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
-    const Division vf = division(p.few, D, a.workspace);
+    const Division vf = division(p.few, false, D, a.workspace);
     if (p.few_takes == Take::kAll) {
         hipLaunchKernelGGL((attention_few_kernel<D>), dim3((unsigned)few), dim3(512), 0, stream, a, vf);
         launch_join<D, Take::kAll>(a, p.few, vf, kTileRows, stream);
         return hipGetLastError();
     }
-    const Division vm = division(p.many, D, a.workspace + p.few.floats);
+    const Division vm = division(p.many, p.by_rows, D, a.workspace + p.few.floats);
     hipLaunchKernelGGL((attention_mixed_kernel<D>), dim3((unsigned)(few + many)), dim3(mixed_threads(D)), 0, stream, a, vf, vm,
                        (int)many);
     launch_join<D, Take::kSmall>(a, p.few, vf, kTileRows, stream);
