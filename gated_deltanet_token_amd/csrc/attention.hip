@@ -457,7 +457,10 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     const int hk = (int)(unit - tile * a.num_kv_heads);
     int within, s;
     if constexpr (TAKE == Take::kSmall) {
-        within = (unsigned)tile / (unsigned)a.num_seqs;      // the first tiles, most of them the only ones, first
+        // the first tiles, most of them the only ones, first (with each request's two
+        // next to each other, half of the XCDs had nothing but empty ones: a mixed step
+        // of 2,048 tokens took 63 us, 54 so)
+        within = (unsigned)tile / (unsigned)a.num_seqs;
         s = tile - within * a.num_seqs;
     } else if (tile < a.num_seqs) {
         s = tile;                                    // every request's first tile: no search
@@ -1105,7 +1108,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // 2,048 tokens: 71 us, 67 so; at D = 128, where both fit, a prompt of 8,192 tokens
 // took 948 us with 16 rows per wave and 583 with 32).  Lanes as in the few-rows
 // kernel with 64 keys, operands from the LDS.  A prompt of 8,192 tokens, 16/4
-// heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 62 us.  What bounds it
+// heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 54 us.  What bounds it
 // are latencies within a tile, which two waves per SIMD do not hide: a tile takes
 // 5,200 cycles, and 3,900 where one of the eight waves has rows.
 // ---------------------------------------------------------------------------
@@ -1335,7 +1338,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // us in one part and 21.6 in two, 16 of 1,500 with heads of 128 15.7 and 17.4), or
 // kIdleChunk where three of four CUs had no work else (one row of 4,000 keys: 18.7
 // us with 512, 25.3 with 1,024; eight of 1,100: 18.1 and 20.3; four of 2,500 with heads
-// of 128: 15.1, 16.7, and 16.9 with 256; five of 40,000 to 131,000 take 206 us in
+// of 128: 15.1, 16.7, and 16.9 with 256; not beside prompts, whose rows take longer:
+// 300 tokens and five such rows 33.6 and 29.9; five of 40,000 to 131,000 take 206 us in
 // parts for 240 CUs and 321 for 120), and kManyChunk where each wave works on
 // them all: 300 tokens of three prompts of up to 1,100 tokens, 16/4 heads of 256,
 // take 31 us with 256, 38 with 512, 33 with 128 and 51 with 1,024; of 128, 27, 31,
@@ -1353,9 +1357,6 @@ struct Launch {
     int chunk, splits;
     long long floats;       // of partial results
 };
-
-// the least keys of a part of the few-rows kernel's
-static long long few_chunk(long long busy, int kv_heads) { return busy * kv_heads * 4 <= kCUs ? kIdleChunk : kMinChunk; }
 
 // `busy`: row tiles that hold rows, as far as the host can tell
 static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len, int aim,
@@ -1389,7 +1390,8 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
         p.few_takes = Take::kAll;
         const long long full = T * G / kTileRows;
         const long long busy = full > T ? full : T;
-        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, kCUs, few_chunk(busy, kv_heads));
+        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, kCUs,
+                       busy * kv_heads * 4 <= kCUs ? kIdleChunk : kMinChunk);
     } else {
         p.few_takes = Take::kSmall;
         const long long full = T * G / kManyRows, busy = full > 1 ? full : 1, room = d == 256 ? kCUs : 2 * kCUs;
@@ -1397,10 +1399,11 @@ static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, 
         // workgroups take anyway: at least this many keys one after the other, where
         // a small request's waves share theirs
         const long long anyway = busy * kv_heads * (T / S) / 2 / room * (mixed_threads(d) / 64);
-        const long long least = few_chunk(S, kv_heads);
         p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
-                       anyway > least ? anyway : least);
-        // the least numbers that are enough: a request of many rows has more than kSmallRows
+                       anyway > kMinChunk ? anyway : kMinChunk);
+        // the fewer tile numbers of two ways that are enough (a request of many rows has
+        // more than kSmallRows): 29 decode rows and 16 tokens take 23 us with 3 per kv
+        // head, 32 with 31
         const long long by_rows = T * G / kSmallRows + 1;
         p.by_rows = by_rows < full + S;
         p.many = divide(p.by_rows ? by_rows : full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
