@@ -1105,10 +1105,10 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // The same with 16 rows per wave and eight waves, for D = 256: 32 rows' sums
 // and q parts leave room for one wave per SIMD only (360 registers), and a
 // lone wave issues every other slot and overlaps nothing (a mixed step of
-// 2,048 tokens: 71 us against 67 when it was tried; at D = 128, where both fit, a prompt of 8,192 tokens
-// took 948 us with 16 rows per wave and 583 with 32).  Lanes as in the few-rows
-// kernel with 64 keys, operands from the LDS.  A prompt of 8,192 tokens, 16/4
-// heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 53 us.  What bounds it
+// 2,048 tokens: 71 us against 67 when it was tried; at D = 128, where both fit, a
+// prompt of 8,192 tokens took 948 us with 16 rows per wave and 583 with 32).
+// Lanes as in the few-rows kernel with 64 keys, operands from the LDS.
+// A prompt of 8,192 tokens, 16/4 heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 53 us.  What bounds it
 // are latencies within a tile, which two waves per SIMD do not hide: a tile takes
 // 5,200 cycles, and 3,900 where one of the eight waves has rows.
 // ---------------------------------------------------------------------------
