@@ -19,7 +19,7 @@
 // Bound by HBM for prompts (q in and out, k and v in, codes out) and by the
 // 64-bit sines, by latency for decode rows.  Measured: 32 decode rows, 16/4 heads
 // of 256 with 64 elements rotated: 7.3 us; 2,048 tokens, of prompts and decode
-// rows: 19.4 us, 2.4 TB/s; 16,384 tokens, 32/8 heads of 128, all rotated: 104 us, 3.6
+// rows: 19.1 us, 2.4 TB/s; 16,384 tokens, 32/8 heads of 128, all rotated: 101 us, 3.7
 // TB/s.
 #include "fp8.h"
 #include "serving_internal.h"
@@ -410,14 +410,16 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
 
     // a window is as many tokens as a page holds; the block takes the rank-th,
     // (rank + ranks)-th ... of the window's tokens that stand for their page,
-    // the first of its new ones.  Rank 0 of all windows comes first, and ranks
-    // are shifted against each other, so that the blocks with work are spread
-    // over the XCDs and CUs whatever their spacing.
+    // the first of its new ones.  Rank 0 of all windows comes first, v's heads
+    // before k's, and ranks are shifted against each other, so that the blocks with
+    // work are spread over the XCDs and CUs whatever their spacing.  (The heads of a
+    // window next to each other give an XCD nothing but k, or v: 16,384 tokens took
+    // 103.5 us and 4,000 decode rows 109, 100.6 and 99 so.)
     const int shift = __builtin_ctz(a.page);
     const unsigned windows = ((unsigned)a.num_tokens + a.page - 1) >> shift, parts = 2 * groups;
-    const unsigned unit = blockIdx.x / parts;
-    const int part = (int)(blockIdx.x - unit * parts), rank = (int)(unit / windows);
-    const int w0 = (int)((unit + 5 * rank) % windows);
+    const unsigned unit = blockIdx.x / windows;
+    const int rank = (int)(unit / parts), part = (int)(parts - 1 - (unit - rank * parts));
+    const int w0 = (int)((blockIdx.x + 5 * rank) % windows);
     const long long slots = (long long)a.num_pages * a.page;
     const int first = w0 * a.page;
     // the slots of the window's tokens and of as many behind them (a page's run
@@ -512,11 +514,11 @@ __global__ __launch_bounds__(kAppendThreads, D == 256 ? 3 : 4) void rope_append_
 // How many blocks share a window: one for every token of it in a small call, so
 // that decode rows run side by side, down to two in a large one: a block costs
 // its start, and most tokens of a prompt continue a page (2,048 tokens: 25 us with
-// four, 19.5 with eight, 23 with 16; a prompt of 16,384: 101 us with one, 107 with
-// two, but then decode rows beside it would be written one after the other).  A q
-// block takes one token while they are few, up to eight as they become many.  (q's
-// blocks first, or between: 23 to 24 us for 2,048 tokens, as the cache's part is
-// the longer chain.)
+// four, 19 with eight, 23 with 16; a prompt of 16,384: 95 us with one and 100 with
+// two, but 8,000 tokens and 500 decode rows, which then go one after the other, 98
+// and 70).  A q block takes one token while they are few, up to eight as they become
+// many.  (q's blocks first, or between: 23 to 24 us for 2,048 tokens, as the cache's
+// part is the longer chain.)
 template <int D>
 static hipError_t launch_append_d(const RopeAppendArgs &a, hipStream_t stream) {
     const int ranks = a.num_tokens <= 512 ? a.page : a.num_tokens <= 4096 ? 8 : 2, q_tokens = min(max(a.num_tokens / 512, 1), 8);
