@@ -70,7 +70,8 @@ __device__ __forceinline__ int last_row(int row, int rows, int n) { return (int)
 // 0, a request of more than `rows` rows owns at least one number per `rows` of
 // them, and the others one at most.  Returns the last request whose first number is at
 // or before `tile` (64 candidates per step), and the tile's place in it.
-__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, bool up, int &within) {
+__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, bool up,
+                                            int &within) {
     const int lane = threadIdx.x & 63;
     int lo = 0, n = a.num_seqs;
     const int add = up ? rows - 1 : 0;
@@ -509,7 +510,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     float ks = 0.f, vs = 0.f;
     auto load_k = [&](int j0, int page) {
         const int j = j0 + NK * kg;
-        const uint8_t *p = a.k_cache + (((long long)(good(page) ? page : 0) * a.num_kv_heads + hk) * a.page + (j & in_page) + (c & 3)) * D + 16 * g;
+        const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
+        const uint8_t *p = a.k_cache + (ph * a.page + (j & in_page) + (c & 3)) * D + 16 * g;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -827,8 +829,8 @@ struct Staging {
 
     __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w, int wave_)
         : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
-          hk(w.hk), wave(wave_), pitch((uint32_t)a_.num_kv_heads * a_.page * D), entry(-1), tile(0), own(-1), s_ks(0.f), s_vs(0.f), k_lo(w.k_lo),
-          met_nan(0) {
+          hk(w.hk), wave(wave_), pitch((uint32_t)a_.num_kv_heads * a_.page * D), entry(-1), tile(0), own(-1), s_ks(0.f),
+          s_vs(0.f), k_lo(w.k_lo), met_nan(0) {
         const WaveKeys all = wave_keys(a, w, w.row0, kManyRows);
         all0 = all.all0;
         all1 = all.all1;

@@ -5,10 +5,6 @@
 
 namespace gdn {
 
-__device__ __forceinline__ bool is_finite(float x) {
-    return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
-}
-
 // four codes from four values, round to nearest even; |x| <= 448, or infinite or
 // NaN: NaN (the format has no infinities)
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
