@@ -19,6 +19,7 @@
 // rows of many (D = 256), a value's conversion would serve few products: there
 // the weights are split as q is, and the codes go in as they are (weigh8).
 // Scores and sums are fp32; the maximum is in units of log2.
+#include "attention_keys.h"
 #include "fp8.h"
 #include "serving_internal.h"
 
@@ -34,13 +35,6 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr int kTileKeys = 64;           // keys a wave takes at once
 constexpr int kTileRows = 16;           // rows of a workgroup of the few-rows kernel
 
-// one request's part in a call, as the kernels see it
-struct Request {
-    int begin, n;       // its first token, and how many
-    int len;            // keys, as seq_lens says (>= 0)
-    int L;              // keys within the block table's row
-};
-
 __device__ __forceinline__ Request request_of(const AttentionArgs &a, int s) {
     Request r;
     int end;
@@ -51,11 +45,8 @@ __device__ __forceinline__ Request request_of(const AttentionArgs &a, int s) {
     return r;
 }
 
-// the keys [jb, je) that token i of the request sees
 __device__ __forceinline__ void key_range(const AttentionArgs &a, const Request &r, int i, int &jb, int &je) {
-    const int upto = r.len - r.n + i + 1;            // its position + 1
-    je = a.causal ? min(r.L, upto) : r.L;
-    jb = a.window > 0 && upto > a.window ? upto - a.window : 0;
+    key_range(a.causal, a.window, r, i, jb, je);
 }
 
 // the token within its request of a row, and the last one of up to `rows` rows
@@ -145,18 +136,6 @@ __device__ __forceinline__ uint32_t key_bytes(int j, int lo, int hi) {
     for (int b = 0; b < 4; ++b)
         if (j + b >= lo && j + b < hi) m |= 0xffu << (8 * b);
     return m;
-}
-
-// The splits of a row tile's keys [lo, hi): split i takes the keys of [i C,
-// (i + 1) C), the last one all that follow.
-struct Splits {
-    int first, last;    // those that have keys (last < first: none)
-};
-__device__ __forceinline__ Splits splits_of(int lo, int hi, int chunk, int n) {
-    Splits s;
-    s.first = min(lo / chunk, n - 1);
-    s.last = hi > lo ? min((hi - 1) / chunk, n - 1) : s.first - 1;
-    return s;
 }
 
 // The larger of the magnitudes of two bf16 pairs, as integers in the same order
@@ -543,7 +522,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     float m = kNegInf, l = 0.f;
     uint32_t met_nan = 0;
     constexpr int step = W * TK;
-    int j0 = (k_lo & ~(TK - 1)) + wave * TK;
+    int j0 = first_tile(k_lo, TK, wave);
     int ek = entry_at(j0 + NK * kg), ev = entry_at(j0 + NK * g), pv = -1;
     // the next tile's keys, and the entries behind it
     auto turn = [&](int j) {
@@ -636,7 +615,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     if (__any(met_nan != 0)) {
         unsigned long long bits[1] = {0};
         find_nan<4 * DT>(
-            a, hk, (k_lo & ~(TK - 1)) + wave * TK, k_hi, step, TK, jb, je, bits,
+            a, hk, first_tile(k_lo, TK, wave), k_hi, step, TK, jb, je, bits,
             [&](int j) { return __any(!good(page_at(j + NK * g))) || j < max(x0, k_lo) || j + TK > min(x1, k_hi); },
             [&](int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }, page_at);
 #pragma unroll
@@ -988,7 +967,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     const int k_row = key * (D / 16), k_swap = k_piece<D>(key, 2 * h2) - k_row, v_swap = v_piece(c, 2 * h2) - 4 * c;
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
-    int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
+    int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
     const bool any = j0 < k_hi;
     if (any) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
@@ -1067,7 +1046,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     if (any && stage.nan_left_out()) {
         unsigned long long bits[(16 * DT + 63) / 64] = {};
         find_nan<16 * DT>(
-            a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
+            a, hk, first_tile(k_lo, kTileKeys, 0), k_hi, kTileKeys, kTileKeys, jb, je, bits,
             [&](int j) { return stage.late(j, stage.page_at(j + 16 * (lane & 3))); },
             [&](int i) { return 32 * (i >> 4) + 8 * (i >> 2 & 3) + 4 * h2 + (i & 3); }, [&](int j) { return stage.page_at(j); });
 #pragma unroll
@@ -1156,7 +1135,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
-    int j0 = k_lo & ~(kTileKeys - 1), buf = 0;
+    int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
     const bool any = j0 < k_hi;
     if (any) stage.begin(j0);
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
@@ -1203,7 +1182,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     if (any && stage.nan_left_out()) {
         unsigned long long bits[1] = {0};
         find_nan<4 * DT>(
-            a, hk, k_lo & ~(kTileKeys - 1), k_hi, kTileKeys, kTileKeys, jb, je, bits,
+            a, hk, first_tile(k_lo, kTileKeys, 0), k_hi, kTileKeys, kTileKeys, jb, je, bits,
             [&](int j) { return stage.late(j, stage.page_at(j + 16 * (lane & 3))); },
             [&](int i) { return 16 * (i >> 2) + 4 * g + (i & 3); }, [&](int j) { return stage.page_at(j); });
 #pragma unroll
