@@ -224,9 +224,10 @@ def _on_gpu(named):
 
 def _workspace(workspace, need, device, stream):
     """The caller's workspace (checked), or one allocated for this call.  An
-    allocated one is marked as used on ``stream`` so that the caching
-    allocator does not hand its memory out again before the call's kernels
-    on that stream are done with it."""
+    allocated one comes from the memory of ``stream`` (the current stream
+    where none is given), to which it also returns: memory that was freed on
+    another stream may still be in use by kernels there, and ``stream`` does
+    not wait for them."""
     torch = _torch()
     if workspace is not None:
         _dtype(workspace, torch.uint8, "workspace")
@@ -234,10 +235,10 @@ def _workspace(workspace, need, device, stream):
         if workspace.numel() < need:
             raise ValueError("workspace of %d bytes, %d needed" % (workspace.numel(), need))
         return workspace
-    ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
 
 
 def _check_conv(x, weight, bias, conv_state, y, rows_name="x"):
