@@ -15,9 +15,10 @@
 // of bf16, and no key is converted.
 //
 // V^T P^T runs on bf16: values are converted in registers (exact), weights
-// rounded to bf16 with their page's value scale in them.  Where a wave has 16
-// rows of many (D = 256), a value's conversion would serve few products: there
-// the weights are split as q is, and the codes go in as they are (weigh8).
+// rounded to bf16 with their page's value scale in them: a light key beside a
+// heavy one keeps its 8 bits.  (Weights in two e4m3 parts with a power of two
+// per 32 keys need no conversion of values, but lose what is below 2^-20 of the
+// heaviest: a prompt of 8,192 tokens with heads of 256 took 589 us so, 596 us now.)
 // Scores and sums are fp32; the maximum is in units of log2.
 #include "attention_keys.h"
 #include "fp8.h"
@@ -234,11 +235,11 @@ constexpr int kLateKeys = 256;
 __device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
-// row) are masked, and the running maximum m, the lane's sum l and the sums o
-// follow.  Returns the lane's own maximum.
+// row) become weights, packed to bf16 pairs with the values' scale in them;
+// the running maximum m, the lane's sum l and the sums o follow.
 template <int NT, int DT>
-__device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs, bool late, bool masked, bool seen_page, int jg,
-                                        int jb, int je, float &m, float &l, f32x4 (&o)[DT]) {
+__device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool late, bool masked, bool seen_page, int jg, int jb,
+                                      int je, float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
     if (masked) {
         // from the row's first and past its last key of these, none of a missing page
         const int from = seen_page ? jb - jg : 4 * NT, to = je - jg;
@@ -262,13 +263,12 @@ __device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs
                     if (x[t][r] != kNegInf) x[t][r] = -x[t][r];
         factor = usable(factor);
     }
-    float own = kNegInf;
+    float mx = kNegInf;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) own = fmaxf(own, x[t][r]);
-    own *= factor;
-    const float mx = max_over32(max_over16(own));
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
+    mx = max_over32(max_over16(mx * factor));
     if (__any(mx > m + slack(vs, late))) {
         const float m_new = fmaxf(m, mx);
         const float f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
@@ -277,14 +277,6 @@ __device__ __forceinline__ float settle(f32x4 (&x)[NT], float &factor, float &vs
 #pragma unroll
         for (int t = 0; t < DT; ++t) o[t] *= f;
     }
-    return own;
-}
-
-// The scores as weights, packed to bf16 pairs with the values' scale in them.
-template <int NT, int DT>
-__device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bool late, bool masked, bool seen_page, int jg, int jb,
-                                      int je, float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[2 * NT]) {
-    settle(x, factor, vs, late, masked, seen_page, jg, jb, je, m, l, o);
     const float at = m == kNegInf ? 0.f : m;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -297,45 +289,6 @@ __device__ __forceinline__ void weigh(f32x4 (&x)[NT], float factor, float vs, bo
         pw[2 * t] = pack_bf16x2(e[0] * vs, e[1] * vs);
         pw[2 * t + 1] = pack_bf16x2(e[2] * vs, e[3] * vs);
     }
-}
-
-// The scores as weights with the values' scale in them, in two e4m3 parts, each
-// divided by a power of two of its block: off by at most 2^-8, as in bf16, or by
-// 2^-22 of the largest one of a block.  Words 0-3 hold the lane's 16 first parts,
-// 4-7 its second ones.  Returns a power's exponent + 127, for the scaled
-// product: there, lanes of groups 0 and 1 share one (their keys are a block of
-// 32), and so do 2 and 3; groups 0 and 1 hold those of the first parts and groups
-// 2 and 3 those of the second ones (measured with one-hot operands).
-template <int DT>
-__device__ __forceinline__ int weigh8(f32x4 (&x)[4], float factor, float vs, bool late, bool masked, bool seen_page, int jg, int jb,
-                                      int je, float &m, float &l, f32x4 (&o)[DT], i32x8 &p) {
-    const float own = settle(x, factor, vs, late, masked, seen_page, jg, jb, je, m, l, o);
-    const float at = m == kNegInf ? 0.f : m;
-    // weights are below 2^(floor(own - at) + 1), the scale's fraction below 1: their
-    // product goes to below 2^8
-    const float ev = vs == 0.f ? -200.f : (float)__builtin_amdgcn_frexp_expf(vs);
-    const float n = fmaxf(max_over16(ev + floorf(fmaxf(own - at, -93.f)) - 7.f), -123.f);
-    const float w = __builtin_amdgcn_ldexpf(__builtin_amdgcn_frexp_mantf(vs), (int)(ev - n));
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        float e[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], factor, -at));
-            l += e[r];
-        }
-        const uint32_t hi = e4m3x4(e[0] * w, e[1] * w, e[2] * w, e[3] * w);
-        const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 16.f, false);
-        const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 16.f, true);
-        p[t] = (int)hi;                // what it leaves is below 2^4: 16 times that
-        p[4 + t] = (int)e4m3x4(__builtin_fmaf(e[0], 16.f * w, -a.x), __builtin_fmaf(e[1], 16.f * w, -a.y),
-                               __builtin_fmaf(e[2], 16.f * w, -b.x), __builtin_fmaf(e[3], 16.f * w, -b.y));
-    }
-    const uint32_t byte = (uint32_t)(n + 127.f);
-    uint32_t other = byte;
-    asm("" : "+v"(other));          // see max_over32
-    const auto r = __builtin_amdgcn_permlane32_swap(byte, other, false, false);
-    return (int)(threadIdx.x & 16 ? r[1] : r[0]) - (threadIdx.x & 32 ? 4 : 0);
 }
 
 // A tile that some of the rows see and others do not cannot pass NaN codes of
@@ -1156,25 +1109,13 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             const int jg = j0 + 16 * g;
             const bool ok = lds.ok[buf][g] != 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
-            // keys 16 g ... 16 g + 15 of the values' operands twice: for the weights' two parts
-            i32x8 p;
-            const int p_scale = weigh8(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], j0 - k_lo >= kLateKeys, masked, ok,
-                                           jg, jb, je, m, l, o, p);
-            auto multiply = [&](int t, const uint4 &u, const uint4 &b) {
-                const i32x8 v8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-                o[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8, p, o[t], 0, 0, 0, 127, 0, p_scale);
-            };
-            struct Twice {
-                uint4 a, b;
-            };
-            run_ahead<DT, kNarrowAhead>(
-                [&](int t) {
-                    // read twice: the LDS has time, copies would take the vector unit's
-                    const uint4 a = vt[16 * 4 * t];
-                    asm volatile("" ::: "memory");
-                    return Twice{a, vt[16 * 4 * t]};
-                },
-                [&](int t, const Twice &w) { multiply(t, w.a, w.b); });
+            uint32_t pw[8];
+            weigh(x, to_log2 * lds.ks[buf][g], lds.vs[buf][g], j0 - k_lo >= kLateKeys, masked, ok, jg, jb, je, m, l, o, pw);
+            const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+            run_ahead<DT, kNarrowAhead>([&](int t) { return vt[16 * 4 * t]; }, [&](int t, const uint4 &w) {
+                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(w.x, w.y), p0, o[t], 0, 0, 0);
+                o[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_to_bf16(w.z, w.w), p1, o[t], 0, 0, 0);
+            });
         }
         stage.next(j0, buf);
     }

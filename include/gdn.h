@@ -673,9 +673,9 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * Scores are products of the cache's codes with q in two 8-bit parts (exact
  * for elements of at least 2^-10 of their head's largest, within 2^-18 of that
  * largest for smaller ones), summed in fp32; softmax statistics and sums are
- * fp32.  In its product with a value a weight is off by at most 2^-8 of itself
- * (bf16) or, with the values' scale in it, by 2^-22 of the largest among 32
- * neighbouring keys; o is rounded to bf16.  A token that sees a key of a page
+ * fp32.  A weight is rounded to bf16 in its product with a value, with the
+ * values' scale in it: off by at most 2^-8 of itself, however light beside
+ * others.  o is rounded to bf16.  A token that sees a key of a page
  * whose v_scale is infinite or NaN gets infinite or NaN elements there.
  * Results do not change from call to call (no atomics).
  *
