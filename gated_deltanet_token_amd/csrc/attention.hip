@@ -7,12 +7,17 @@
 // a kv head.
 //
 // K Q^T runs on e4m3 operands.  The cache's codes go into the matrix cores as
-// they lie in memory, and q is split into two e4m3 parts, q = (hi + lo) / f
+// they lie in memory, and q is split into two e4m3 parts, q = (hi + lo / 32) / f
 // with f a power of two that brings the row's largest element to [128, 256):
-// hi keeps 4 significant bits, lo the other 4 of a bf16 value.  The split is
-// exact for elements down to 2^-10 of the row's largest, and within 2^-18 of
-// that for smaller ones.  Two products of 8-bit operands take as long as one
-// of bf16, and no key is converted.
+// hi keeps 4 significant bits, lo the other 4 of a bf16 value, at most 8 and 32
+// times that in its operand.  The split is exact for elements down to 2^-14 of
+// the row's largest, where lo is 2^-9 or a multiple, and within 2^-22 of that for
+// smaller ones (2^-9 and 2^-17 if lo were not taken 32-fold).  Two products of
+// 8-bit operands take as long as one of bf16, and no key is converted.  The 32
+// goes back out as a power of two of lo's product in waves of 32 rows, where
+// that costs nothing, and by sums of lo's own, an fma per score, in waves of 16 (a
+// prompt of 8,192 tokens, heads of 256: 614 us, 645 by scaled products, 600 without
+// the 32; heads of 128: 572 with it and without).
 //
 // V^T P^T runs on bf16: values are converted in registers (exact), weights
 // rounded to bf16 with their page's value scale in them: a light key beside a
@@ -157,7 +162,9 @@ __device__ __forceinline__ float split_factor(float m) {
     const int ex = max((int)(__builtin_bit_cast(uint32_t, m) >> 23), 8);
     return __builtin_bit_cast(float, (uint32_t)(261 - ex) << 23);
 }
-// four elements' two parts
+// four elements' two parts, the second one 32-fold
+constexpr float kLowTimes = 32.f;
+constexpr int kWhole = 127, kLowPart = 127 - 5;         // 1 and 1 / 32 as powers of two of a scaled product
 __device__ __forceinline__ void split4(const float *f, float up, int &hi, int &lo) {
     float v[4], b[4];
 #pragma unroll
@@ -165,7 +172,7 @@ __device__ __forceinline__ void split4(const float *f, float up, int &hi, int &l
     const uint32_t w = e4m3x4(v[0], v[1], v[2], v[3]);
     e4m3_values(w, b);
     hi = (int)w;
-    lo = (int)e4m3x4(v[0] - b[0], v[1] - b[1], v[2] - b[2], v[3] - b[3]);
+    lo = (int)e4m3x4(kLowTimes * (v[0] - b[0]), kLowTimes * (v[1] - b[1]), kLowTimes * (v[2] - b[2]), kLowTimes * (v[3] - b[3]));
 }
 
 // A lane's elements of one row, for lanes of 16 rows: 64 l + 16 g + e.
@@ -510,11 +517,16 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         __syncthreads();
     }
 
+    // At D = 64 one product takes both parts.  Its powers are those of 32 elements
+    // in a row: the lanes of groups 0 and 1 hold those of the lower 16 bytes, groups
+    // 2 and 3 those of the upper ones (measured with one-hot operands).
+    [[maybe_unused]] const int both = g < 2 ? kWhole : kLowPart;
+
     for (; j0 < k_hi; j0 += step) {
         const int jn = j0 + step;
         int pv_n = -1;
         // X^T: keys NK g + 4 t + r of row c
-        f32x4 x[NT] = {};
+        f32x4 x[NT] = {}, y[NT] = {};
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
             i32x8 hi8 = qh[st], lo8 = ql[st];
@@ -528,10 +540,19 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
             for (int t = 0; t < NT; ++t) {
                 const uint4 u = kr[t][D == 64 ? 0 : 2 * st], w = kr[t][D == 64 ? 0 : 2 * st + 1];
                 const i32x8 k8 = {(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)w.x, (int)w.y, (int)w.z, (int)w.w};
-                x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, hi8, x[t], 0, 0, 0, 0, 0, 0);
-                if constexpr (D != 64)
-                    x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, lo8, x[t], 0, 0, 0, 0, 0, 0);
+                if constexpr (D == 64) {
+                    x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, hi8, x[t], 0, 0, 0, kWhole, 0, both);
+                } else {
+                    x[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, hi8, x[t], 0, 0, 0, 0, 0, 0);
+                    y[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, lo8, y[t], 0, 0, 0, 0, 0, 0);
+                }
             }
+        }
+        if constexpr (D != 64) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(y[t][r], 1.f / kLowTimes, x[t][r]);
         }
         if (jn < k_hi) pv_n = turn(jn);
         asm volatile("" ::: "memory");
@@ -942,7 +963,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                     },
                     [&](int st, const i32x8 &k8) {
                         x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, qh[st], x, 0, 0, 0, 0, 0, 0);
-                        x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x, 0, 0, 0, 0, 0, 0);
+                        x = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k8, ql[st], x, 0, 0, 0, kWhole, 0, kLowPart);
                     });
                 const bool ok = ok01[t];
                 float mx = kNegInf, factor = to_log2 * lds.ks[buf][2 * h2 + t], vs = lds.vs[buf][2 * h2 + t];
@@ -1095,7 +1116,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
         const int jn = j0 + kTileKeys;
         stage.ahead(j0);
         if (j0 < wk.hi && jn > wk.lo) {
-            f32x4 x[4] = {};
+            f32x4 x[4] = {}, y[4] = {};
             const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + 4 * c + v_swap;
             auto k_operand = [&](int i) {
                 const int t = i / KS, st = i % KS;
@@ -1104,8 +1125,12 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             };
             run_ahead<4 * KS, kNarrowAhead>(k_operand, [&](int i, const i32x8 &k8) {
                 x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, qh[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
-                x[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], x[i / KS], 0, 0, 0, 0, 0, 0);
+                y[i / KS] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(k8, ql[i % KS], y[i / KS], 0, 0, 0, 0, 0, 0);
             });
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[t][r] = __builtin_fmaf(y[t][r], 1.f / kLowTimes, x[t][r]);
             const int jg = j0 + 16 * g;
             const bool ok = lds.ok[buf][g] != 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);

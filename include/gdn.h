@@ -671,7 +671,7 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * bytes past L are free to hold anything.
  *
  * Scores are products of the cache's codes with q in two 8-bit parts (exact
- * for elements of at least 2^-10 of their head's largest, within 2^-18 of that
+ * for elements of at least 2^-14 of their head's largest, within 2^-22 of that
  * largest for smaller ones), summed in fp32; softmax statistics and sums are
  * fp32.  A weight is rounded to bf16 in its product with a value, with the
  * values' scale in it: off by at most 2^-8 of itself, however light beside
