@@ -679,6 +679,13 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * whose v_scale is infinite or NaN gets infinite or NaN elements there.
  * Results do not change from call to call (no atomics).
  *
+ * With at most as many tokens as requests (num_tokens <= num_seqs) the call
+ * takes each request for a few rows, as a decode step's are.  Requests without
+ * new tokens count there: a prompt in a batch padded with empty ones up to that
+ * point is right but slower (2,000 tokens among 2,000 requests: 171 us at heads
+ * of 256 and 195 us at 128; among 1,999: 92 and 79 us; alone: 84 and 62 us).  Leave
+ * empty requests out of num_seqs where prompts are among the others.
+ *
  *   q            bf16, token t head h at q + t*q_stride + h*head_dim
  *   block_table  int32 [num_seqs][block_table_stride], max_pages entries used
  *   seq_lens     int32 [num_seqs] (negative counts as 0)
