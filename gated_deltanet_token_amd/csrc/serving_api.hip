@@ -202,6 +202,10 @@ GDN_EXPORT int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, cons
     if (rc) return rc;
     if (num_q_heads < 1 || num_q_heads % num_kv_heads)
         return fail(GDN_ERR_INVALID, "num_q_heads must be a positive multiple of num_kv_heads");
+    // offsets within a page are 32-bit where prompts are read
+    if ((int64_t)num_kv_heads * page_size * head_dim > 0x7fffffff)
+        return fail(GDN_ERR_UNSUPPORTED, "a page of %d heads x %d tokens x %d elements passes 2^31 - 1 bytes", num_kv_heads, page_size,
+                    head_dim);
     if (max_pages < 1 || block_table_stride < max_pages)
         return fail(GDN_ERR_INVALID, "max_pages must be >= 1 and at most block_table_stride");
     if (max_pages > (0x7fffffff - 1024) / page_size)     // key numbers, a few tiles past the end too, are 32-bit

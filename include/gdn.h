@@ -702,8 +702,9 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * Errors: GDN_ERR_INVALID (required pointer NULL, negative counts,
  * num_q_heads not a positive multiple of num_kv_heads, num_pages or max_pages
  * < 1, max_seq_len < 1, window < 0, strides too small, o or the workspace
- * overlapping an operand); GDN_ERR_UNSUPPORTED (page_size, head_dim,
- * alignment contract); GDN_ERR_CAPACITY (workspace too small); GDN_ERR_HIP.
+ * overlapping an operand); GDN_ERR_UNSUPPORTED (page_size, head_dim, a page of
+ * all heads or a row of max_pages pages past 32-bit offsets, alignment
+ * contract); GDN_ERR_CAPACITY (workspace too small); GDN_ERR_HIP.
  */
 size_t gdn_paged_attention_kv8_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                                               int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
