@@ -35,8 +35,8 @@ def want(c, causal=True, window=0):
             see = see & (j > pos - window)
         at = np.where((ids >= 0) & (ids < c.kq.shape[0]), ids, 0)
         for h in range(HK):
-            K = c.kq[at, h, j % page] * np.float64(c.ks[at, h])[:, None]
-            V = c.vq[at, h, :, j % page] * np.float64(c.vs[at, h])[:, None]
+            K = c.kq[at, h, j % page] * c.ks[at, h].astype(np.float64)[:, None]
+            V = c.vq[at, h, :, j % page] * c.vs[at, h].astype(np.float64)[:, None]
             bad = np.isnan(V)
             for g in range(h * G, h * G + G):
                 x = np.where(see, c.scale * (q[a:b, g] @ K.T), -np.inf)
