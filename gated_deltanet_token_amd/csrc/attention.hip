@@ -235,9 +235,10 @@ __device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0
 // to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
 // row of a wave, hardly any such a one (a prompt of 8,192 tokens, heads of 128: 589
 // us with none, 573).  None is let through where the values' scale is so large
-// that weight times scale or their sum could pass fp32's end, nor in a wave's first
-// kLateKeys keys: of few keys the heaviest often makes up the sum, and its weight
-// of 1 is exact.
+// that weight times scale or their sum could pass fp32's end, nor in the first
+// kLateKeys keys of a workgroup's part: of few keys the heaviest often makes up
+// the sum, and its weight of 1 is exact.  (A wave that begins behind them begins
+// with its first tile's maximum, too.)
 constexpr int kLateKeys = 256;
 __device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 

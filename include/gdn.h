@@ -581,7 +581,10 @@ typedef enum gdn_rope_scaling {
  * for the scalings: with r_i = original_context f_i / 2pi turns over the
  * original context, f_i gamma + (f_i / factor) (1 - gamma), gamma = clamp((r_i
  * - beta_slow) / (beta_fast - beta_slow), 0, 1), and the factor 0.1 ln(factor)
- * + 1.
+ * + 1.  The ramp is that paper's, linear in turns.  A model that was trained with
+ * another one (linear in the pair's number i between the two borders, rounded or
+ * not) has other frequencies: pass its own to gdn_rope_append_kv8, which takes
+ * any, with its own factor.
  *
  *   out           host, double [rotary_dim / 2]
  *   rope_scale    host, receives the factor
@@ -675,8 +678,10 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  * largest for smaller ones), summed in fp32; softmax statistics and sums are
  * fp32.  A weight is rounded to bf16 in its product with a value, with the
  * values' scale in it: off by at most 2^-8 of itself, however light beside
- * others.  o is rounded to bf16.  A token that sees a key of a page
- * whose v_scale is infinite or NaN gets infinite or NaN elements there.
+ * others, while that product is above bf16's least normal value, 2^-126.  o is
+ * rounded to bf16.  Its sums are finite where the keys seen times the largest
+ * magnitude among their values stay below 2^128.  A token that sees a key of a
+ * page whose v_scale is infinite or NaN gets infinite or NaN elements there.
  * Results do not change from call to call (no atomics).
  *
  * With at most as many tokens as requests (num_tokens <= num_seqs) the call
@@ -724,7 +729,8 @@ int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, const uint8_t *
  * gate (the GDN mixer's output norm; without a gate, the norm of q and k
  * heads):
  *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight) * silu(gate)
- * over head_dim elements, in fp32, rounded once.
+ * over head_dim elements, in fp32, rounded once.  (A head whose sum of squares
+ * passes fp32's range, with elements of 2^60 and more, comes out as zeros.)
  *
  *   x, gate, y  bf16, token t head h at x + t*x_stride + h*head_dim; gate may
  *               be NULL; y may be x itself with the same stride
@@ -746,7 +752,7 @@ int gdn_gated_rms_norm(const gdn_bf16 *x, int64_t x_stride, const gdn_bf16 *gate
  *   h = residual + residual_scale * u;  new_residual = h (rounded to bf16)
  *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
  * in fp32; y is formed from h before its rounding, so the sum's rounding does
- * not enter the next block.
+ * not enter the next block.  (Sums of squares past fp32's range: as above.)
  *
  *   x, residual, gate, new_residual, y  bf16 [rows][stride], hidden elements
  *               used; gate may be NULL; new_residual may be residual or x, and
