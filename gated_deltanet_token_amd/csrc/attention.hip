@@ -363,7 +363,7 @@ __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int
 // TK is 64; at D = 256, 32, so that two tiles and the sums fit a lane's 256
 // registers (with 64 keys and no tile ahead a decode step of 32 requests took
 // 25.0 us).
-// Measured: 32 requests of 1,100 tokens, 16/4 heads of 256: 20.8 us, half of it start
+// Measured: 32 requests of 1,100 tokens, 16/4 heads of 256: 20 to 22 us, half of it start
 // and end; five of 40,000 to 131,000, 32/8 heads of 128: 188 us, 5.9 TB/s, and 6 us to
 // join the parts.
 // ---------------------------------------------------------------------------
@@ -652,8 +652,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the matrix cores and the exponentials: tiles of 64 keys and values pass
 // through the LDS once for all four waves, the next one on its way from HBM
 // to registers meanwhile, with one barrier per tile between two buffers.
-// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 562 us on one card and 618
-// on another, 980 and 890 TFLOP/s (4 D per row and key it sees).  Vector and matrix instructions hardly overlap here: an
+// Measured: a prompt of 8,192 tokens, 32/8 heads of 128: 552 to 618 us, by card,
+// 996 to 890 TFLOP/s (4 D per row and key it sees).  Vector and matrix instructions hardly overlap here: an
 // operation takes 2.4 cycles of a SIMD, an exponential 8, a pair of values'
 // conversion 4, a matrix product 32 of which it hides 10; their sum over a tile is
 // what a tile takes.  (Values converted once for the workgroup, on their way to the
@@ -1064,9 +1064,9 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // 2,048 tokens: 71 us against 67 when it was tried; at D = 128, where both fit, a
 // prompt of 8,192 tokens took 948 us with 16 rows per wave and 583 with 32).
 // Lanes as in the few-rows kernel with 64 keys, operands from the LDS.
-// A prompt of 8,192 tokens, 16/4 heads of 256: 571 to 615 us, by card; a mixed step of 2,048: 53 us.  What bounds it
-// are latencies within a tile, which two waves per SIMD do not hide: a tile takes
-// 5,200 cycles, and 3,900 where one of the eight waves has rows.
+// A prompt of 8,192 tokens, 16/4 heads of 256: 598 to 615 us; a mixed step of 2,048:
+// 55 to 57 us.  What bounds it are latencies within a tile, which two waves per SIMD
+// do not hide: one of the eight waves alone takes three quarters of a tile's time.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowThreads = 512;
 constexpr int kNarrowAhead = 3;
