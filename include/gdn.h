@@ -696,7 +696,8 @@ int gdn_rope_append_kv8(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, 
  *   seq_lens     int32 [num_seqs] (negative counts as 0)
  *   max_seq_len  the largest of seq_lens as the caller knows it; it decides
  *                how the work is split, and results do not depend on it but
- *                for rounding (0 < it; a request may be longer)
+ *                for rounding (0 < it; a request may be longer).  A bound far
+ *                above the lengths costs time: parts come out too long, and few
  *   o            bf16 [.][o_stride], rows of tokens that no request owns are
  *                left as they are; must not overlap an input
  *   workspace    device scratch of gdn_paged_attention_kv8_workspace_size
