@@ -31,6 +31,8 @@ EXPORTS = ("gdn_last_error", "gdn_build_conv_chunks", "gdn_causal_conv1d_varlen"
            "gdn_chunk_rule_and_fused_decode_noalloc",
            "gdn_build_step_tables", "gdn_rope_frequencies", "gdn_rope_append_kv8",
            "gdn_paged_attention_kv8_workspace_size", "gdn_paged_attention_kv8",
+           "gdn_rope_append_kv4", "gdn_paged_read_kv4",
+           "gdn_paged_attention_kv4_workspace_size", "gdn_paged_attention_kv4",
            "gdn_gated_rms_norm", "gdn_residual_rms_norm")
 # bytes of the static device scratch gdn_chunk_rule_and_fused_decode_noalloc uses (gdn.h)
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -84,6 +86,11 @@ def _bind(path):
     lib.gdn_paged_attention_kv8_workspace_size.restype = size
     lib.gdn_paged_attention_kv8.argtypes = [P, i64, P, P, P, P, i32, i32, P, i64, i32, P, P, i32, P, i64,
                                             i32, i32, i32, i32, i32, f32, i32, i32, P, size, P]
+    lib.gdn_rope_append_kv4.argtypes = lib.gdn_rope_append_kv8.argtypes
+    lib.gdn_paged_read_kv4.argtypes = [P, P, P, P, i32, i32, P, i64, i32, P, P, P, i64, P, i64, i32, i32, i32, i32, P]
+    lib.gdn_paged_attention_kv4_workspace_size.argtypes = [i32] * 6
+    lib.gdn_paged_attention_kv4_workspace_size.restype = size
+    lib.gdn_paged_attention_kv4.argtypes = lib.gdn_paged_attention_kv8.argtypes
     lib.gdn_gated_rms_norm.argtypes = [P, i64, P, i64, P, P, i64, i32, i32, i32, f32, f32, P]
     lib.gdn_residual_rms_norm.argtypes = [P, i64, P, i64, P, P, i64, P, P, i64, P, i64, i32, i32, f32, f32, f32, P]
     return lib
@@ -650,19 +657,31 @@ def _bf16_heads(t, T, H, d, name):
     return _head_stride(shape, t.stride(), name)
 
 
-def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale,
-                        interleaved=False, rope_scale=1.0, stream=None):
-    """Rotary positions on q and k, and k and v written into the 8-bit paged
-    cache; see gdn.h.
+def _kv4(k_cache, v_cache, k_scale, v_scale):
+    """dtypes and shapes of the 4-bit paged cache; returns (pages, HK, page, D)."""
+    u8 = torch.uint8
+    if k_cache.dtype != u8 or v_cache.dtype != u8 or k_scale.dtype != u8:
+        raise TypeError("k_cache, v_cache and k_scale must be torch.uint8, got %s, %s and %s"
+                        % (k_cache.dtype, v_cache.dtype, k_scale.dtype))
+    if v_scale.dtype != torch.bfloat16:
+        raise TypeError("v_scale must be torch.bfloat16, got %s" % v_scale.dtype)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages][HK][page][D / 2], got shape %s" % (tuple(k_cache.shape),))
+    n, hk, page, half = k_cache.shape
+    d = 2 * half
+    if v_cache.shape != (n, hk, page // 16, d, 8):
+        raise ValueError("v_cache must have shape %s, got %s" % ((n, hk, page // 16, d, 8), tuple(v_cache.shape)))
+    if k_scale.shape != (n, hk, d // 32, page) or v_scale.shape != (n, hk, page):
+        raise ValueError("k_scale and v_scale must have shapes %s and %s, got %s and %s"
+                         % ((n, hk, d // 32, page), (n, hk, page), tuple(k_scale.shape), tuple(v_scale.shape)))
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("k_cache, v_cache, k_scale and v_scale must be contiguous")
+    return n, hk, page, d
 
-    q, q_out: bf16 [T][HQ][D], or both None; q_out may be q; k, v: bf16
-    [T][HK][D] (token rows may be strided views of one projection's output);
-    positions int32 [T]; slot_mapping int64 [T]; frequencies float64
-    [rotary_dim / 2] on the GPU, or None for no rotation; k_cache
-    float8_e4m3fn [pages][HK][page][D]; v_cache [pages][HK][D][page]; k_scale,
-    v_scale fp32 [pages][HK] (all four in place).
-    """
-    n, hk, page, d = _kv8(k_cache, v_cache, k_scale, v_scale)
+
+def _rope_append(call, name, shape, q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale,
+                 v_scale, interleaved, rope_scale, stream):
+    n, hk, page, d = shape
     T = k.shape[0]
     ks, vs = _bf16_heads(k, T, hk, d, "k"), _bf16_heads(v, T, hk, d, "v")
     hq = qs = os_ = 0
@@ -683,7 +702,68 @@ def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_
             n, page, T, hq, hk, d)
     dev = _on_current("k v positions slot_mapping frequencies k_cache v_cache k_scale v_scale q q_out", k, v, positions,
                       slot_mapping, frequencies, k_cache, v_cache, k_scale, v_scale, q, q_out)
-    _check(lib.gdn_rope_append_kv8(*args, _stream_on(stream, dev)), "gdn_rope_append_kv8")
+    _check(call(*args, _stream_on(stream, dev)), name)
+
+
+def gdn_rope_append_kv8(q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale,
+                        interleaved=False, rope_scale=1.0, stream=None):
+    """Rotary positions on q and k, and k and v written into the 8-bit paged
+    cache; see gdn.h.
+
+    q, q_out: bf16 [T][HQ][D], or both None; q_out may be q; k, v: bf16
+    [T][HK][D] (token rows may be strided views of one projection's output);
+    positions int32 [T]; slot_mapping int64 [T]; frequencies float64
+    [rotary_dim / 2] on the GPU, or None for no rotation; k_cache
+    float8_e4m3fn [pages][HK][page][D]; v_cache [pages][HK][D][page]; k_scale,
+    v_scale fp32 [pages][HK] (all four in place).
+    """
+    _rope_append(lib.gdn_rope_append_kv8, "gdn_rope_append_kv8", _kv8(k_cache, v_cache, k_scale, v_scale), q, k, v,
+                 positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale, interleaved, rope_scale,
+                 stream)
+
+
+def gdn_rope_append_kv4(q, k, v, positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale,
+                        interleaved=False, rope_scale=1.0, stream=None):
+    """Rotary positions on q and k, and k and v written into the 4-bit paged
+    cache; see gdn.h.
+
+    As gdn_rope_append_kv8, with k_cache uint8 [pages][HK][page][D / 2],
+    v_cache uint8 [pages][HK][page / 16][D][8], k_scale uint8
+    [pages][HK][D / 32][page] and v_scale bf16 [pages][HK][page] (all four in
+    place).
+    """
+    _rope_append(lib.gdn_rope_append_kv4, "gdn_rope_append_kv4", _kv4(k_cache, v_cache, k_scale, v_scale), q, k, v,
+                 positions, slot_mapping, frequencies, q_out, k_cache, v_cache, k_scale, v_scale, interleaved, rope_scale,
+                 stream)
+
+
+def gdn_paged_read_kv4(k_cache, v_cache, k_scale, v_scale, block_table, key_starts, out_start_loc, k_out, v_out,
+                       stream=None):
+    """Ranges of keys and values out of the 4-bit paged cache; see gdn.h.
+
+    The cache as gdn_rope_append_kv4 leaves it; block_table int32
+    [S][max_pages]; key_starts int32 [S] or None (from key 0 on);
+    out_start_loc int32 [S+1]; k_out, v_out: bf16 [R][HK][D] (rows may be
+    strided), one of them may be None.
+    """
+    n, hk, page, d = _kv4(k_cache, v_cache, k_scale, v_scale)
+    if k_out is None and v_out is None:
+        raise ValueError("k_out or v_out is required")
+    R = (v_out if k_out is None else k_out).shape[0]
+    ks = 0 if k_out is None else _bf16_heads(k_out, R, hk, d, "k_out")
+    vs = 0 if v_out is None else _bf16_heads(v_out, R, hk, d, "v_out")
+    _dims(out_start_loc, 1, "out_start_loc")
+    S = out_start_loc.shape[0] - 1
+    if S < 0:
+        raise ValueError("out_start_loc must have an entry per request and one more")
+    _table(block_table, S)
+    args = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
+            block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
+            None if key_starts is None else _vector(key_starts, torch.int32, S, "key_starts"),
+            _vector(out_start_loc, torch.int32, S + 1, "out_start_loc"), _ptr(k_out), ks, _ptr(v_out), vs, S, R, hk, d)
+    dev = _on_current("k_cache v_cache k_scale v_scale block_table key_starts out_start_loc k_out v_out", k_cache, v_cache,
+                      k_scale, v_scale, block_table, key_starts, out_start_loc, k_out, v_out)
+    _check(lib.gdn_paged_read_kv4(*args, _stream_on(stream, dev)), "gdn_paged_read_kv4")
 
 
 def gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
@@ -691,6 +771,42 @@ def gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, nu
     """Bytes of device scratch gdn_paged_attention_kv8 needs."""
     return int(lib.gdn_paged_attention_kv8_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
                                                           max_seq_len))
+
+
+def gdn_paged_attention_kv4_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                           max_seq_len) -> int:
+    """Bytes of device scratch gdn_paged_attention_kv4 needs."""
+    return int(lib.gdn_paged_attention_kv4_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                                          max_seq_len))
+
+
+def _table(block_table, S):
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
+    if block_table.dim() != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must have %d rows, got shape %s" % (S, tuple(block_table.shape)))
+
+
+def _paged_attention(call, size, name, shape, q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+                     query_start_loc, o, max_seq_len, scale, causal, window, workspace, stream):
+    n, hk, page, d = shape
+    _dims(q, 3, "q")
+    T, hq = q.shape[0], q.shape[1]
+    qs, os_ = _bf16_heads(q, T, hq, d, "q"), _bf16_heads(o, T, hq, d, "o")
+    _dims(seq_lens, 1, "seq_lens")
+    S = seq_lens.shape[0]
+    _table(block_table, S)
+    args = (q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
+            block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
+            _vector(seq_lens, torch.int32, S, "seq_lens"),
+            _vector(query_start_loc, torch.int32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
+            d, scale, 1 if causal else 0, window)
+    dev = _on_current("q k_cache v_cache k_scale v_scale block_table seq_lens query_start_loc o workspace", q, k_cache,
+                      v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o, workspace)
+    need = size(T, S, hq, hk, d, max_seq_len)
+    if need or workspace is not None:
+        workspace = _workspace(workspace, need, q.device, stream)
+    _check(call(*args, _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream_on(stream, dev)), name)
 
 
 def gdn_paged_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o,
@@ -704,28 +820,22 @@ def gdn_paged_attention_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     gdn_paged_attention_kv8_workspace_size(...) bytes; when omitted, torch
     allocates one for the call where it is needed.
     """
-    n, hk, page, d = _kv8(k_cache, v_cache, k_scale, v_scale)
-    _dims(q, 3, "q")
-    T, hq = q.shape[0], q.shape[1]
-    qs, os_ = _bf16_heads(q, T, hq, d, "q"), _bf16_heads(o, T, hq, d, "o")
-    _dims(seq_lens, 1, "seq_lens")
-    S = seq_lens.shape[0]
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError("block_table must have %d rows, got shape %s" % (S, tuple(block_table.shape)))
-    args = (q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
-            block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
-            _vector(seq_lens, torch.int32, S, "seq_lens"),
-            _vector(query_start_loc, torch.int32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
-            d, scale, 1 if causal else 0, window)
-    dev = _on_current("q k_cache v_cache k_scale v_scale block_table seq_lens query_start_loc o workspace", q, k_cache,
-                      v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o, workspace)
-    need = lib.gdn_paged_attention_kv8_workspace_size(T, S, hq, hk, d, max_seq_len)
-    if need or workspace is not None:
-        workspace = _workspace(workspace, need, q.device, stream)
-    _check(lib.gdn_paged_attention_kv8(*args, _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                       _stream_on(stream, dev)), "gdn_paged_attention_kv8")
+    _paged_attention(lib.gdn_paged_attention_kv8, lib.gdn_paged_attention_kv8_workspace_size, "gdn_paged_attention_kv8",
+                     _kv8(k_cache, v_cache, k_scale, v_scale), q, k_cache, v_cache, k_scale, v_scale, block_table,
+                     seq_lens, query_start_loc, o, max_seq_len, scale, causal, window, workspace, stream)
+
+
+def gdn_paged_attention_kv4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o,
+                            max_seq_len, scale, causal=True, window=0, workspace=None, stream=None):
+    """Attention of a step's tokens over the 4-bit paged cache; see gdn.h.
+
+    As gdn_paged_attention_kv8, over the cache as gdn_rope_append_kv4 leaves
+    it, with a ``workspace`` of gdn_paged_attention_kv4_workspace_size(...)
+    bytes; when omitted, torch allocates one for the call where it is needed.
+    """
+    _paged_attention(lib.gdn_paged_attention_kv4, lib.gdn_paged_attention_kv4_workspace_size, "gdn_paged_attention_kv4",
+                     _kv4(k_cache, v_cache, k_scale, v_scale), q, k_cache, v_cache, k_scale, v_scale, block_table,
+                     seq_lens, query_start_loc, o, max_seq_len, scale, causal, window, workspace, stream)
 
 
 def gdn_gated_rms_norm(x, weight, y, gate=None, eps=1e-6, weight_offset=0.0, stream=None):

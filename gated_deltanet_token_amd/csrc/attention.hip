@@ -25,83 +25,10 @@
 // per 32 keys need no conversion of values, but lose what is below 2^-20 of the
 // heaviest: a prompt of 8,192 tokens with heads of 256 took 589 us so, 596 us now.)
 // Scores and sums are fp32; the maximum is in units of log2.
-#include "attention_keys.h"
+#include "attention_split.h"
 #include "fp8.h"
-#include "serving_internal.h"
 
 namespace gdn {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegInf = -__builtin_inff();
-constexpr int kTileKeys = 64;           // keys a wave takes at once
-constexpr int kTileRows = 16;           // rows of a workgroup of the few-rows kernel
-
-__device__ __forceinline__ Request request_of(const AttentionArgs &a, int s) {
-    Request r;
-    int end;
-    clamp_range(a.qsl[s], a.qsl[s + 1], a.num_tokens, r.begin, end);
-    r.n = end - r.begin;
-    r.len = max(a.seq_lens[s], 0);
-    r.L = (int)min((long long)r.len, (long long)a.max_pages * a.page);
-    return r;
-}
-
-__device__ __forceinline__ void key_range(const AttentionArgs &a, const Request &r, int i, int &jb, int &je) {
-    key_range(a.causal, a.window, r, i, jb, je);
-}
-
-// the token within its request of a row, and the last one of up to `rows` rows
-// from `row` on, of n
-__device__ __forceinline__ int token_of(int row, int G) { return (int)((unsigned)row / (unsigned)G); }
-__device__ __forceinline__ int last_row(int row, int rows, int n) { return (int)min((unsigned)row + rows, (unsigned)n) - 1; }
-
-// Row tiles without a list: request s owns the tile numbers from
-// floor(query_start_loc[s] * G / rows) + s * each on, G rows per token.  With
-// each = 1 that is as many as it needs or more, with each = 0 as many as it
-// needs behind its first one.  `up` rounds the first number up: then, with each =
-// 0, a request of more than `rows` rows owns at least one number per `rows` of
-// them, and the others one at most.  Returns the last request whose first number is at
-// or before `tile` (64 candidates per step), and the tile's place in it.
-__device__ __forceinline__ int find_request(const AttentionArgs &a, long long tile, int group, int rows, int each, bool up,
-                                            int &within) {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, n = a.num_seqs;
-    const int add = up ? rows - 1 : 0;
-    auto first = [&](int s) { return (long long)(((unsigned long long)max(a.qsl[s], 0) * group + add) / rows) + s * each; };
-    while (n > 1) {
-        const int step = (n + 63) / 64;
-        const bool in = lane * step < n && first(lo + lane * step) <= tile;
-        const unsigned long long b = __ballot(in);
-        const int k = b ? 63 - __builtin_clzll(b) : 0;
-        lo += k * step;
-        n = min(step, n - k * step);
-    }
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    within = (int)(tile - first(lo));
-    return lo;
-}
-
-// The larger of a lane's value and that of the lane 32 (16) further or back: the
-// swap of half-waves (of neighbouring rows of 16) between two copies leaves both
-// lanes' values in each.  (The compiler must not see that they are copies: it
-// then takes the two results for equal.)
-__device__ __forceinline__ float max_over32(float x) {
-    uint32_t u = __builtin_bit_cast(uint32_t, x), v = u;
-    asm("" : "+v"(v));
-    const auto r = __builtin_amdgcn_permlane32_swap(u, v, false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
-}
-__device__ __forceinline__ float max_over16(float x) {
-    uint32_t u = __builtin_bit_cast(uint32_t, x), v = u;
-    asm("" : "+v"(v));
-    const auto r = __builtin_amdgcn_permlane16_swap(u, v, false, false);
-    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
-}
 
 // 8 codes -> 8 bf16 values
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w0, uint32_t w1) {
@@ -109,12 +36,6 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w0, uint32_t w1) {
                      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true)),
                      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false)),
                      __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true))};
-    return __builtin_bit_cast(bf16x8, v);
-}
-
-// 8 bf16 from packed pairs
-__device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    const i32x4 v = {(int)a, (int)b, (int)c, (int)d};
     return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -230,17 +151,6 @@ __device__ __forceinline__ void split_q16(const Row16<D> &q, float up, i32x8 (&q
 // so that it keeps a masked score at -infinity.
 __device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0x1p-126f : factor < 0.f ? -factor : factor; }
 
-// The sums are brought to a row's new maximum only where that is more than this
-// above the maximum m that they are relative to (in units of log2): weights up
-// to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
-// row of a wave, hardly any such a one (a prompt of 8,192 tokens, heads of 128: 589
-// us with none, 573).  None is let through where the values' scale is so large
-// that weight times scale or their sum could pass fp32's end, nor in the first
-// kLateKeys keys of a workgroup's part: of few keys the heaviest often makes up
-// the sum, and its weight of 1 is exact.  (A wave that begins behind them begins
-// with its first tile's maximum, too.)
-constexpr int kLateKeys = 256;
-__device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
 // row) become weights, packed to bf16 pairs with the values' scale in them;
@@ -320,32 +230,6 @@ __device__ __forceinline__ void find_nan(const AttentionArgs &a, int hk, int j0,
                 if ((v[(long long)element(i) * a.page] & 0x7f) == 0x7f) bits[N > 64 ? i / 64 : 0] |= 1ull << (i & 63);
         }
     }
-}
-
-// Which requests a launch takes: all, those of at most kSmallRows rows per kv
-// head, or the larger ones.
-enum class Take { kAll, kSmall, kLarge };
-constexpr int kSmallRows = 32;
-
-// A launch's division of its requests' keys, and its partial results: a row's D
-// sums per split, and behind all of them a maximum and a sum of weights per
-// (row, split).  Rows are (token, q head), or for the small requests alone
-// (request, row of kSmallRows, kv head).
-struct Division {
-    int chunk, splits;
-    bool by_rows;       // many rows: a tile number per kSmallRows rows, else one per kManyRows and one per request
-    float *sums, *stats;
-};
-__device__ __forceinline__ float *part_o(const Division &v, int d, long long row, int split) {
-    return v.sums + (row * v.splits + split) * d;
-}
-__device__ __forceinline__ float *part_ml(const Division &v, long long row, int split) {
-    return v.stats + (row * v.splits + split) * 2;
-}
-template <Take TAKE>
-__device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int t, int h, long long row, int hk) {
-    return TAKE == Take::kSmall ? ((long long)s * kSmallRows + row) * a.num_kv_heads + hk
-                                : (long long)t * a.num_q_heads + h;
 }
 
 // ---------------------------------------------------------------------------
@@ -461,8 +345,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
         const int j = j0 + NK * g;
         const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
         const uint8_t *p = a.v_cache + (ph * D + c) * a.page + (j & in_page);
-        ks = a.k_scale[ph];              // needed before the values
-        vs = a.v_scale[ph];
+        ks = static_cast<const float *>(a.k_scale)[ph];              // needed before the values
+        vs = static_cast<const float *>(a.v_scale)[ph];
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
             if constexpr (NV == 4) {
@@ -668,24 +552,8 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // lanes 0-3, 12-15 and 20-27 of a half-wave, or the other 16 of it (measured: a
 // read takes 4 cycles, and 5 with two of these lanes at the same banks).
 // ---------------------------------------------------------------------------
-constexpr int kManyRows = 128;
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
 constexpr int kWideAhead = 3;
-
-// use(i, read(i)) for i < N, each read A steps before its use and, left alone
-// by the compiler, not earlier: it would read until it runs out of registers.
-template <int N, int A, typename Read, typename Use>
-__device__ __forceinline__ void run_ahead(Read read, Use use) {
-    decltype(read(0)) w[N];          // all but A + 1 of them dead at any time
-#pragma unroll
-    for (int i = 0; i < (A < N ? A : N); ++i) w[i] = read(i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (i + A < N) w[i + A] = read(i + A);
-        asm volatile("" ::: "memory");
-        use(i, w[i]);
-    }
-}
 
 template <int D>
 struct ManyLds {
@@ -695,58 +563,6 @@ struct ManyLds {
     int ok[2][4];
     int met_nan;
 };
-
-// A workgroup's share of a many-rows launch.
-struct ManyShare {
-    int s, hk, split;
-    Request rq;
-    int row0, n_rows;
-    int k_lo, k_hi;        // its keys
-    bool whole;            // no other split has any
-};
-// The last tiles see the most keys and go first; a kv head's workgroups are
-// num_kv_heads apart, so that with eight heads an XCD keeps to one.
-__device__ __forceinline__ bool many_share(const AttentionArgs &a, const Division &v, int block, int blocks, ManyShare &w) {
-    const int G = a.num_q_heads / a.num_kv_heads;
-    const unsigned units = (unsigned)blocks / (unsigned)v.splits, unit = (unsigned)block / (unsigned)v.splits, hks = a.num_kv_heads;
-    w.split = block - (int)(unit * v.splits);
-    const int tile = (int)(units / hks - 1 - unit / hks);
-    w.hk = (int)(unit % hks);
-    int within;
-    w.s = v.by_rows ? find_request(a, tile, G, kSmallRows, 0, true, within) : find_request(a, tile, G, kManyRows, 1, false, within);
-    w.rq = request_of(a, w.s);
-    w.n_rows = w.rq.n * G;
-    if (within < 0 || (long long)within * kManyRows >= w.n_rows || w.n_rows <= kSmallRows) return false;
-    w.row0 = within * kManyRows;
-    int lo, hi, x;
-    key_range(a, w.rq, token_of(w.row0, G), lo, x);
-    key_range(a, w.rq, token_of(last_row(w.row0, kManyRows, w.n_rows), G), x, hi);
-    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
-    if (w.split != sp.first && (w.split < sp.first || w.split > sp.last)) return false;
-    w.whole = sp.last <= sp.first;
-    w.k_lo = max(lo, w.split * v.chunk);
-    w.k_hi = w.split == v.splits - 1 ? hi : min(hi, (w.split + 1) * v.chunk);
-    return true;
-}
-
-// The keys [lo, hi) of [k_lo, k_hi) that some of `rows` rows from `row` on see,
-// and those [all0, all1) that each of them sees.
-struct WaveKeys {
-    int lo, hi, all0, all1;
-};
-__device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const ManyShare &w, int row, int rows) {
-    const int G = a.num_q_heads / a.num_kv_heads;
-    WaveKeys k{0, 0, 0, 0};
-    if (row < w.n_rows) {
-        key_range(a, w.rq, token_of(row, G), k.lo, k.all1);
-        key_range(a, w.rq, token_of(last_row(row, rows, w.n_rows), G), k.all0, k.hi);
-        k.lo = max(k.lo, w.k_lo);
-        k.hi = min(k.hi, w.k_hi);
-        k.all0 = max(k.all0, w.k_lo);
-        k.all1 = min(k.all1, w.k_hi);
-    }
-    return k;
-}
 
 // the LDS place of piece p of element row d of a tile's values
 __device__ __forceinline__ int v_piece(int d, int p) { return d * 4 + (p ^ (-(d >> 2) & 3)); }
@@ -817,8 +633,8 @@ struct Staging {
         for (int i = 0; i < NL; ++i) vr[i] = *reinterpret_cast<const uint4 *>(v + i * (THREADS / 4) * a.page);
         if (threadIdx.x < 4) {
             const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk;
-            s_ks = a.k_scale[ph];
-            s_vs = a.v_scale[ph];
+            s_ks = static_cast<const float *>(a.k_scale)[ph];
+            s_vs = static_cast<const float *>(a.v_scale)[ph];
         }
     }
     // Whether some rows see keys of the tile at j0 and others do not.  Zero weights
@@ -1211,70 +1027,6 @@ __global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kernel(At
 }
 
 // ---------------------------------------------------------------------------
-// The splits of a row joined: one wave per row of the launch that made them,
-// its splits' sums brought to the common maximum.
-// ---------------------------------------------------------------------------
-template <int D, Take TAKE>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Division v, int rows, int tile_rows) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63;
-    const unsigned part = blockIdx.x * 4u + (threadIdx.x >> 6);
-    if (part >= (unsigned)rows) return;
-    const int G = a.num_q_heads / a.num_kv_heads;
-    int s, t, h;
-    int r;                                  // the row within its request and kv head
-    if constexpr (TAKE == Take::kSmall) {
-        const unsigned of = part / (unsigned)a.num_kv_heads;
-        r = (int)(of % kSmallRows);
-        s = (int)(of / kSmallRows);
-        h = (int)(part - of * a.num_kv_heads) * G + r % G;
-        t = 0;
-    } else {
-        t = (int)(part / (unsigned)a.num_q_heads);
-        h = (int)(part - (unsigned)t * a.num_q_heads);
-        s = 0;
-        int n = a.num_seqs;                 // the request of token t, 64 candidates per step
-        while (n > 1) {
-            const int step = (n + 63) / 64;
-            const unsigned long long b = __ballot(lane * step < n && a.qsl[s + lane * step] <= t);
-            const int k = b ? 63 - __builtin_clzll(b) : 0;
-            s += k * step;
-            n = min(step, n - k * step);
-        }
-    }
-    const Request rq = request_of(a, s);
-    const int n_rows = rq.n * G;
-    if constexpr (TAKE == Take::kSmall) {
-        if (n_rows > kSmallRows || r >= n_rows) return;
-        t = rq.begin + token_of(r, G);
-    } else {
-        if (t < rq.begin || t >= rq.begin + rq.n || (TAKE == Take::kLarge && n_rows <= kSmallRows)) return;
-        r = (t - rq.begin) * G + h % G;
-    }
-    // the keys of the row's tile decide which splits wrote
-    const int r0 = r - r % tile_rows;
-    int k_lo, k_hi, x;
-    key_range(a, rq, token_of(r0, G), k_lo, x);
-    key_range(a, rq, token_of(last_row(r0, tile_rows, n_rows), G), x, k_hi);
-    const Splits sp = splits_of(k_lo, k_hi, v.chunk, v.splits);
-    if (sp.last <= sp.first) return;
-    float m = kNegInf, l = 0.f, o[E] = {};
-    for (int i = sp.first; i <= sp.last; ++i) m = fmaxf(m, part_ml(v, part, i)[0]);
-    const float at = m == kNegInf ? 0.f : m;
-    for (int i = sp.first; i <= sp.last; ++i) {
-        const float *ml = part_ml(v, part, i), *p = part_o(v, D, part, i);
-        const float f = __builtin_amdgcn_exp2f(ml[0] - at);
-        l = __builtin_fmaf(ml[1], f, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = __builtin_fmaf(p[lane * E + e], f, o[e]);
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *op = a.o + (long long)t * a.o_stride + (long long)h * D + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) op[e] = f32_to_bf16(o[e] * inv);
-}
-
-// ---------------------------------------------------------------------------
 // How a call is split.  With at most a token per request on average the
 // few-rows kernel takes everything; else it takes the requests of up to
 // kSmallRows rows, and the many-rows kernel the others (16 rows of a wave cost
@@ -1295,104 +1047,36 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
 // step of 2,048 tokens took 100 us with two parts and 67 with one, as partial
 // sums cost more than the long rows' wait.)
 // ---------------------------------------------------------------------------
-constexpr int kCUs = 256;
 constexpr int kMinChunk = 1024, kIdleChunk = 512;
 constexpr int kManyChunk = 256;
 
-struct Launch {
-    long long units;        // (row tile, kv head) pairs, upper bound; 0: none
-    long long rows;         // of partial results
-    int chunk, splits;
-    long long floats;       // of partial results
-};
-
-// `busy`: row tiles that hold rows, as far as the host can tell
-static Launch divide(long long tiles, long long busy, long long rows, int kv_heads, int d, int max_seq_len, int aim,
-                     long long min_chunk) {
-    Launch p{tiles * kv_heads, rows, 0x40000000, 1, 0};
-    busy *= kv_heads;
-    long long want = busy > 0 ? aim / busy : 1;
-    const long long most = max_seq_len / min_chunk;
-    if (want > most) want = most;
-    if (want > 1) {
-        const long long chunk = ((max_seq_len + want - 1) / want + kTileKeys - 1) / kTileKeys * kTileKeys;
-        p.splits = (int)((max_seq_len + chunk - 1) / chunk);
-        if (p.splits > 1) {
-            p.chunk = (int)chunk;
-            p.floats = rows * p.splits * (d + 2);
-        }
-    }
-    return p;
-}
-
-struct Plan {
-    Take few_takes;
-    bool by_rows;
-    Launch few, many;
-};
-
-static Plan plan_of(long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len) {
-    const long long G = q_heads / kv_heads;
-    Plan p{};
-    if (T <= S) {
-        p.few_takes = Take::kAll;
-        const long long full = T * G / kTileRows;
-        const long long busy = full > T ? full : T;
-        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, kCUs,
-                       busy * kv_heads * 4 <= kCUs ? kIdleChunk : kMinChunk);
-    } else {
-        p.few_takes = Take::kSmall;
-        const long long full = T * G / kManyRows, busy = full > 1 ? full : 1, room = d == 256 ? kCUs : 2 * kCUs;
-        // the small requests' parts need not be shorter than what the other
-        // workgroups take anyway: at least this many keys one after the other, where
-        // a small request's waves share theirs
-        const long long anyway = busy * kv_heads * (T / S) / 2 / room * (mixed_threads(d) / 64);
-        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
-                       anyway > kMinChunk ? anyway : kMinChunk);
-        // the fewer tile numbers of two ways that are enough (a request of many rows has
-        // more than kSmallRows): 29 decode rows and 16 tokens take 23 us with 3 per kv
-        // head, 32 with 31
-        const long long by_rows = T * G / kSmallRows + 1;
-        p.by_rows = by_rows < full + S;
-        p.many = divide(p.by_rows ? by_rows : full + S, busy, T * q_heads, kv_heads, d, max_seq_len, room, kManyChunk);
-    }
-    return p;
+// a mixed workgroup is alone on its CU at D = 256, two of them fit else
+static SplitRules rules(int d) {
+    return {kMinChunk, kIdleChunk, kManyChunk, mixed_threads(d) / 64, d == 256 ? kCUs : 2 * kCUs};
 }
 
 int64_t attention_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d, int max_seq_len) {
-    const Plan p = plan_of(num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
+    const Plan p = plan_of(rules(d), num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
     return (p.few.floats + p.many.floats) * 4;
-}
-
-// the partial results of a launch at `ws`
-static Division division(const Launch &p, bool by_rows, int d, float *ws) {
-    return {p.chunk, p.splits, by_rows, ws, ws + p.rows * p.splits * d};
-}
-
-template <int D, Take TAKE>
-static void launch_join(const AttentionArgs &a, const Launch &p, const Division &v, int tile_rows, hipStream_t stream) {
-    if (p.splits > 1)
-        hipLaunchKernelGGL((attention_join_kernel<D, TAKE>), dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, stream, a, v,
-                           (int)p.rows, tile_rows);
 }
 
 template <int D>
 static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
-    const Plan p = plan_of(a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
+    const Plan p = plan_of(rules(D), a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
     const long long few = p.few.units * p.few.splits, many = p.many.units * p.many.splits;
     if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
     const Division vf = division(p.few, false, D, a.workspace);
     if (p.few_takes == Take::kAll) {
         hipLaunchKernelGGL((attention_few_kernel<D>), dim3((unsigned)few), dim3(512), 0, stream, a, vf);
-        launch_join<D, Take::kAll>(a, p.few, vf, kTileRows, stream);
+        launch_join(Take::kAll, a, p.few, vf, kTileRows, stream);
         return hipGetLastError();
     }
     const Division vm = division(p.many, p.by_rows, D, a.workspace + p.few.floats);
     hipLaunchKernelGGL((attention_mixed_kernel<D>), dim3((unsigned)(few + many)), dim3(mixed_threads(D)), 0, stream, a, vf, vm,
                        (int)many);
-    launch_join<D, Take::kSmall>(a, p.few, vf, kTileRows, stream);
-    launch_join<D, Take::kLarge>(a, p.many, vm, kManyRows, stream);
+    launch_join(Take::kSmall, a, p.few, vf, kTileRows, stream);
+    launch_join(Take::kLarge, a, p.many, vm, kManyRows, stream);
     return hipGetLastError();
 }
 

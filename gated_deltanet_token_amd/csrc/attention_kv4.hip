@@ -1,0 +1,852 @@
+// Attention over the 4-bit paged cache (gdn_paged_attention_kv4), gfx950.
+//
+// Scores are formed transposed, X^T = K Q^T (keys down, rows across), so that
+// the exponentials P^T leave the matrix cores in the lanes that the second
+// product O^T = V^T P^T wants them in.  A row here is one (token, q head) pair of
+// the q heads that share a kv head.
+//
+// K Q^T runs on the scaled products: a key's codes and the scale of each 32 of
+// its elements go into the matrix cores as they lie in memory.  q goes in as
+// three e2m3 parts, each with a power of two per 32 elements (split_q): they take
+// 48 cycles per 16 keys of 128 elements (two e4m3 parts take 64, bf16 takes 64 and
+// the keys' conversion).
+//
+// V^T P^T runs on bf16: codes are converted in registers (exact), a weight is
+// rounded to bf16 with its token's value scale in it: a light key beside a heavy
+// one keeps its 8 bits.  Codes are finite whatever they are; a key that a row
+// does not see gets a weight of zero there, and so no influence.
+// Scores and sums are fp32; the maximum is in units of log2.
+#include "attention_split.h"
+#include "fp4.h"
+
+namespace gdn {
+
+typedef uint32_t u32x6 __attribute__((ext_vector_type(6)));
+typedef uint32_t u32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+typedef __bf16 bf16x32 __attribute__((ext_vector_type(32)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kE2m1 = 4, kE2m3 = 2;             // operand formats of the scaled products
+
+// Weights are relative to a maximum that is this much (in units of log2) above
+// the largest one met when it was set, in all but the first kLateKeys keys of a
+// workgroup's part: most tiles have a new maximum for some row of a wave, hardly
+// any one above that, and sums follow only then.  (In the first keys the heaviest
+// often makes up the sum, and its weight of 1 is exact.)  A weight is never above
+// 1, so that no product with a scale passes the values' own range.
+constexpr float kHeadroom = 8.f;
+
+__device__ __forceinline__ const uint8_t *k_scales(const AttentionArgs &a) { return static_cast<const uint8_t *>(a.k_scale); }
+__device__ __forceinline__ const uint16_t *v_scales(const AttentionArgs &a) { return static_cast<const uint16_t *>(a.v_scale); }
+
+__device__ __forceinline__ bf16x8 values8(uint32_t w) { return __builtin_bit_cast(bf16x8, e2m1_bf16(w)); }
+
+// 32 values as e2m3 codes and back, over the power of two s.  These instructions
+// write their first results before they have read their last operands (with the
+// scale's register among the results', codes came out at other scales), which the
+// compiler does not know: operands are kept until they are done.
+__device__ __forceinline__ u32x6 e2m3_codes(const bf16x32 &x, float s) {
+    u32x6 w = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x, s);
+    asm("" : "+v"(w) : "v"(x), "v"(s));
+    return w;
+}
+__device__ __forceinline__ u32x6 e2m3_codes(const f32x16 &even, const f32x16 &odd, float s) {
+    u32x6 w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, s);
+    asm("" : "+v"(w) : "v"(even), "v"(odd), "v"(s));
+    return w;
+}
+__device__ __forceinline__ f32x32 e2m3_values(const u32x6 &w, float s) {
+    f32x32 x = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s);
+    asm("" : "+v"(x) : "v"(w), "v"(s));
+    return x;
+}
+
+// 32 elements of q in three parts, x = s (hi + mid / 32 + lo / 1024), s the power
+// of two that brings their largest to [2, 4).  A part has four significant bits and
+// steps of 1/8 below 2: exact for elements down to 2^-7 of the largest, and
+// within 2^-15 of that for smaller ones.  Scale bytes: hi's, mid's and lo's.  An
+// infinity or NaN: scales of NaN, as the parts have none.
+struct SplitQ {
+    u32x6 part[3];
+    uint32_t scale;
+};
+__device__ __forceinline__ SplitQ split_q(const uint4 (&w)[4], uint32_t flip) {
+    u32x16 x;
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[4 * i + e] = u[e] ^ flip;
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, u[e] & 0x7fff7fffu));
+        }
+    }
+    const int top = max((int)m[0], (int)m[1]) >> 7;              // the largest one's biased exponent
+    const int s = max(top, 17) - 1;                              // 2^-111 at least
+    const float s0 = __builtin_bit_cast(float, (uint32_t)s << 23), s1 = __builtin_bit_cast(float, (uint32_t)(s - 5) << 23);
+    const float s2 = __builtin_bit_cast(float, (uint32_t)(s - 10) << 23);
+    SplitQ q;
+    const bf16x32 v = __builtin_bit_cast(bf16x32, x);
+    q.part[0] = e2m3_codes(v, s0);
+    f32x16 even, odd;
+    f32x32 got = e2m3_values(q.part[0], s0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        even[i] = bf16_lo(x[i]) - got[2 * i];
+        odd[i] = bf16_hi(x[i]) - got[2 * i + 1];
+    }
+    q.part[1] = e2m3_codes(even, odd, s1);
+    got = e2m3_values(q.part[1], s1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        even[i] -= got[2 * i];
+        odd[i] -= got[2 * i + 1];
+    }
+    q.part[2] = e2m3_codes(even, odd, s2);
+    q.scale = top == 255 ? 0xffffffu : (uint32_t)(s | (s - 5) << 8 | (s - 10) << 16);
+    return q;
+}
+
+__device__ __forceinline__ i32x8 operand(const u32x6 &p) {
+    return i32x8{(int)p[0], (int)p[1], (int)p[2], (int)p[3], (int)p[4], (int)p[5], 0, 0};
+}
+__device__ __forceinline__ i32x8 operand(const uint4 &k) {
+    return i32x8{(int)k.x, (int)k.y, (int)k.z, (int)k.w, 0, 0, 0, 0};
+}
+
+// A row's parts for waves of 16 rows: a lane's are those of its 32 elements, 128
+// st + 32 g on, of step st.  At D = 64 one product takes two parts: groups 0 and 1
+// have hi, groups 2 and 3 mid of the same elements, and then lo and zeros.
+template <int D>
+struct Q16 {
+    static constexpr int KS = D >= 128 ? D / 128 : 1, P = D == 64 ? 2 : 3;
+    u32x6 part[KS][P];
+    uint32_t scale[KS];
+
+    __device__ __forceinline__ void load(const uint16_t *q, int g, uint32_t flip) {
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+            uint4 w[4];
+            const int e0 = D == 64 ? 32 * (g & 1) : 128 * st + 32 * g;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(q + e0 + 8 * i);
+            const SplitQ s = split_q(w, flip);
+            if constexpr (D == 64) {
+#pragma unroll
+                for (int i = 0; i < 6; ++i) {
+                    part[0][0][i] = g < 2 ? s.part[0][i] : s.part[1][i];
+                    part[0][1][i] = g < 2 ? s.part[2][i] : 0u;
+                }
+                scale[0] = (s.scale >> (g < 2 ? 0 : 8) & 255) | (s.scale >> 16) << 8;
+            } else {
+#pragma unroll
+                for (int p = 0; p < 3; ++p) part[st][p] = s.part[p];
+                scale[st] = s.scale;
+            }
+        }
+    }
+};
+
+// x += the products of 16 keys' codes and the row's parts; `ks` has the scales of
+// four operands' keys, byte T this one's
+template <int T, int D>
+__device__ __forceinline__ void score16(f32x4 &x, const uint4 &k, uint32_t ks, const Q16<D> &q, int st) {
+    x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(k), operand(q.part[st][0]), x, kE2m1, kE2m3, T, ks, 0, q.scale[st]);
+    x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(k), operand(q.part[st][1]), x, kE2m1, kE2m3, T, ks, 1, q.scale[st]);
+    if constexpr (D != 64)
+        x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(k), operand(q.part[st][2]), x, kE2m1, kE2m3, T, ks, 2, q.scale[st]);
+}
+
+// A new maximum of a row and what its sums are multiplied by, where some row of the
+// wave is past its own.
+__device__ __forceinline__ bool new_maximum(float mx, bool late, float &m, float &f) {
+    if (!__any(mx > m)) return false;
+    const float m_new = mx > m ? mx + (late ? kHeadroom : 0.f) : m;
+    f = m_new == m ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
+    m = m_new;
+    return true;
+}
+
+// One tile of a wave with 16 rows: the scores x (x[t][r]: key jg + 4 r + t of the
+// lane's row) become weights, packed to bf16 pairs in the keys' order with the
+// tokens' value scales vs in them; the running maximum m, the lane's sum l and the
+// sums o follow.
+template <int DT>
+__device__ __forceinline__ void weigh16(f32x4 (&x)[4], float factor, float (&vs)[16], bool late, bool masked, bool seen_page, int jg,
+                                        int jb, int je, float &m, float &l, f32x4 (&o)[DT], uint32_t (&pw)[8]) {
+    if (masked) {
+        // from the row's first and past its last key of these, none of a missing page
+        const int from = seen_page ? jb - jg : 16, to = je - jg;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (4 * r + t < from || 4 * r + t >= to) {
+                    x[t][r] = kNegInf;
+                    vs[4 * r + t] = 0.f;
+                }
+    }
+    float mx = kNegInf;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
+    mx = max_over32(max_over16(mx)) * factor;
+    float f;
+    if (new_maximum(mx, late, m, f)) {
+        l *= f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) o[t] *= f;
+    }
+    const float at = m == kNegInf ? 0.f : m;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < 4; t += 2) {
+            const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][r], factor, -at));
+            const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t + 1][r], factor, -at));
+            l += e0 + e1;
+            pw[2 * r + t / 2] = pack_bf16x2(e0 * vs[4 * r + t], e1 * vs[4 * r + t + 1]);
+        }
+}
+
+// A row's o from its lane's sums of waves of 16 rows, 8 elements 32 i + 8 g on
+// from each pair of them: written out, or as a part's sums.
+__device__ __forceinline__ void put8(const AttentionArgs &a, const Division &v, bool whole, float inv, const f32x4 &s0, const f32x4 &s1,
+                                     long long token, int h, long long part, int split, int d) {
+    const float f[8] = {s0.x, s1.x, s0.y, s1.y, s0.z, s1.z, s0.w, s1.w};
+    if (whole) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = f[e] * inv;
+        *reinterpret_cast<uint4 *>(a.o + token * a.o_stride + (long long)h * a.d + d) = pack8(y);
+    } else {
+        float *p = part_o(v, a.d, part, split) + d;
+        *reinterpret_cast<f32x4 *>(p) = f32x4{f[0], f[1], f[2], f[3]};
+        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: one workgroup of W waves per (16 rows of one request that share a
+// kv head, split of its keys).  Bound by reading the cache: each wave takes every
+// W-th tile of 64 keys straight from HBM into registers in the order of the
+// matrix operands (16-byte loads), with the next tile's keys and values on their
+// way while it works on this one.  The waves' sums are joined in the LDS.
+//
+// Lanes: with c = lane % 16 and g = lane / 16, a lane holds row c and the 16
+// keys from 16 g on of the tile, a granule of the cache: one page number per
+// lane for values, and one for the keys whose codes it loads.  Row i of the t-th K
+// operand is key 16 (i / 4) + 4 (i % 4) + t: the four operands' scales are
+// neighbouring bytes.  Row i of the V operands 2 u and 2 u + 1 is element 32 u + 2 i
+// and the one behind it: a 16-byte load has both.
+// ---------------------------------------------------------------------------
+template <int D, int W>
+struct FewLds {
+    f32x4 red[W][D >= 128 ? 8 : D / 16][64];
+    float red_m[W][16], red_l[W][16];
+};
+
+template <int D, int W, Take TAKE>
+__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block, FewLds<D, W> &lds) {
+    constexpr int KS = Q16<D>::KS;
+    constexpr int DT = D / 16;                       // operands of 16 value elements
+    constexpr int DTH = DT < 8 ? DT : 8;             // of which joined at once
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4, kg = c >> 2;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    // rows and workgroups of a launch are fewer than 2^31 (launch_d): 32-bit divisions
+    const unsigned unit = (unsigned)block / (unsigned)v.splits;
+    const int split = block - (int)(unit * v.splits);
+    const int tile = (int)(unit / (unsigned)a.num_kv_heads);
+    const int hk = (int)(unit - tile * a.num_kv_heads);
+    int within, s;
+    if constexpr (TAKE == Take::kSmall) {
+        // the first tiles, most of them the only ones, first
+        within = (unsigned)tile / (unsigned)a.num_seqs;
+        s = tile - within * a.num_seqs;
+    } else if (tile < a.num_seqs) {
+        s = tile;                                    // every request's first tile: no search
+        within = 0;
+    } else {
+        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, false, within);
+        ++within;
+    }
+    const Request rq = request_of(a, s);
+    const int n_rows = rq.n * G;
+    if (within < 0 || (long long)within * kTileRows >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
+    const int row0 = within * kTileRows, i_first = token_of(row0, G), i_last = token_of(last_row(row0, kTileRows, n_rows), G);
+    int lo, hi, x0, x1;                              // keys that some row sees, that every row sees
+    key_range(a, rq, i_first, lo, x1);
+    key_range(a, rq, i_last, x0, hi);
+    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
+    if (split != sp.first && (split < sp.first || split > sp.last)) return;
+    const bool whole = sp.last <= sp.first;          // no other split: write o itself
+    const int k_lo = max(lo, split * v.chunk);
+    const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
+
+    const int row = row0 + c, i_row = token_of(row, G), h = hk * G + row - i_row * G;
+    const bool live = row < n_rows;
+    int jb = 0, je = 0;
+    if (live) key_range(a, rq, i_row, jb, je);
+    jb = max(jb, k_lo);
+    je = min(je, k_hi);
+
+    const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
+    const int32_t *bt = a.block_table + s * a.block_table_stride;
+    auto good = [&](int p) { return (unsigned)p < (unsigned)a.num_pages; };
+    // Page numbers are loaded a tile ahead of the loads that use them, and not
+    // looked at before: loads come back in order, so that looking at one that was
+    // asked for behind a tile waits for the tile.
+    auto entry_at = [&](int j) { return bt[min(j >> shift, a.max_pages - 1)]; };
+    auto page_of = [&](int entry, int j) { return j < k_hi && good(entry) ? entry : -1; };
+
+    uint4 kr[4][KS], vr[DT / 2], vw[2];
+    uint32_t ks[KS];
+    auto load_k = [&](int j0, int page) {
+        const int j = j0 + 16 * kg + 4 * (c & 3);
+        const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
+        const int block = D == 64 ? g & 1 : g;
+        const uint8_t *p = a.k_cache + (ph * a.page + (j & in_page)) * (D / 2) + 16 * block;
+        const uint8_t *sc = k_scales(a) + (ph * (D / 32) + block) * a.page + (j & in_page);
+#pragma unroll
+        for (int st = 0; st < KS; ++st) ks[st] = *reinterpret_cast<const uint32_t *>(sc + 4 * st * a.page);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int st = 0; st < KS; ++st) kr[t][st] = *reinterpret_cast<const uint4 *>(p + t * (D / 2) + 64 * st);
+    };
+    auto load_v = [&](int j0, int page) {
+        const int j = j0 + 16 * g;
+        const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk, at = ph * a.page + (j & in_page);
+        const uint4 *sc = reinterpret_cast<const uint4 *>(v_scales(a) + at);     // needed before the values
+        vw[0] = sc[0];
+        vw[1] = sc[1];
+        const uint8_t *p = a.v_cache + at * (D / 2) + 16 * c;
+#pragma unroll
+        for (int u = 0; u < DT / 2; ++u) vr[u] = *reinterpret_cast<const uint4 *>(p + 256 * u);
+    };
+
+    f32x4 o[DT] = {};
+    float m = kNegInf, l = 0.f;
+    constexpr int step = W * kTileKeys;
+    int j0 = first_tile(k_lo, kTileKeys, wave);
+    int ek = entry_at(j0 + 16 * kg), ev = entry_at(j0 + 16 * g), pv = -1;
+    // the next tile's keys, and the entries behind it
+    auto turn = [&](int j) {
+        const int pk = page_of(ek, j + 16 * kg), page = page_of(ev, j + 16 * g);
+        load_k(j, pk);
+        ek = entry_at(j + step + 16 * kg);
+        ev = entry_at(j + step + 16 * g);
+        return page;
+    };
+    if (j0 < k_hi) {
+        pv = turn(j0);
+        asm volatile("" ::: "memory");
+        load_v(j0, pv);
+        asm volatile("" ::: "memory");
+    }
+    // q is split while the first tile is on its way
+    Q16<D> q;
+    q.load(a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D, g,
+           a.scale < 0.f ? 0x80008000u : 0u);
+    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+
+    for (; j0 < k_hi; j0 += step) {
+        const int jn = j0 + step;
+        int pv_n = -1;
+        f32x4 x[4] = {};
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+            score16<0>(x[0], kr[0][st], ks[st], q, st);
+            score16<1>(x[1], kr[1][st], ks[st], q, st);
+            score16<2>(x[2], kr[2][st], ks[st], q, st);
+            score16<3>(x[3], kr[3][st], ks[st], q, st);
+        }
+        if (jn < k_hi) pv_n = turn(jn);
+        asm volatile("" ::: "memory");
+
+        const bool seen_page = good(pv);
+        const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + kTileKeys > min(x1, k_hi);
+        float vs[16];
+        unpack8(vw[0], vs);
+        unpack8(vw[1], vs + 8);
+        uint32_t pw[8];
+        weigh16(x, factor, vs, j0 - k_lo >= kLateKeys, masked, seen_page, j0 + 16 * g, jb, je, m, l, o, pw);
+        const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+#pragma unroll
+        for (int u = 0; u < DT / 2; ++u) {
+            o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].x), p0, o[2 * u], 0, 0, 0);
+            o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].y), p1, o[2 * u], 0, 0, 0);
+            o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].z), p0, o[2 * u + 1], 0, 0, 0);
+            o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].w), p1, o[2 * u + 1], 0, 0, 0);
+        }
+        if (jn < k_hi) load_v(jn, pv_n);
+        asm volatile("" ::: "memory");
+        pv = pv_n;
+    }
+
+    // join the waves: maxima, then each wave's sums at the common maximum
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) {
+        lds.red_m[wave][c] = m;
+        lds.red_l[wave][c] = l;
+    }
+    __syncthreads();
+    float m_all = kNegInf, l_all = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, lds.red_m[w][c]);
+    const float at = m_all == kNegInf ? 0.f : m_all;
+#pragma unroll
+    for (int w = 0; w < W; ++w) l_all += lds.red_l[w][c] * __builtin_amdgcn_exp2f(lds.red_m[w][c] - at);
+    const float f = __builtin_amdgcn_exp2f(m - at);
+    const long long out_row = part_row<TAKE>(a, s, rq.begin + i_row, h, row, hk);
+    const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+#pragma unroll
+    for (int t0 = 0; t0 < DT; t0 += DTH) {
+        if (t0) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < DTH; ++t) lds.red[wave][t][lane] = o[t0 + t] * f;
+        __syncthreads();
+        for (int t = 2 * wave; t < DTH; t += 2 * W) {
+            f32x4 s0 = lds.red[0][t][lane], s1 = lds.red[0][t + 1][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) {
+                s0 += lds.red[w][t][lane];
+                s1 += lds.red[w][t + 1][lane];
+            }
+            if (live) put8(a, v, whole, inv, s0, s1, rq.begin + i_row, h, out_row, split, 16 * (t0 + t) + 8 * g);
+        }
+    }
+    if (!whole && wave == 0 && g == 0 && live) {
+        float *ml = part_ml(v, out_row, split);
+        ml[0] = m_all;
+        ml[1] = l_all;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: one workgroup per (128 rows of one request that share a kv head,
+// split of its keys).  Bound by the matrix cores, the exponentials and the
+// values' conversion: tiles of 64 keys and values pass through the LDS once for
+// all waves, the next one on its way from HBM to registers meanwhile, with one
+// barrier per tile between two buffers.
+//
+// Keys lie in the LDS as rows of 16-byte pieces (32 elements), values as in
+// memory, granule by granule.  The 16 lanes that a 16-byte read serves together are
+// lanes 0-3, 12-15 and 20-27 of a half-wave, or the other 16 of it: PLACE puts
+// the pieces that they read into 16 different places of the 256 bytes that the
+// banks span.  A read of values is of 512 bytes in a row.
+// ---------------------------------------------------------------------------
+template <int D>
+struct ManyLds {
+    uint4 k[2][kTileKeys * D / 32], v[2][kTileKeys * D / 32];
+    uint32_t ks[2][kTileKeys * D / 128];   // [block of 32 elements][key], a byte each
+    float vs[2][kTileKeys];
+    int ok[2][4];                          // whether the tile's four granules have a page
+};
+
+// Staging of a workgroup of THREADS threads, D / 2 of them per granule of 16 keys:
+// a thread has one 16-byte piece of keys, one of values, and the first ones four
+// keys' scales or two values' of the same granule, of one page.
+template <int D, int THREADS, int (*PLACE)(int, int)>
+struct Staging {
+    static constexpr int PER = D / 2, USED = 4 * PER, PPK = D / 32;
+    static_assert(USED <= THREADS, "");
+    const AttentionArgs &a;
+    ManyLds<D> &lds;
+    const int32_t *bt;
+    int k_hi, shift, in_page, hk, granule, i;
+    // the block table's entry for the granule of the tile to load next, as it came
+    // (looking at it here would wait for it and all loads before it)
+    int entry, tile, own;
+    uint4 kr, vr;
+    uint32_t sc;
+
+    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w)
+        : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
+          in_page(a_.page - 1), hk(w.hk), granule(threadIdx.x / PER), i(threadIdx.x % PER), entry(-1), tile(0), own(-1), sc(0) {}
+    __device__ __forceinline__ bool works() const { return USED == THREADS || (int)threadIdx.x < USED; }
+    __device__ __forceinline__ void pages(int j0) {
+        tile = j0;
+        if (works()) entry = bt[min((j0 + 16 * granule) >> shift, a.max_pages - 1)];
+    }
+    __device__ __forceinline__ void load() {
+        if (!works()) return;
+        const int j = tile + 16 * granule;
+        own = j < k_hi && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
+        const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk, at = ph * a.page + (j & in_page);
+        kr = *reinterpret_cast<const uint4 *>(a.k_cache + at * (D / 2) + 16 * i);
+        vr = *reinterpret_cast<const uint4 *>(a.v_cache + at * (D / 2) + 16 * i);
+        if (i < D / 8)
+            sc = *reinterpret_cast<const uint32_t *>(k_scales(a) + (ph * (D / 32) + i / 4) * a.page + (j & in_page) + 4 * (i % 4));
+        else if (i < D / 8 + 8)
+            sc = *reinterpret_cast<const uint32_t *>(v_scales(a) + at + 2 * (i - D / 8));
+    }
+    __device__ __forceinline__ void put(int buf) {
+        if (!works()) return;
+        lds.k[buf][PLACE(16 * granule + i / PPK, i % PPK)] = kr;
+        lds.v[buf][granule * PER + i] = vr;
+        if (i < D / 8) {
+            lds.ks[buf][(i / 4) * 16 + granule * 4 + i % 4] = sc;
+        } else if (i < D / 8 + 8) {
+            const int at = 16 * granule + 2 * (i - D / 8);
+            lds.vs[buf][at] = bf16_lo(sc);
+            lds.vs[buf][at + 1] = bf16_hi(sc);
+        }
+        if (i == 0) lds.ok[buf][granule] = own >= 0;
+    }
+    __device__ __forceinline__ void begin(int j0) {
+        pages(j0);
+        load();
+        pages(j0 + kTileKeys);
+        put(0);
+        __syncthreads();
+    }
+    // before the work on the tile at j0: the next one's loads go out
+    __device__ __forceinline__ void ahead(int j0) {
+        if (j0 + kTileKeys < k_hi) {
+            load();
+            pages(j0 + 2 * kTileKeys);
+        }
+        asm volatile("" ::: "memory");
+    }
+    // after it: into the other buffer
+    __device__ __forceinline__ void next(int j0, int buf) {
+        asm volatile("" ::: "memory");
+        if (j0 + kTileKeys < k_hi) put(buf ^ 1);
+        __syncthreads();
+    }
+};
+
+// ---------------------------------------------------------------------------
+// 32 rows per wave, four waves (D = 64 and 128).
+//
+// Lanes: with c = lane % 32 and h = lane / 32, a lane holds row c and the keys
+// 32 h .. 32 h + 31 of the tile, x[b][r] being key 32 h + 2 r + b.  For that, row i
+// of the b-th K operand is key 32 (i / 4 % 2) + 8 (i / 8) + 2 (i % 4) + b: the two
+// operands' scales are neighbouring bytes.  Row i of the V operands 2 u and 2 u + 1
+// is element 64 u + 2 i and the one behind it.
+// ---------------------------------------------------------------------------
+constexpr int kWideThreads = 256;
+
+// 32 lanes read the same piece of keys 32 (c / 4 % 2) + 8 (c / 8) + 2 (c % 4) + b
+template <int D>
+__device__ __forceinline__ int k_place(int key, int p) {
+    // with the tile's key bits 5 .. 0 as (h a1 a0 r1 r0 b), b leads, so that the lanes'
+    // rows follow each other
+    const int row = (key & 1) << 5 | key >> 1;
+    constexpr int shift = D == 64 ? 3 : 2, mask = D / 32 - 1;
+    return row * (D / 32) + (p ^ (row >> shift & mask));
+}
+
+template <int D>
+__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
+    constexpr int KS = D / 64;                       // contraction steps of 64
+    constexpr int DT = D / 32;                       // operands of 32 value elements
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 31, h2 = lane >> 5;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    ManyShare w;
+    if (!many_share(a, v, block, blocks, w)) return;
+    const Request &rq = w.rq;
+    const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
+
+    // this wave's rows
+    const int wrow = w.row0 + 32 * wave, row = wrow + c;
+    const bool live = row < w.n_rows;
+    const int i_row = live ? token_of(row, G) : 0, h = hk * G + (live ? row - i_row * G : 0);
+    int jb = 0, je = 0;
+    if (live) key_range(a, rq, i_row, jb, je);
+    jb = max(jb, k_lo);
+    je = min(je, k_hi);
+    const WaveKeys wk = wave_keys(a, w, wrow, 32);
+
+    // q's parts of step st: elements 64 st + 32 h2 on
+    SplitQ q[KS];
+    {
+        const uint16_t *qp = a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D + 32 * h2;
+#pragma unroll
+        for (int st = 0; st < KS; ++st) {
+            uint4 e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = *reinterpret_cast<const uint4 *>(qp + 64 * st + 8 * i);
+            q[st] = split_q(e, a.scale < 0.f ? 0x80008000u : 0u);
+        }
+    }
+    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+
+    Staging<D, kWideThreads, k_place<D>> stage(a, lds, w);
+    const int key = 32 * (c >> 2 & 1) + 8 * (c >> 3) + 2 * (c & 3);
+    const int k_row = k_place<D>(key, 0) & ~(D / 32 - 1), k_swap = k_place<D>(key, h2) - k_row;
+    f32x16 o[DT] = {};
+    float m = kNegInf, l = 0.f;
+    int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
+    if (j0 < k_hi) stage.begin(j0);
+    for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
+        const int jn = j0 + kTileKeys;
+        stage.ahead(j0);
+        if (j0 < wk.hi && jn > wk.lo) {
+            const bool ok0 = lds.ok[buf][2 * h2] != 0, ok1 = lds.ok[buf][2 * h2 + 1] != 0;
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1)), late = j0 - k_lo >= kLateKeys;
+            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + h2 * D + c;
+            const uint8_t *kst = reinterpret_cast<const uint8_t *>(lds.ks[buf]) + key + 64 * h2;
+            f32x16 x[2] = {};
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                const int sc = *reinterpret_cast<const uint16_t *>(kst + 128 * st);
+                const uint4 k0 = kt[k_swap ^ 2 * st], k1 = kt[32 * (D / 32) + (k_swap ^ 2 * st)];
+                // (the products' operand selections are constants)
+                x[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k0), operand(q[st].part[0]), x[0], kE2m1, kE2m3, 0, sc, 0, q[st].scale);
+                x[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k1), operand(q[st].part[0]), x[1], kE2m1, kE2m3, 1, sc, 0, q[st].scale);
+                x[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k0), operand(q[st].part[1]), x[0], kE2m1, kE2m3, 0, sc, 1, q[st].scale);
+                x[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k1), operand(q[st].part[1]), x[1], kE2m1, kE2m3, 1, sc, 1, q[st].scale);
+                x[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k0), operand(q[st].part[2]), x[0], kE2m1, kE2m3, 0, sc, 2, q[st].scale);
+                x[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k1), operand(q[st].part[2]), x[1], kE2m1, kE2m3, 1, sc, 2, q[st].scale);
+            }
+            const int jg = j0 + 32 * h2;
+            if (masked) {
+                // from the row's first and past its last key of these, none of a missing page
+                const int from = jb - jg, to = je - jg;
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        if (2 * r + b < from || 2 * r + b >= to || !(r < 8 ? ok0 : ok1)) x[b][r] = kNegInf;
+            }
+            float mx = kNegInf;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, fmaxf(x[0][r], x[1][r]));
+            mx = max_over32(mx) * factor;
+            float f;
+            if (new_maximum(mx, late, m, f)) {
+                l *= f;
+#pragma unroll
+                for (int i = 0; i < DT; ++i) o[i] *= f;
+            }
+            const float at = m == kNegInf ? 0.f : m;
+            const f32x4 *vst = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 32 * h2);
+            uint32_t pw[16];
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                f32x4 s = vst[r / 2];
+                if (masked)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[e] = x[e & 1][r + e / 2] == kNegInf ? 0.f : s[e];
+                const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[0][r], factor, -at));
+                const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[1][r], factor, -at));
+                const float e2 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[0][r + 1], factor, -at));
+                const float e3 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[1][r + 1], factor, -at));
+                l += (e0 + e1) + (e2 + e3);
+                pw[r] = pack_bf16x2(e0 * s.x, e1 * s.y);
+                pw[r + 1] = pack_bf16x2(e2 * s.z, e3 * s.w);
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf16x8 p0 = as_bf16x8(pw[8 * b], pw[8 * b + 1], pw[8 * b + 2], pw[8 * b + 3]);
+                const bf16x8 p1 = as_bf16x8(pw[8 * b + 4], pw[8 * b + 5], pw[8 * b + 6], pw[8 * b + 7]);
+#pragma unroll
+                for (int u = 0; u < DT / 2; ++u) {
+                    const uint4 w4 = vt[b * (D / 2) + 32 * u];
+                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.x), p0, o[2 * u], 0, 0, 0);
+                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.y), p1, o[2 * u], 0, 0, 0);
+                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.z), p0, o[2 * u + 1], 0, 0, 0);
+                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.w), p1, o[2 * u + 1], 0, 0, 0);
+                }
+            }
+        }
+        stage.next(j0, buf);
+    }
+
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long token = rq.begin + i_row, out_row = token * a.num_q_heads + h;
+    // elements 64 u + 16 i + 8 h2 + 2 r and the one behind it of row c are o[2 u][4 i + r] and o[2 u + 1][4 i + r]
+#pragma unroll
+    for (int u = 0; u < DT / 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 s0 = {o[2 * u][4 * i], o[2 * u][4 * i + 1], o[2 * u][4 * i + 2], o[2 * u][4 * i + 3]};
+            const f32x4 s1 = {o[2 * u + 1][4 * i], o[2 * u + 1][4 * i + 1], o[2 * u + 1][4 * i + 2], o[2 * u + 1][4 * i + 3]};
+            put8(a, v, w.whole, inv, s0, s1, token, h, out_row, w.split, 64 * u + 16 * i + 8 * h2);
+        }
+    if (!w.whole && h2 == 0) {
+        float *ml = part_ml(v, out_row, w.split);
+        ml[0] = m;
+        ml[1] = l;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 16 rows per wave, eight waves, for D = 256: 32 rows' sums and q parts leave room
+// for one wave per SIMD only.  Lanes as in the few-rows kernel, operands from the
+// LDS.
+// ---------------------------------------------------------------------------
+constexpr int kNarrowThreads = 512;
+
+// 16 lanes read the same piece of keys 16 (c / 4) + 4 (c % 4) + t
+template <int D>
+__device__ __forceinline__ int k_place_narrow(int key, int p) {
+    static_assert(D == 256, "");
+    // key bit 2 leads within eight keys, so that the lanes' rows are even and odd
+    const int row = (key & ~7) | (key & 3) << 1 | (key >> 2 & 1);
+    return row * 8 + (p ^ ((key >> 5 & 1) << 1 | (key >> 3 & 1) << 2));
+}
+
+template <int D>
+__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
+    constexpr int KS = D / 128, DT = D / 16;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    ManyShare w;
+    if (!many_share(a, v, block, blocks, w)) return;
+    const Request &rq = w.rq;
+    const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
+    const int wrow = w.row0 + 16 * wave, row = wrow + c;
+    const bool live = row < w.n_rows;
+    const int i_row = live ? token_of(row, G) : 0, h = hk * G + (live ? row - i_row * G : 0);
+    int jb = 0, je = 0;
+    if (live) key_range(a, rq, i_row, jb, je);
+    jb = max(jb, k_lo);
+    je = min(je, k_hi);
+    const WaveKeys wk = wave_keys(a, w, wrow, 16);
+    Q16<D> q;
+    q.load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, a.scale < 0.f ? 0x80008000u : 0u);
+    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+
+    Staging<D, kNarrowThreads, k_place_narrow<D>> stage(a, lds, w);
+    const int key = 16 * (c >> 2) + 4 * (c & 3);
+    const int k_row = k_place_narrow<D>(key, 0) & ~7, k_swap = k_place_narrow<D>(key, g) & 7;
+    f32x4 o[DT] = {};
+    float m = kNegInf, l = 0.f;
+    int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
+    if (j0 < k_hi) stage.begin(j0);
+    for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
+        const int jn = j0 + kTileKeys;
+        stage.ahead(j0);
+        if (j0 < wk.hi && jn > wk.lo) {
+            const bool ok = lds.ok[buf][g] != 0;
+            const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
+            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + g * (D / 2) + c;
+            f32x4 x[4] = {};
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                const uint32_t ks = lds.ks[buf][16 * (4 * st + g) + key / 4];
+                const int at = k_swap ^ 4 * st;
+                score16<0>(x[0], kt[at], ks, q, st);            // (key t is row 2 t of these eight)
+                score16<1>(x[1], kt[2 * 8 + at], ks, q, st);
+                score16<2>(x[2], kt[4 * 8 + at], ks, q, st);
+                score16<3>(x[3], kt[6 * 8 + at], ks, q, st);
+            }
+            float vs[16];
+            const f32x4 *vst = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 16 * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 s = vst[i];
+                vs[4 * i] = s.x;
+                vs[4 * i + 1] = s.y;
+                vs[4 * i + 2] = s.z;
+                vs[4 * i + 3] = s.w;
+            }
+            uint32_t pw[8];
+            weigh16(x, factor, vs, j0 - k_lo >= kLateKeys, masked, ok, j0 + 16 * g, jb, je, m, l, o, pw);
+            const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
+#pragma unroll
+            for (int u = 0; u < DT / 2; ++u) {
+                const uint4 w4 = vt[16 * u];
+                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.x), p0, o[2 * u], 0, 0, 0);
+                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.y), p1, o[2 * u], 0, 0, 0);
+                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.z), p0, o[2 * u + 1], 0, 0, 0);
+                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.w), p1, o[2 * u + 1], 0, 0, 0);
+            }
+        }
+        stage.next(j0, buf);
+    }
+
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long token = rq.begin + i_row, out_row = token * a.num_q_heads + h;
+#pragma unroll
+    for (int t = 0; t < DT; t += 2) put8(a, v, w.whole, inv, o[t], o[t + 1], token, h, out_row, w.split, 16 * t + 8 * g);
+    if (!w.whole && g == 0) {
+        float *ml = part_ml(v, out_row, w.split);
+        ml[0] = m;
+        ml[1] = l;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The kernels: a token per request at most on average (few rows alone, eight
+// waves), and else both kinds of requests in one grid -- the large ones'
+// workgroups first, those of the small ones (decode rows) take the CUs that
+// are left and each that becomes free.
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ __launch_bounds__(512, 2) void attention_few_kv4_kernel(AttentionArgs a, Division v) {
+    __shared__ FewLds<D, 8> lds;
+    few_rows<D, 8, Take::kAll>(a, v, blockIdx.x, lds);
+}
+
+constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThreads; }
+
+template <int D>
+__global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kv4_kernel(AttentionArgs a, Division few, Division many,
+                                                                                  int many_blocks) {
+    constexpr int W = mixed_threads(D) / 64;
+    __shared__ union {
+        FewLds<D, W> few;
+        ManyLds<D> many;
+    } lds;
+    const int block = blockIdx.x;
+    if (block >= many_blocks) few_rows<D, W, Take::kSmall>(a, few, block - many_blocks, lds.few);
+    else if constexpr (D == 256) many_rows_narrow<D>(a, many, block, many_blocks, lds.many);
+    else many_rows_wide<D>(a, many, block, many_blocks, lds.many);
+}
+
+static SplitRules rules(int d) { return {1024, 512, 256, mixed_threads(d) / 64, d == 256 ? kCUs : 2 * kCUs}; }
+
+int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d, int max_seq_len) {
+    const Plan p = plan_of(rules(d), num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
+    return (p.few.floats + p.many.floats) * 4;
+}
+
+template <int D>
+static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
+    const Plan p = plan_of(rules(D), a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
+    const long long few = p.few.units * p.few.splits, many = p.many.units * p.many.splits;
+    if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
+        return hipErrorInvalidConfiguration;
+    const Division vf = division(p.few, false, D, a.workspace);
+    if (p.few_takes == Take::kAll) {
+        hipLaunchKernelGGL((attention_few_kv4_kernel<D>), dim3((unsigned)few), dim3(512), 0, stream, a, vf);
+        launch_join(Take::kAll, a, p.few, vf, kTileRows, stream);
+        return hipGetLastError();
+    }
+    const Division vm = division(p.many, p.by_rows, D, a.workspace + p.few.floats);
+    hipLaunchKernelGGL((attention_mixed_kv4_kernel<D>), dim3((unsigned)(few + many)), dim3(mixed_threads(D)), 0, stream, a, vf, vm,
+                       (int)many);
+    launch_join(Take::kSmall, a, p.few, vf, kTileRows, stream);
+    launch_join(Take::kLarge, a, p.many, vm, kManyRows, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_attention_kv4(const AttentionArgs &a, hipStream_t stream) {
+    switch (a.d) {
+        case 64: return launch_d<64>(a, stream);
+        case 128: return launch_d<128>(a, stream);
+        case 256: return launch_d<256>(a, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace gdn

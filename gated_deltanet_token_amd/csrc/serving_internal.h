@@ -42,8 +42,8 @@ struct RopeAppendArgs {
     const double *freq;
     uint8_t *k_cache;
     uint8_t *v_cache;
-    float *k_scale;
-    float *v_scale;
+    void *k_scale;               // their types are the cache format's
+    void *v_scale;
     double rope_scale;
     int rot;
     int interleaved;
@@ -55,13 +55,14 @@ struct RopeAppendArgs {
     int d;
 };
 
+// an attention over a paged cache
 struct AttentionArgs {
     const uint16_t *q;
     int64_t q_stride;
     const uint8_t *k_cache;
     const uint8_t *v_cache;
-    const float *k_scale;
-    const float *v_scale;
+    const void *k_scale;         // their types are the cache format's
+    const void *v_scale;
     const int32_t *block_table;
     int64_t block_table_stride;
     const int32_t *seq_lens;
@@ -81,6 +82,27 @@ struct AttentionArgs {
     float scale;
     int causal;
     int window;
+};
+
+struct PagedReadArgs {
+    const uint8_t *k_cache;
+    const uint8_t *v_cache;
+    const uint8_t *k_scale;
+    const uint16_t *v_scale;
+    const int32_t *block_table;
+    int64_t block_table_stride;
+    const int32_t *key_starts;   // nullptr: from key 0 on
+    const int32_t *out_start_loc;
+    uint16_t *k_out;             // nullptr: no keys
+    uint16_t *v_out;
+    int64_t k_out_stride, v_out_stride;
+    int num_pages;
+    int page;
+    int max_pages;
+    int num_seqs;
+    int num_rows;
+    int num_kv_heads;
+    int d;
 };
 
 struct HeadNormArgs {
@@ -117,6 +139,11 @@ hipError_t launch_rope_append(const RopeAppendArgs &a, hipStream_t stream);
 int64_t attention_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d,
                                   int max_seq_len);
 hipError_t launch_attention(const AttentionArgs &a, hipStream_t stream);
+hipError_t launch_rope_append_kv4(const RopeAppendArgs &a, hipStream_t stream);
+hipError_t launch_paged_read_kv4(const PagedReadArgs &a, hipStream_t stream);
+int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d,
+                                      int max_seq_len);
+hipError_t launch_attention_kv4(const AttentionArgs &a, hipStream_t stream);
 hipError_t launch_head_norm(const HeadNormArgs &a, hipStream_t stream);
 hipError_t launch_residual_norm(const ResidualNormArgs &a, hipStream_t stream);
 

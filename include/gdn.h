@@ -32,6 +32,12 @@
  *                               decode rows and prompt chunks
  *   gdn_paged_attention_kv8_workspace_size
  *                               host: scratch bytes the attention needs
+ *   gdn_rope_append_kv4         GPU: the same, into the 4-bit paged cache
+ *   gdn_paged_read_kv4          GPU: ranges of keys and values out of that
+ *                               cache, as packed bf16 rows
+ *   gdn_paged_attention_kv4     GPU: attention over the 4-bit cache
+ *   gdn_paged_attention_kv4_workspace_size
+ *                               host: scratch bytes the attention needs
  *   gdn_gated_rms_norm          GPU: norm of each head with its output gate
  *   gdn_residual_rms_norm       GPU: norm after a block, its gate, residual
  *                               scale and sum, and the next block's norm
@@ -717,6 +723,123 @@ size_t gdn_paged_attention_kv8_workspace_size(int32_t num_tokens, int32_t num_se
 
 int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, const uint8_t *k_cache,
                             const uint8_t *v_cache, const float *k_scale, const float *v_scale,
+                            int32_t num_pages, int32_t page_size, const int32_t *block_table,
+                            int64_t block_table_stride, int32_t max_pages, const int32_t *seq_lens,
+                            const int32_t *query_start_loc, int32_t max_seq_len,
+                            gdn_bf16 *o, int64_t o_stride, int32_t num_seqs, int32_t num_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
+                            int32_t causal, int32_t window, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/*
+ * The 4-bit paged cache of gdn_rope_append_kv4, gdn_paged_read_kv4 and
+ * gdn_paged_attention_kv4: 4.25 bits per element of a key and 4 bits and two
+ * bytes per head of a value, where the 8-bit cache has 8.
+ *   k_cache  e2m1 codes (2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3,
+ *            4, 6 and a sign) [num_pages][num_kv_heads][page_size][head_dim / 2]:
+ *            two elements of a key to a byte, the even one in the low half
+ *   k_scale  e8m0 (2^(byte - 127), 255: NaN), one of 32 elements of a key
+ *            [num_pages][num_kv_heads][head_dim / 32][page_size]
+ *   v_cache  e2m1 codes [num_pages][num_kv_heads][page_size / 16][head_dim][8]:
+ *            an element's codes of 16 neighbouring tokens (a granule), two
+ *            tokens to a byte, the even one in the low half
+ *   v_scale  bf16 [num_pages][num_kv_heads][page_size], one of a token's value
+ * An element is its code times its scale.  page_size is 16, 32 or 64; head_dim
+ * 64, 128 or 256.  All four are 16-byte aligned.
+ */
+
+/*
+ * gdn_rope_append_kv4 -- rotary positions on q and k, and the new k and v
+ * written into the cache, in one launch.
+ *
+ * Rotation, positions and frequencies are those of gdn_rope_append_kv8, and so is
+ * the order that slot_mapping has to have; angles, and sines and cosines times
+ * rope_scale, are in 64 bits, products in fp32.
+ *
+ * Cache: k and v are rounded to nearest even at their scale.  A key's 32
+ * elements' scale is the power of two below which their largest magnitude m has
+ * two bits: 2^(e - 2), m between 1 and 1.75 times 2^e, or between 0.875 and 1 (so m
+ * is met by 3.5 to 7 scales, 7 excluded); 2^-100 at least.  A value's scale is
+ * m / 6 rounded to bf16, m the largest magnitude of the token's head; 2^-100 at
+ * least.  A block or head with an infinity or NaN has a scale of NaN, and all of
+ * it reads as NaN.  (m above 1.75 2^127 reads as infinite.)  What was stored
+ * before keeps its codes and scales: a token's do not depend on its neighbours'.
+ * Two new tokens of one granule whose order is not the one above leave the codes
+ * of that granule's values undefined, but nothing outside the cache is accessed.
+ *
+ *   q, k, v, q_out, positions, slot_mapping, frequencies, rotary_dim,
+ *   interleaved, rope_scale   as gdn_rope_append_kv8's
+ *
+ * Errors: as gdn_rope_append_kv8's.
+ */
+int gdn_rope_append_kv4(const gdn_bf16 *q, int64_t q_stride, const gdn_bf16 *k, int64_t k_stride,
+                        const gdn_bf16 *v, int64_t v_stride, const int32_t *positions,
+                        const int64_t *slot_mapping, const double *frequencies, int32_t rotary_dim,
+                        int32_t interleaved, double rope_scale, gdn_bf16 *q_out, int64_t q_out_stride,
+                        uint8_t *k_cache, uint8_t *v_cache, uint8_t *k_scale, gdn_bf16 *v_scale,
+                        int32_t num_pages, int32_t page_size, int32_t num_tokens,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, void *stream);
+
+/*
+ * gdn_paged_read_kv4 -- ranges of keys and values read back out of the cache:
+ * contexts for another attention, another cache or another engine.
+ *
+ * Request s fills the rows [a, b) of out_start_loc[s], out_start_loc[s + 1]: row
+ * a + i is key key_starts[s] + i, as it lies at its row of its page of the block
+ * table.  k is exact in bf16, v rounded once.  Rows whose key has no page (-1 in
+ * the block table, or outside [0, num_pages), or past max_pages), and rows that no
+ * request owns, are left as they are.
+ *
+ *   block_table    int32 [num_seqs][block_table_stride], max_pages entries used
+ *   key_starts     int32 [num_seqs] (negative counts as 0), or NULL: from key 0 on
+ *   out_start_loc  int32 [num_seqs + 1], as query_start_loc, clamped to [0, num_rows)
+ *   k_out, v_out   bf16, row r head h at k_out + r*k_out_stride + h*head_dim; one
+ *                  of them may be NULL: not read
+ *
+ * Errors: GDN_ERR_INVALID (required pointer NULL, negative counts, num_kv_heads,
+ * num_pages or max_pages < 1, strides too small, an output overlapping an input or
+ * the other one); GDN_ERR_UNSUPPORTED (page_size, head_dim, alignment contract);
+ * GDN_ERR_HIP.
+ */
+int gdn_paged_read_kv4(const uint8_t *k_cache, const uint8_t *v_cache, const uint8_t *k_scale,
+                       const gdn_bf16 *v_scale, int32_t num_pages, int32_t page_size,
+                       const int32_t *block_table, int64_t block_table_stride, int32_t max_pages,
+                       const int32_t *key_starts, const int32_t *out_start_loc, gdn_bf16 *k_out,
+                       int64_t k_out_stride, gdn_bf16 *v_out, int64_t v_out_stride, int32_t num_seqs,
+                       int32_t num_rows, int32_t num_kv_heads, int32_t head_dim, void *stream);
+
+/*
+ * gdn_paged_attention_kv4 -- attention of a step's tokens over the 4-bit cache.
+ *
+ * Tokens, requests, masks, pages and what comes of rows that see no key are those
+ * of gdn_paged_attention_kv8; a masked key has no influence whatever its codes
+ * and scales hold.
+ *
+ * Scores are products of the cache's codes and scales with q in three 6-bit parts
+ * per 32 elements (exact for elements of at least 2^-7 of those 32's largest,
+ * within 2^-15 of that largest for smaller ones: bf16 itself is off by up to 2^-9
+ * of it there), summed in fp32; softmax statistics and sums are fp32.  A weight is
+ * rounded to bf16 in its product with a value, with the value's scale in it: off
+ * by at most 2^-8 of itself while that product is above 2^-126.  o is rounded to
+ * bf16.  A head of q with an infinity or NaN gives NaN, and so does a seen key or
+ * value whose scale is NaN.  Products with 2^127 and more overflow.  Results do not
+ * change from call to call (no atomics).
+ *
+ * The split of the work, and what a padded batch or a max_seq_len far above the
+ * lengths costs, are as gdn_paged_attention_kv8's.
+ *
+ *   scale        finite
+ *   others       as gdn_paged_attention_kv8's, the workspace of
+ *                gdn_paged_attention_kv4_workspace_size bytes
+ *
+ * Errors: as gdn_paged_attention_kv8's, and GDN_ERR_INVALID where scale is not
+ * finite.
+ */
+size_t gdn_paged_attention_kv4_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
+
+int gdn_paged_attention_kv4(const gdn_bf16 *q, int64_t q_stride, const uint8_t *k_cache,
+                            const uint8_t *v_cache, const uint8_t *k_scale, const gdn_bf16 *v_scale,
                             int32_t num_pages, int32_t page_size, const int32_t *block_table,
                             int64_t block_table_stride, int32_t max_pages, const int32_t *seq_lens,
                             const int32_t *query_start_loc, int32_t max_seq_len,
