@@ -559,19 +559,20 @@ def _on_current(names, *tensors):
     """Every tensor (None: not given) on the current GPU, whose number is
     returned."""
     cur = None
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        at = t.get_device()
-        if at != cur:
-            name = names.split()[i]
-            if at < 0:
-                raise ValueError("%s must be a GPU tensor, got one on %s" % (name, t.device))
-            if at != torch.cuda.current_device():
-                raise ValueError("%s is on cuda:%d but the current device is cuda:%d"
-                                 % (name, at, torch.cuda.current_device()))
-            cur = at
-    return cur
+    for t in tensors:
+        if t is not None and t.get_device() != cur:
+            if cur is not None:
+                break
+            cur = t.get_device()
+    else:
+        if cur is None or (cur >= 0 and cur == torch._C._cuda_getDevice()):
+            return cur
+    for name, t in zip(names.split(), tensors):
+        if t is not None and t.get_device() < 0:
+            raise ValueError("%s must be a GPU tensor, got one on %s" % (name, t.device))
+        if t is not None and t.get_device() != torch.cuda.current_device():
+            raise ValueError("%s is on cuda:%d but the current device is cuda:%d"
+                             % (name, t.get_device(), torch.cuda.current_device()))
 
 
 def _stream_on(stream, device):
@@ -654,7 +655,10 @@ def _bf16_heads(t, T, H, d, name):
     shape = (T, H, d)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    return _head_stride(shape, t.stride(), name)
+    strides = t.stride()
+    if T > 1 and strides[2] == 1 and strides[1] == d:
+        return strides[0]
+    return _head_stride(shape, strides, name)
 
 
 def _kv4(k_cache, v_cache, k_scale, v_scale):
@@ -665,9 +669,10 @@ def _kv4(k_cache, v_cache, k_scale, v_scale):
                         % (k_cache.dtype, v_cache.dtype, k_scale.dtype))
     if v_scale.dtype != torch.bfloat16:
         raise TypeError("v_scale must be torch.bfloat16, got %s" % v_scale.dtype)
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [pages][HK][page][D / 2], got shape %s" % (tuple(k_cache.shape),))
-    n, hk, page, half = k_cache.shape
+    shape = k_cache.shape
+    if len(shape) != 4:
+        raise ValueError("k_cache must be [pages][HK][page][D / 2], got shape %s" % (tuple(shape),))
+    n, hk, page, half = shape
     d = 2 * half
     if v_cache.shape != (n, hk, page // 16, d, 8):
         raise ValueError("v_cache must have shape %s, got %s" % ((n, hk, page // 16, d, 8), tuple(v_cache.shape)))

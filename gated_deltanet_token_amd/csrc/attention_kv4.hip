@@ -125,14 +125,22 @@ struct Q16 {
     u32x6 part[KS][P];
     uint32_t scale[KS];
 
-    __device__ __forceinline__ void load(const uint16_t *q, int g, uint32_t flip) {
+    struct Raw {
+        uint4 w[KS][4];
+    };
+    static __device__ __forceinline__ Raw load(const uint16_t *q, int g) {
+        Raw r;
+#pragma unroll
+        for (int st = 0; st < KS; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r.w[st][i] = *reinterpret_cast<const uint4 *>(q + (D == 64 ? 32 * (g & 1) : 128 * st + 32 * g) + 8 * i);
+        return r;
+    }
+    __device__ __forceinline__ void split(const Raw &r, int g, uint32_t flip) {
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
-            uint4 w[4];
-            const int e0 = D == 64 ? 32 * (g & 1) : 128 * st + 32 * g;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(q + e0 + 8 * i);
-            const SplitQ s = split_q(w, flip);
+            const SplitQ s = split_q(r.w[st], flip);
             if constexpr (D == 64) {
 #pragma unroll
                 for (int i = 0; i < 6; ++i) {
@@ -234,7 +242,10 @@ __device__ __forceinline__ void put8(const AttentionArgs &a, const Division &v, 
 // kv head, split of its keys).  Bound by reading the cache: each wave takes every
 // W-th tile of 64 keys straight from HBM into registers in the order of the
 // matrix operands (16-byte loads), with the next tile's keys and values on their
-// way while it works on this one.  The waves' sums are joined in the LDS.
+// way while it works on this one.  The waves' sums are joined in the LDS.  Of a
+// decode step of 32 requests of 1,100 keys (13.6 us) 1.3 us go to the request's
+// lengths, 2 to the first tile, 7 to 4.5 tiles of each wave, 1.5 to the join; 192
+// requests of 4,096 keys: 5.8 TB/s, as much as two tiles on their way, or more waves, gave.
 //
 // Lanes: with c = lane % 16 and g = lane / 16, a lane holds row c and the 16
 // keys from 16 g on of the tile, a granule of the cache: one page number per
@@ -243,75 +254,77 @@ __device__ __forceinline__ void put8(const AttentionArgs &a, const Division &v, 
 // neighbouring bytes.  Row i of the V operands 2 u and 2 u + 1 is element 32 u + 2 i
 // and the one behind it: a 16-byte load has both.
 // ---------------------------------------------------------------------------
-template <int D, int W>
-struct FewLds {
-    f32x4 red[W][D >= 128 ? 8 : D / 16][64];
-    float red_m[W][16], red_l[W][16];
+// one of a kv head's tiles of 16 rows of a request
+struct RowTile {
+    int lo, hi;              // keys that some row sees
+    int x0, x1;              // that every row sees
+    int i_row, h;            // the lane's row: its token within the request and q head
+    int jb, je;              // the keys that it sees
+    bool live;
+};
+__device__ __forceinline__ RowTile row_tile(const AttentionArgs &a, const Request &rq, int hk, int row0, int c) {
+    const int G = a.num_q_heads / a.num_kv_heads, n_rows = rq.n * G;
+    RowTile w;
+    key_range(a, rq, token_of(row0, G), w.lo, w.x1);
+    key_range(a, rq, token_of(last_row(row0, kTileRows, n_rows), G), w.x0, w.hi);
+    const int row = row0 + c;
+    w.live = row < n_rows;
+    w.i_row = w.live ? token_of(row, G) : 0;
+    w.h = w.live ? hk * G + row - w.i_row * G : hk * G;
+    w.jb = w.je = 0;
+    if (w.live) key_range(a, rq, w.i_row, w.jb, w.je);
+    return w;
+}
+
+// a lane's share of a row tile's sums, of the keys that its wave has taken
+template <int D>
+struct Sums {
+    f32x4 o[D / 16];
+    float m, l;              // l: the lane's own keys
 };
 
-template <int D, int W, Take TAKE>
-__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block, FewLds<D, W> &lds) {
-    constexpr int KS = Q16<D>::KS;
-    constexpr int DT = D / 16;                       // operands of 16 value elements
-    constexpr int DTH = DT < 8 ? DT : 8;             // of which joined at once
-
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 15, g = lane >> 4, kg = c >> 2;
-    const int G = a.num_q_heads / a.num_kv_heads;
-    // rows and workgroups of a launch are fewer than 2^31 (launch_d): 32-bit divisions
-    const unsigned unit = (unsigned)block / (unsigned)v.splits;
-    const int split = block - (int)(unit * v.splits);
-    const int tile = (int)(unit / (unsigned)a.num_kv_heads);
-    const int hk = (int)(unit - tile * a.num_kv_heads);
-    int within, s;
-    if constexpr (TAKE == Take::kSmall) {
-        // the first tiles, most of them the only ones, first
-        within = (unsigned)tile / (unsigned)a.num_seqs;
-        s = tile - within * a.num_seqs;
-    } else if (tile < a.num_seqs) {
-        s = tile;                                    // every request's first tile: no search
-        within = 0;
-    } else {
-        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, false, within);
-        ++within;
-    }
-    const Request rq = request_of(a, s);
-    const int n_rows = rq.n * G;
-    if (within < 0 || (long long)within * kTileRows >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
-    const int row0 = within * kTileRows, i_first = token_of(row0, G), i_last = token_of(last_row(row0, kTileRows, n_rows), G);
-    int lo, hi, x0, x1;                              // keys that some row sees, that every row sees
-    key_range(a, rq, i_first, lo, x1);
-    key_range(a, rq, i_last, x0, hi);
-    const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
-    if (split != sp.first && (split < sp.first || split > sp.last)) return;
-    const bool whole = sp.last <= sp.first;          // no other split: write o itself
-    const int k_lo = max(lo, split * v.chunk);
-    const int k_hi = split == v.splits - 1 ? hi : min(hi, (split + 1) * v.chunk);
-
-    const int row = row0 + c, i_row = token_of(row, G), h = hk * G + row - i_row * G;
-    const bool live = row < n_rows;
-    int jb = 0, je = 0;
-    if (live) key_range(a, rq, i_row, jb, je);
-    jb = max(jb, k_lo);
-    je = min(je, k_hi);
-
-    const int shift = __builtin_ctz(a.page), in_page = a.page - 1;
+// The block table's entries for a wave's tile of 64 keys at j: of the keys that the lane
+// loads and of the values.
+struct Entries {
+    int k, v;
+};
+__device__ __forceinline__ Entries entries_at(const AttentionArgs &a, int s, unsigned j) {
+    const int lane = threadIdx.x & 63, shift = __builtin_ctz(a.page);
     const int32_t *bt = a.block_table + s * a.block_table_stride;
+    const unsigned last = a.max_pages - 1;
+    return {bt[min((j + 16 * (lane >> 2 & 3)) >> shift, last)], bt[min((j + 16 * (lane >> 4)) >> shift, last)]};
+}
+
+// One wave takes the keys [k_lo, k_hi) of a row tile from `first` on, 64 at a time and
+// `step` further on the next time, one tile on its way while it works on another.
+// `next`: the entries of the first one.
+template <int D>
+__device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const Request &rq, int hk, const RowTile &w, int k_lo, int k_hi,
+                                          int first, int step, Entries next, Sums<D> &sum) {
+    constexpr int KS = Q16<D>::KS, DT = D / 16;      // DT operands of 16 value elements
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, kg = c >> 2;
+    const int jb = max(w.jb, k_lo), je = min(w.je, k_hi);
+    const int in_page = a.page - 1;
     auto good = [&](int p) { return (unsigned)p < (unsigned)a.num_pages; };
-    // Page numbers are loaded a tile ahead of the loads that use them, and not
-    // looked at before: loads come back in order, so that looking at one that was
-    // asked for behind a tile waits for the tile.
-    auto entry_at = [&](int j) { return bt[min(j >> shift, a.max_pages - 1)]; };
-    auto page_of = [&](int entry, int j) { return j < k_hi && good(entry) ? entry : -1; };
+    // Entries are loaded a tile ahead of the loads that use them, and not looked at
+    // before: loads come back in order, so that looking at one that was asked for
+    // behind a tile waits for the tile.  Keys are counted without a sign: a few tiles
+    // past the last one may lie past 2^31.  Tiles past it are loaded all the same, from
+    // the first page: with their loads under a condition the compiler cannot tell how
+    // many are on their way, and waits for all of them before the values of the tile
+    // at hand.
+    const unsigned end = max(k_hi, 0);
+    auto page_of = [&](int entry, unsigned j) { return j < end && good(entry) ? entry : -1; };
 
     uint4 kr[4][KS], vr[DT / 2], vw[2];
     uint32_t ks[KS];
-    auto load_k = [&](int j0, int page) {
-        const int j = j0 + 16 * kg + 4 * (c & 3);
-        const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk;
+    int pv;                                          // the values' page
+    auto load_k = [&](unsigned j0, int page) {
+        const int j = (int)(j0 + 16 * kg + 4 * (c & 3)) & in_page;
+        const long long ph = (long long)max(page, 0) * a.num_kv_heads + hk;
         const int block = D == 64 ? g & 1 : g;
-        const uint8_t *p = a.k_cache + (ph * a.page + (j & in_page)) * (D / 2) + 16 * block;
-        const uint8_t *sc = k_scales(a) + (ph * (D / 32) + block) * a.page + (j & in_page);
+        const uint8_t *p = a.k_cache + (ph * a.page + j) * (D / 2) + 16 * block;
+        const uint8_t *sc = k_scales(a) + (ph * (D / 32) + block) * a.page + j;
 #pragma unroll
         for (int st = 0; st < KS; ++st) ks[st] = *reinterpret_cast<const uint32_t *>(sc + 4 * st * a.page);
 #pragma unroll
@@ -319,45 +332,41 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 #pragma unroll
             for (int st = 0; st < KS; ++st) kr[t][st] = *reinterpret_cast<const uint4 *>(p + t * (D / 2) + 64 * st);
     };
-    auto load_v = [&](int j0, int page) {
-        const int j = j0 + 16 * g;
-        const long long ph = (long long)(good(page) ? page : 0) * a.num_kv_heads + hk, at = ph * a.page + (j & in_page);
+    auto load_v = [&](unsigned j0) {
+        const long long ph = (long long)max(pv, 0) * a.num_kv_heads + hk, at = ph * a.page + ((int)(j0 + 16 * g) & in_page);
         const uint4 *sc = reinterpret_cast<const uint4 *>(v_scales(a) + at);     // needed before the values
         vw[0] = sc[0];
         vw[1] = sc[1];
         const uint8_t *p = a.v_cache + at * (D / 2) + 16 * c;
 #pragma unroll
         for (int u = 0; u < DT / 2; ++u) vr[u] = *reinterpret_cast<const uint4 *>(p + 256 * u);
+        asm volatile("" ::: "memory");
     };
 
-    f32x4 o[DT] = {};
+#pragma unroll
+    for (int t = 0; t < DT; ++t) sum.o[t] = f32x4{};
     float m = kNegInf, l = 0.f;
-    constexpr int step = W * kTileKeys;
-    int j0 = first_tile(k_lo, kTileKeys, wave);
-    int ek = entry_at(j0 + 16 * kg), ev = entry_at(j0 + 16 * g), pv = -1;
-    // the next tile's keys, and the entries behind it
-    auto turn = [&](int j) {
-        const int pk = page_of(ek, j + 16 * kg), page = page_of(ev, j + 16 * g);
+    unsigned j0 = first;
+    // a tile's keys, and the entries of the one behind it
+    auto turn = [&](unsigned j) {
+        const int pk = page_of(next.k, j + 16 * kg);
+        pv = page_of(next.v, j + 16 * g);
         load_k(j, pk);
-        ek = entry_at(j + step + 16 * kg);
-        ev = entry_at(j + step + 16 * g);
-        return page;
+        next = entries_at(a, s, j + step);
+        asm volatile("" ::: "memory");
     };
-    if (j0 < k_hi) {
-        pv = turn(j0);
-        asm volatile("" ::: "memory");
-        load_v(j0, pv);
-        asm volatile("" ::: "memory");
-    }
-    // q is split while the first tile is on its way
+    // q is asked for before the first tile, and split while that is on its way
+    const auto raw = Q16<D>::load(a.q + (long long)(rq.begin + w.i_row) * a.q_stride + (long long)w.h * D, g);
+    asm volatile("" ::: "memory");
+    turn(j0);
+    load_v(j0);
+    __builtin_amdgcn_sched_barrier(0);
     Q16<D> q;
-    q.load(a.q + (long long)(rq.begin + (live ? i_row : 0)) * a.q_stride + (long long)(live ? h : hk * G) * D, g,
-           a.scale < 0.f ? 0x80008000u : 0u);
+    q.split(raw, g, a.scale < 0.f ? 0x80008000u : 0u);
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+    const int all0 = max(w.x0, k_lo), all1 = min(w.x1, k_hi) - kTileKeys;
 
-    for (; j0 < k_hi; j0 += step) {
-        const int jn = j0 + step;
-        int pv_n = -1;
+    for (; j0 < end; j0 += step) {
         f32x4 x[4] = {};
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
@@ -366,66 +375,193 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
             score16<2>(x[2], kr[2][st], ks[st], q, st);
             score16<3>(x[3], kr[3][st], ks[st], q, st);
         }
-        if (jn < k_hi) pv_n = turn(jn);
-        asm volatile("" ::: "memory");
-
         const bool seen_page = good(pv);
-        const bool masked = __any(!seen_page) || j0 < max(x0, k_lo) || j0 + kTileKeys > min(x1, k_hi);
+        turn(j0 + step);
+
+        const int j = (int)j0;
+        const bool masked = __any(!seen_page) || j < all0 || j > all1;
         float vs[16];
         unpack8(vw[0], vs);
         unpack8(vw[1], vs + 8);
         uint32_t pw[8];
-        weigh16(x, factor, vs, j0 - k_lo >= kLateKeys, masked, seen_page, j0 + 16 * g, jb, je, m, l, o, pw);
+        weigh16(x, factor, vs, j - k_lo >= kLateKeys, masked, seen_page, j + 16 * g, jb, je, m, l, sum.o, pw);
         const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
 #pragma unroll
         for (int u = 0; u < DT / 2; ++u) {
-            o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].x), p0, o[2 * u], 0, 0, 0);
-            o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].y), p1, o[2 * u], 0, 0, 0);
-            o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].z), p0, o[2 * u + 1], 0, 0, 0);
-            o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].w), p1, o[2 * u + 1], 0, 0, 0);
+            sum.o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].x), p0, sum.o[2 * u], 0, 0, 0);
+            sum.o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].y), p1, sum.o[2 * u], 0, 0, 0);
+            sum.o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].z), p0, sum.o[2 * u + 1], 0, 0, 0);
+            sum.o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].w), p1, sum.o[2 * u + 1], 0, 0, 0);
         }
-        if (jn < k_hi) load_v(jn, pv_n);
-        asm volatile("" ::: "memory");
-        pv = pv_n;
+        load_v(j0 + step);
     }
+    sum.m = m;
+    sum.l = l;
+}
 
-    // join the waves: maxima, then each wave's sums at the common maximum
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    if (g == 0) {
-        lds.red_m[wave][c] = m;
-        lds.red_l[wave][c] = l;
+// The waves' sums of a row tile, row by row.  Rows are 8 floats longer than they are, so
+// that four of them do not begin at the same bank.
+template <int D, int W>
+struct FewLds {
+    float sums[W][16][D + 8];
+    float m[W][16], l[W][16];
+};
+
+// The request with the r-th most keys, in 64 classes up to max_seq_len, and in order
+// within a class: found by a whole workgroup from a histogram, in every one alike.
+constexpr int kOrderThreads = 256, kOrdered = 4;        // passes over the requests
+
+struct OrderLds {
+    int count[64], wave[kOrdered][kOrderThreads / 64];
+    Request request;
+    int found;
+};
+__device__ __forceinline__ int nth_longest(const AttentionArgs &a, int r, OrderLds &lds, Request &rq) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    if (tid < 64) lds.count[tid] = 0;
+    __syncthreads();
+    const float classes = 64.f / (float)a.max_seq_len;
+    int part[kOrdered];
+    Request own[kOrdered];
+#pragma unroll
+    for (int i = 0; i < kOrdered; ++i) {
+        const int s = i * kOrderThreads + tid;
+        part[i] = -1;
+        if (s < a.num_seqs) {
+            own[i] = request_of(a, s);
+            int lo, hi, x;
+            key_range(a, own[i], 0, lo, x);
+            key_range(a, own[i], max(own[i].n - 1, 0), x, hi);
+            const int keys = own[i].n > 0 ? max(hi - lo, 0) : 0;
+            part[i] = 63 - (int)fminf(63.f, (float)keys * classes);
+            atomicAdd(&lds.count[part[i]], 1);
+        }
     }
     __syncthreads();
-    float m_all = kNegInf, l_all = 0.f;
+    const int n = lds.count[lane];
+    int up = n;
 #pragma unroll
-    for (int w = 0; w < W; ++w) m_all = fmaxf(m_all, lds.red_m[w][c]);
-    const float at = m_all == kNegInf ? 0.f : m_all;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int other = __shfl_up(up, d, 64);
+        if (lane >= d) up += other;
+    }
+    const int at = __builtin_ctzll(__ballot(up > r)), left = r - __shfl(up - n, at, 64);
+    unsigned long long mine[kOrdered];
 #pragma unroll
-    for (int w = 0; w < W; ++w) l_all += lds.red_l[w][c] * __builtin_amdgcn_exp2f(lds.red_m[w][c] - at);
-    const float f = __builtin_amdgcn_exp2f(m - at);
-    const long long out_row = part_row<TAKE>(a, s, rq.begin + i_row, h, row, hk);
-    const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+    for (int i = 0; i < kOrdered; ++i) {
+        mine[i] = __ballot(part[i] == at);
+        if (lane == 0) lds.wave[i][wave] = __builtin_popcountll(mine[i]);
+    }
+    __syncthreads();
+    int before = 0;
 #pragma unroll
-    for (int t0 = 0; t0 < DT; t0 += DTH) {
-        if (t0) __syncthreads();
+    for (int i = 0; i < kOrdered; ++i)
 #pragma unroll
-        for (int t = 0; t < DTH; ++t) lds.red[wave][t][lane] = o[t0 + t] * f;
-        __syncthreads();
-        for (int t = 2 * wave; t < DTH; t += 2 * W) {
-            f32x4 s0 = lds.red[0][t][lane], s1 = lds.red[0][t + 1][lane];
-#pragma unroll
-            for (int w = 1; w < W; ++w) {
-                s0 += lds.red[w][t][lane];
-                s1 += lds.red[w][t + 1][lane];
+        for (int w = 0; w < kOrderThreads / 64; ++w) {
+            if (w == wave && part[i] == at && before + __builtin_popcountll(mine[i] & ((1ull << lane) - 1)) == left) {
+                lds.request = own[i];
+                lds.found = i * kOrderThreads + tid;
             }
-            if (live) put8(a, v, whole, inv, s0, s1, rq.begin + i_row, h, out_row, split, 16 * (t0 + t) + 8 * g);
+            before += lds.wave[i][w];
+        }
+    __syncthreads();
+    rq = lds.request;
+    const int s = __builtin_amdgcn_readfirstlane(lds.found);
+    __syncthreads();                     // (the LDS has another use behind this)
+    return s;
+}
+
+template <int D, int W, Take TAKE>
+__device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block, FewLds<D, W> &lds, OrderLds *order = nullptr) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    // rows and workgroups of a launch are fewer than 2^31 (launch_d): 32-bit divisions
+    const unsigned unit = (unsigned)block / (unsigned)v.splits;
+    const int split = block - (int)(unit * v.splits);
+    const int tile = (int)(unit / (unsigned)a.num_kv_heads);
+    const int hk = (int)(unit - tile * a.num_kv_heads);
+    int within, s;
+    Request rq{};
+    if constexpr (TAKE == Take::kSmall) {
+        // the first tiles, most of them the only ones, first
+        within = (unsigned)tile / (unsigned)a.num_seqs;
+        s = tile - within * a.num_seqs;
+    } else if (tile < a.num_seqs) {
+        s = tile;                                    // every request's first tile: no search
+        within = 0;
+        if (order) s = nth_longest(a, tile, *order, rq);
+    } else {
+        s = find_request(a, tile - a.num_seqs, G, kTileRows, 0, false, within);
+        ++within;
+    }
+    // without a window the part's first key is known before its request is
+    const int start = a.window ? 0 : split * v.chunk + wave * kTileKeys;
+    Entries next = entries_at(a, s, start);
+    asm volatile("" ::: "memory");
+    if (!order || tile >= a.num_seqs) rq = request_of(a, s);
+    const int n_rows = rq.n * G;
+    if (within < 0 || (long long)within * kTileRows >= n_rows || (TAKE == Take::kSmall && n_rows > kSmallRows)) return;
+    const int row0 = within * kTileRows;
+    const RowTile w = row_tile(a, rq, hk, row0, c);
+    const Splits sp = splits_of(w.lo, w.hi, v.chunk, v.splits);
+    if (split != sp.first && (split < sp.first || split > sp.last)) return;
+    const bool whole = sp.last <= sp.first;          // no other split: write o itself
+    const int k_lo = max(w.lo, split * v.chunk);
+    const int k_hi = split == v.splits - 1 ? w.hi : min(w.hi, (split + 1) * v.chunk);
+    const int first = first_tile(k_lo, kTileKeys, wave);
+    if (first != start) next = entries_at(a, s, first);
+    Sums<D> sum;
+    take_keys<D>(a, s, rq, hk, w, k_lo, k_hi, first, W * kTileKeys, next, sum);
+
+    // join the waves: maxima, then each wave's sums at the common maximum
+    float l = sum.l;
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (w.live) {
+        float *p = &lds.sums[wave][c][8 * g];
+#pragma unroll
+        for (int t = 0; t < D / 16; t += 2) {
+            const f32x4 s0 = sum.o[t], s1 = sum.o[t + 1];
+            *reinterpret_cast<f32x4 *>(p + 16 * t) = f32x4{s0.x, s1.x, s0.y, s1.y};
+            *reinterpret_cast<f32x4 *>(p + 16 * t + 4) = f32x4{s0.z, s1.z, s0.w, s1.w};
+        }
+        if (g == 0) {
+            lds.m[wave][c] = sum.m;
+            lds.l[wave][c] = l;
         }
     }
-    if (!whole && wave == 0 && g == 0 && live) {
-        float *ml = part_ml(v, out_row, split);
-        ml[0] = m_all;
-        ml[1] = l_all;
+    __syncthreads();
+    const int rows = min(n_rows - row0, kTileRows), h0 = hk * G;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * W) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float m = kNegInf, all = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) m = fmaxf(m, lds.m[j][r]);
+        const float at = m == kNegInf ? 0.f : m;
+        f32x4 o = {};
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float f = __builtin_amdgcn_exp2f(lds.m[j][r] - at);
+            all += lds.l[j][r] * f;
+            o += *reinterpret_cast<const f32x4 *>(&lds.sums[j][r][d]) * f;
+        }
+        const int row = row0 + r, i_row = token_of(row, G), h = h0 + row - i_row * G;
+        if (whole) {
+            const float inv = all == 0.f ? 0.f : 1.f / all;
+            uint2 y;
+            y.x = pack_bf16x2(o.x * inv, o.y * inv);
+            y.y = pack_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2 *>(a.o + (long long)(rq.begin + i_row) * a.o_stride + (long long)h * D + d) = y;
+        } else {
+            const long long out_row = part_row<TAKE>(a, s, rq.begin + i_row, h, row, hk);
+            *reinterpret_cast<f32x4 *>(part_o(v, D, out_row, split) + d) = o;
+            if (d == 0) {
+                float *ml = part_ml(v, out_row, split);
+                ml[0] = m;
+                ml[1] = all;
+            }
+        }
     }
 }
 
@@ -719,7 +855,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     je = min(je, k_hi);
     const WaveKeys wk = wave_keys(a, w, wrow, 16);
     Q16<D> q;
-    q.load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g, a.scale < 0.f ? 0x80008000u : 0u);
+    q.split(Q16<D>::load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), g, a.scale < 0.f ? 0x80008000u : 0u);
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
 
     Staging<D, kNarrowThreads, k_place_narrow<D>> stage(a, lds, w);
@@ -791,10 +927,13 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 // workgroups first, those of the small ones (decode rows) take the CUs that
 // are left and each that becomes free.
 // ---------------------------------------------------------------------------
-template <int D>
-__global__ __launch_bounds__(512, 2) void attention_few_kv4_kernel(AttentionArgs a, Division v) {
-    __shared__ FewLds<D, 8> lds;
-    few_rows<D, 8, Take::kAll>(a, v, blockIdx.x, lds);
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void attention_few_kv4_kernel(AttentionArgs a, Division v, bool ordered) {
+    __shared__ union {
+        FewLds<D, W> few;
+        OrderLds order;
+    } lds;
+    few_rows<D, W, Take::kAll>(a, v, blockIdx.x, lds.few, ordered ? &lds.order : nullptr);
 }
 
 constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThreads; }
@@ -813,7 +952,25 @@ __global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kv4_kerne
     else many_rows_wide<D>(a, many, block, many_blocks, lds.many);
 }
 
-static SplitRules rules(int d) { return {1024, 512, 256, mixed_threads(d) / 64, d == 256 ? kCUs : 2 * kCUs}; }
+// A decode call's keys are split until there is a workgroup for every CU, into
+// parts of 1,024 keys or more, or of 512 where three of four CUs are idle (one
+// request of 4,000 keys, 16/4 heads of 256: 14.5 us, 10 and 5 to join the parts).
+constexpr int kMinChunk = 1024, kIdleChunk = 512, kManyChunk = 256;
+static SplitRules rules(int d) {
+    return {kMinChunk, kIdleChunk, kManyChunk, mixed_threads(d) / 64, d == 256 ? kCUs : 2 * kCUs};
+}
+
+// Workgroups of four waves: two of them on a CU, one of which streams while the other begins or
+// ends (192 requests of 4,096 keys, 32/8 heads of 128: 146 us, 156 with eight waves; 32 of
+// 1,100, 16/4 of 256: 13.6, 14.4).  Of eight where parts are long and there is one for
+// a CU at most (five of 40,000 to 131,000: 108 us, 113 with four; eight of up to
+// 30,000: 37.6 and 40.9).
+constexpr int kLongPart = 2048;
+// Longest requests first where there are two rounds of workgroups and more: the last ones
+// then end together (200 requests of 1 to 8,000 keys, 32/8 heads of 128: 168 us, 184 in
+// order).  Finding its request costs a workgroup 1.9 us (100 requests of 1,000 to 2,000, 32/8 of
+// 64, in one round: 27.8 us, 24.7 in order).
+constexpr int kManyUnits = 4 * kCUs;
 
 int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d, int max_seq_len) {
     const Plan p = plan_of(rules(d), num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
@@ -828,7 +985,12 @@ static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
         return hipErrorInvalidConfiguration;
     const Division vf = division(p.few, false, D, a.workspace);
     if (p.few_takes == Take::kAll) {
-        hipLaunchKernelGGL((attention_few_kv4_kernel<D>), dim3((unsigned)few), dim3(512), 0, stream, a, vf);
+        const dim3 grid((unsigned)few);
+        if (p.few.splits > 1 && p.few.chunk >= kLongPart)
+            hipLaunchKernelGGL((attention_few_kv4_kernel<D, 8>), grid, dim3(512), 0, stream, a, vf, false);
+        else
+            hipLaunchKernelGGL((attention_few_kv4_kernel<D, 4>), grid, dim3(kOrderThreads), 0, stream, a, vf,
+                               (long long)a.num_tokens * a.num_kv_heads > kManyUnits && a.num_seqs <= kOrdered * kOrderThreads);
         launch_join(Take::kAll, a, p.few, vf, kTileRows, stream);
         return hipGetLastError();
     }

@@ -64,6 +64,20 @@ __device__ __forceinline__ int find_request(const AttentionArgs &a, long long ti
     return lo;
 }
 
+// the request of token t, or the last one that begins before it, 64 candidates per step
+__device__ __forceinline__ int find_token(const AttentionArgs &a, int t) {
+    const int lane = threadIdx.x & 63;
+    int s = 0, n = a.num_seqs;
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const unsigned long long b = __ballot(lane * step < n && a.qsl[s + lane * step] <= t);
+        const int k = b ? 63 - __builtin_clzll(b) : 0;
+        s += k * step;
+        n = min(step, n - k * step);
+    }
+    return s;
+}
+
 // The larger of a lane's value and that of the lane 32 (16) further or back: the
 // swap of half-waves (of neighbouring rows of 16) between two copies leaves both
 // lanes' values in each.  (The compiler must not see that they are copies: it

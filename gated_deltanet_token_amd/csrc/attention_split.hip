@@ -25,15 +25,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Di
     } else {
         t = (int)(part / (unsigned)a.num_q_heads);
         h = (int)(part - (unsigned)t * a.num_q_heads);
-        s = 0;
-        int n = a.num_seqs;                 // the request of token t, 64 candidates per step
-        while (n > 1) {
-            const int step = (n + 63) / 64;
-            const unsigned long long b = __ballot(lane * step < n && a.qsl[s + lane * step] <= t);
-            const int k = b ? 63 - __builtin_clzll(b) : 0;
-            s += k * step;
-            n = min(step, n - k * step);
-        }
+        s = find_token(a, t);
     }
     const Request rq = request_of(a, s);
     const int n_rows = rq.n * G;

@@ -381,6 +381,34 @@ def test_more_requests_than_a_wave():
     Case(19, [(int(r.integers(1, 60)), 1) for _ in range(300)], 4, 2, 64, 16).check()
 
 
+@pytest.mark.parametrize("d,hk", [(64, 8), (128, 5), (256, 4)])
+@pytest.mark.parametrize("S", [257, 1024, 1025])
+def test_many_requests_of_unlike_lengths(d, hk, S):
+    """Over 1,024 (request, kv head) pairs, taken longest first up to 1,024 requests: empty ones,
+    some with several tokens, equal lengths and one far longer than the others among them."""
+    r = np.random.default_rng(S + d)
+    n = np.ones(S, int)
+    n[r.permutation(S)[:S // 4]] = 0
+    n[r.permutation(np.flatnonzero(n == 0))[:3]] = (2, 7, 20)
+    L = np.where(r.random(S) < 0.3, 20, r.integers(0, 70, S))
+    L[r.integers(0, S)] = 700
+    lens = [(max(int(a), int(b)) if r.random() < 0.9 else int(a), int(b)) for a, b in zip(L, n)]
+    if sum(n) * hk <= 1024:
+        hk = -(-1025 // int(sum(n)))
+    c = Case(S, lens, hk, hk, d, 16)
+    assert c.qsl[-1] <= S and c.qsl[-1] * hk > 1024
+    c.check()
+    if S == 257:
+        c.check(longest=30)
+        c.check(window=9)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_long_parts(d):
+    """Parts of 2,048 keys and more, joined."""
+    Case(27, [(9000, 1)] * 2 + [(20, 1), (30000, 1)] + [(7000, 1)] * 6, 10, 10, d, 16).check()
+
+
 def test_caller_workspace_of_any_content():
     c = Case(20, [(6000, 1), (70, 1)], 8, 2, 128, 16)
     n = gdn.gdn_paged_attention_kv4_workspace_size(2, 2, 8, 2, 128, 6000)
