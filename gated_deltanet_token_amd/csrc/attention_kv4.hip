@@ -586,76 +586,57 @@ struct ManyLds {
     int ok[2][4];                          // whether the tile's four granules have a page
 };
 
-// Staging of a workgroup of THREADS threads, D / 2 of them per granule of 16 keys:
-// a thread has one 16-byte piece of keys, one of values, and the first ones four
-// keys' scales or two values' of the same granule, of one page.
+// Staging: D / 2 pieces of 16 bytes of a granule's keys, and as many of its values.  A
+// thread has one of each (at D = 64 one of either), of one page: the first ones also
+// four keys' scales or two values' of the same granule.  As in take_keys, loads are
+// without conditions, tiles past the last one come from the first page.
 template <int D, int THREADS, int (*PLACE)(int, int)>
 struct Staging {
-    static constexpr int PER = D / 2, USED = 4 * PER, PPK = D / 32;
-    static_assert(USED <= THREADS, "");
-    const AttentionArgs &a;
-    ManyLds<D> &lds;
+    static constexpr int PER = D / 2, PPK = D / 32;
+    static constexpr bool BOTH = 4 * PER == THREADS;
+    static_assert(BOTH || 8 * PER == THREADS, "");
     const int32_t *bt;
-    int k_hi, shift, in_page, hk, granule, i;
-    // the block table's entry for the granule of the tile to load next, as it came
-    // (looking at it here would wait for it and all loads before it)
-    int entry, tile, own;
-    uint4 kr, vr;
+    int granule, i;
+    bool keys, values;
+    unsigned end;
+    u32x4 kr, vr;                // what is on its way
     uint32_t sc;
+    int entry, own;              // the block table's entry for the tile behind it, as it came; its page
 
-    __device__ __forceinline__ Staging(const AttentionArgs &a_, ManyLds<D> &lds_, const ManyShare &w)
-        : a(a_), lds(lds_), bt(a_.block_table + w.s * a_.block_table_stride), k_hi(w.k_hi), shift(__builtin_ctz(a_.page)),
-          in_page(a_.page - 1), hk(w.hk), granule(threadIdx.x / PER), i(threadIdx.x % PER), entry(-1), tile(0), own(-1), sc(0) {}
-    __device__ __forceinline__ bool works() const { return USED == THREADS || (int)threadIdx.x < USED; }
-    __device__ __forceinline__ void pages(int j0) {
-        tile = j0;
-        if (works()) entry = bt[min((j0 + 16 * granule) >> shift, a.max_pages - 1)];
+    __device__ __forceinline__ Staging(const AttentionArgs &a, const ManyShare &w)
+        : bt(a.block_table + w.s * a.block_table_stride), granule((threadIdx.x % (4 * PER)) / PER), i(threadIdx.x % PER),
+          keys(BOTH || threadIdx.x < 4 * PER), values(BOTH || threadIdx.x >= 4 * PER), end(max(w.k_hi, 0)) {}
+    __device__ __forceinline__ void pages(const AttentionArgs &a, unsigned j0) {
+        entry = bt[min((j0 + 16 * granule) >> __builtin_ctz(a.page), (unsigned)a.max_pages - 1)];
     }
-    __device__ __forceinline__ void load() {
-        if (!works()) return;
-        const int j = tile + 16 * granule;
-        own = j < k_hi && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
-        const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk, at = ph * a.page + (j & in_page);
-        kr = *reinterpret_cast<const uint4 *>(a.k_cache + at * (D / 2) + 16 * i);
-        vr = *reinterpret_cast<const uint4 *>(a.v_cache + at * (D / 2) + 16 * i);
-        if (i < D / 8)
-            sc = *reinterpret_cast<const uint32_t *>(k_scales(a) + (ph * (D / 32) + i / 4) * a.page + (j & in_page) + 4 * (i % 4));
-        else if (i < D / 8 + 8)
-            sc = *reinterpret_cast<const uint32_t *>(v_scales(a) + at + 2 * (i - D / 8));
-    }
-    __device__ __forceinline__ void put(int buf) {
-        if (!works()) return;
-        lds.k[buf][PLACE(16 * granule + i / PPK, i % PPK)] = kr;
-        lds.v[buf][granule * PER + i] = vr;
-        if (i < D / 8) {
-            lds.ks[buf][(i / 4) * 16 + granule * 4 + i % 4] = sc;
-        } else if (i < D / 8 + 8) {
-            const int at = 16 * granule + 2 * (i - D / 8);
-            lds.vs[buf][at] = bf16_lo(sc);
-            lds.vs[buf][at + 1] = bf16_hi(sc);
+    __device__ __forceinline__ void load(const AttentionArgs &a, int hk, unsigned j0) {
+        const unsigned j = j0 + 16 * granule;
+        own = j < end && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
+        const int in_page = (int)j & (a.page - 1);
+        const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk, at = ph * a.page + in_page;
+        if constexpr (BOTH) {
+            kr = *reinterpret_cast<const u32x4 *>(a.k_cache + at * (D / 2) + 16 * i);
+            vr = *reinterpret_cast<const u32x4 *>(a.v_cache + at * (D / 2) + 16 * i);
+        } else {
+            kr = vr = *reinterpret_cast<const u32x4 *>((keys ? a.k_cache : a.v_cache) + at * (D / 2) + 16 * i);
         }
-        if (i == 0) lds.ok[buf][granule] = own >= 0;
+        const uint8_t *ks = k_scales(a) + (ph * (D / 32) + i / 4 % PPK) * a.page + in_page + 4 * (i % 4);
+        const uint8_t *vs = reinterpret_cast<const uint8_t *>(v_scales(a) + at + 2 * (i % 8));
+        sc = *reinterpret_cast<const uint32_t *>(i < D / 8 ? ks : vs);
     }
-    __device__ __forceinline__ void begin(int j0) {
-        pages(j0);
-        load();
-        pages(j0 + kTileKeys);
-        put(0);
-        __syncthreads();
-    }
-    // before the work on the tile at j0: the next one's loads go out
-    __device__ __forceinline__ void ahead(int j0) {
-        if (j0 + kTileKeys < k_hi) {
-            load();
-            pages(j0 + 2 * kTileKeys);
+    __device__ __forceinline__ void put(ManyLds<D> &lds, int buf) const {
+        if (keys) {
+            *reinterpret_cast<u32x4 *>(&lds.k[buf][PLACE(16 * granule + i / PPK, i % PPK)]) = kr;
+            if (i < D / 8) {
+                lds.ks[buf][(i / 4) * 16 + granule * 4 + i % 4] = sc;
+            } else if (i < D / 8 + 8) {
+                const int at = 16 * granule + 2 * (i - D / 8);
+                lds.vs[buf][at] = bf16_lo(sc);
+                lds.vs[buf][at + 1] = bf16_hi(sc);
+            }
+            if (i == 0) lds.ok[buf][granule] = own >= 0;
         }
-        asm volatile("" ::: "memory");
-    }
-    // after it: into the other buffer
-    __device__ __forceinline__ void next(int j0, int buf) {
-        asm volatile("" ::: "memory");
-        if (j0 + kTileKeys < k_hi) put(buf ^ 1);
-        __syncthreads();
+        if (values) *reinterpret_cast<u32x4 *>(&lds.v[buf][granule * PER + i]) = vr;
     }
 };
 
@@ -717,16 +698,24 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     }
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
 
-    Staging<D, kWideThreads, k_place<D>> stage(a, lds, w);
+    Staging<D, kWideThreads, k_place<D>> stage(a, w);
     const int key = 32 * (c >> 2 & 1) + 8 * (c >> 3) + 2 * (c & 3);
     const int k_row = k_place<D>(key, 0) & ~(D / 32 - 1), k_swap = k_place<D>(key, h2) - k_row;
     f32x16 o[DT] = {};
     float m = kNegInf, l = 0.f;
     int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
-    if (j0 < k_hi) stage.begin(j0);
+    if (j0 < k_hi) {
+        stage.pages(a, j0);
+        stage.load(a, hk, j0);
+        stage.pages(a, j0 + kTileKeys);
+        stage.put(lds, 0);
+        __syncthreads();
+    }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.ahead(j0);
+        stage.load(a, hk, jn);
+        stage.pages(a, jn + kTileKeys);
+        __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {
             const bool ok0 = lds.ok[buf][2 * h2] != 0, ok1 = lds.ok[buf][2 * h2 + 1] != 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1)), late = j0 - k_lo >= kLateKeys;
@@ -796,7 +785,9 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 }
             }
         }
-        stage.next(j0, buf);
+        __builtin_amdgcn_sched_barrier(0);
+        stage.put(lds, buf ^ 1);
+        __syncthreads();
     }
 
     l += __shfl_xor(l, 32, 64);
@@ -858,16 +849,24 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     q.split(Q16<D>::load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), g, a.scale < 0.f ? 0x80008000u : 0u);
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
 
-    Staging<D, kNarrowThreads, k_place_narrow<D>> stage(a, lds, w);
+    Staging<D, kNarrowThreads, k_place_narrow<D>> stage(a, w);
     const int key = 16 * (c >> 2) + 4 * (c & 3);
     const int k_row = k_place_narrow<D>(key, 0) & ~7, k_swap = k_place_narrow<D>(key, g) & 7;
     f32x4 o[DT] = {};
     float m = kNegInf, l = 0.f;
     int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
-    if (j0 < k_hi) stage.begin(j0);
+    if (j0 < k_hi) {
+        stage.pages(a, j0);
+        stage.load(a, hk, j0);
+        stage.pages(a, j0 + kTileKeys);
+        stage.put(lds, 0);
+        __syncthreads();
+    }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.ahead(j0);
+        stage.load(a, hk, jn);
+        stage.pages(a, jn + kTileKeys);
+        __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {
             const bool ok = lds.ok[buf][g] != 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
@@ -904,7 +903,9 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.w), p1, o[2 * u + 1], 0, 0, 0);
             }
         }
-        stage.next(j0, buf);
+        __builtin_amdgcn_sched_barrier(0);
+        stage.put(lds, buf ^ 1);
+        __syncthreads();
     }
 
     l += __shfl_xor(l, 16, 64);
