@@ -167,6 +167,10 @@ __device__ __forceinline__ void score16(f32x4 &x, const uint4 &k, uint32_t ks, c
         x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(k), operand(q.part[st][2]), x, kE2m1, kE2m3, T, ks, 2, q.scale[st]);
 }
 
+// The larger of two scores, NaN if one is (the row is, then, whatever its maximum: fmaxf
+// would first turn each operand into a quiet one).
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 // A new maximum of a row and what its sums are multiplied by, where some row of the
 // wave is past its own.
 __device__ __forceinline__ bool new_maximum(float mx, bool late, float &m, float &f) {
@@ -200,7 +204,7 @@ __device__ __forceinline__ void weigh16(f32x4 (&x)[4], float factor, float (&vs)
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[t][r]);
+        for (int r = 0; r < 4; ++r) mx = larger(mx, x[t][r]);
     mx = max_over32(max_over16(mx)) * factor;
     float f;
     if (new_maximum(mx, late, m, f)) {
@@ -319,12 +323,16 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
     uint4 kr[4][KS], vr[DT / 2], vw[2];
     uint32_t ks[KS];
     int pv;                                          // the values' page
-    auto load_k = [&](unsigned j0, int page) {
-        const int j = (int)(j0 + 16 * kg + 4 * (c & 3)) & in_page;
-        const long long ph = (long long)max(page, 0) * a.num_kv_heads + hk;
-        const int block = D == 64 ? g & 1 : g;
-        const uint8_t *p = a.k_cache + (ph * a.page + j) * (D / 2) + 16 * block;
-        const uint8_t *sc = k_scales(a) + (ph * (D / 32) + block) * a.page + j;
+    // a tile begins at a multiple of 64 keys: places in a page stay the same
+    const uint32_t pitch = (uint32_t)(a.num_kv_heads * a.page) * (D / 2);        // bytes of codes, all kv heads
+    const uint32_t k_row = hk * a.page + (16 * kg + 4 * (c & 3) & in_page), v_row = hk * a.page + (16 * g & in_page);
+    const uint8_t *k_at = a.k_cache + (k_row * (D / 2) + 16 * (D == 64 ? g & 1 : g));
+    const uint8_t *ks_at = k_scales(a) + ((hk * (D / 32) + (D == 64 ? g & 1 : g)) * a.page + (16 * kg + 4 * (c & 3) & in_page));
+    const uint8_t *v_at = a.v_cache + (v_row * (D / 2) + 16 * c);
+    const uint8_t *vs_at = reinterpret_cast<const uint8_t *>(v_scales(a) + v_row);
+    auto load_k = [&](int page) {
+        const uint64_t off = (uint64_t)(uint32_t)max(page, 0) * pitch;
+        const uint8_t *p = k_at + off, *sc = ks_at + (off >> 4);                 // (scales: a 16th of the codes)
 #pragma unroll
         for (int st = 0; st < KS; ++st) ks[st] = *reinterpret_cast<const uint32_t *>(sc + 4 * st * a.page);
 #pragma unroll
@@ -332,12 +340,12 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
 #pragma unroll
             for (int st = 0; st < KS; ++st) kr[t][st] = *reinterpret_cast<const uint4 *>(p + t * (D / 2) + 64 * st);
     };
-    auto load_v = [&](unsigned j0) {
-        const long long ph = (long long)max(pv, 0) * a.num_kv_heads + hk, at = ph * a.page + ((int)(j0 + 16 * g) & in_page);
-        const uint4 *sc = reinterpret_cast<const uint4 *>(v_scales(a) + at);     // needed before the values
+    auto load_v = [&]() {
+        const uint64_t off = (uint64_t)(uint32_t)max(pv, 0) * pitch;
+        const uint4 *sc = reinterpret_cast<const uint4 *>(vs_at + (off >> __builtin_ctz(D / 4)));        // needed before the values
         vw[0] = sc[0];
         vw[1] = sc[1];
-        const uint8_t *p = a.v_cache + at * (D / 2) + 16 * c;
+        const uint8_t *p = v_at + off;
 #pragma unroll
         for (int u = 0; u < DT / 2; ++u) vr[u] = *reinterpret_cast<const uint4 *>(p + 256 * u);
         asm volatile("" ::: "memory");
@@ -351,7 +359,7 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
     auto turn = [&](unsigned j) {
         const int pk = page_of(next.k, j + 16 * kg);
         pv = page_of(next.v, j + 16 * g);
-        load_k(j, pk);
+        load_k(pk);
         next = entries_at(a, s, j + step);
         asm volatile("" ::: "memory");
     };
@@ -359,7 +367,7 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
     const auto raw = Q16<D>::load(a.q + (long long)(rq.begin + w.i_row) * a.q_stride + (long long)w.h * D, g);
     asm volatile("" ::: "memory");
     turn(j0);
-    load_v(j0);
+    load_v();
     __builtin_amdgcn_sched_barrier(0);
     Q16<D> q;
     q.split(raw, g, a.scale < 0.f ? 0x80008000u : 0u);
@@ -393,7 +401,7 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
             sum.o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].z), p0, sum.o[2 * u + 1], 0, 0, 0);
             sum.o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(vr[u].w), p1, sum.o[2 * u + 1], 0, 0, 0);
         }
-        load_v(j0 + step);
+        load_v();
     }
     sum.m = m;
     sum.l = l;
@@ -599,30 +607,40 @@ struct Staging {
     int granule, i;
     bool keys, values;
     unsigned end;
+    // of a page: bytes of codes, of all kv heads; where the thread's piece and its scales
+    // are (a tile begins at a multiple of 64 keys: the same in every one)
+    uint32_t pitch, at, sc_at, sc_shift;
+    const uint8_t *sc_base;
     u32x4 kr, vr;                // what is on its way
     uint32_t sc;
     int entry, own;              // the block table's entry for the tile behind it, as it came; its page
 
     __device__ __forceinline__ Staging(const AttentionArgs &a, const ManyShare &w)
         : bt(a.block_table + w.s * a.block_table_stride), granule((threadIdx.x % (4 * PER)) / PER), i(threadIdx.x % PER),
-          keys(BOTH || threadIdx.x < 4 * PER), values(BOTH || threadIdx.x >= 4 * PER), end(max(w.k_hi, 0)) {}
+          keys(BOTH || threadIdx.x < 4 * PER), values(BOTH || threadIdx.x >= 4 * PER), end(max(w.k_hi, 0)),
+          pitch((uint32_t)(a.num_kv_heads * a.page) * PER) {
+        const uint32_t in_page = 16 * granule & (a.page - 1), row = w.hk * a.page + in_page;
+        at = row * PER + 16 * i;
+        // key scales are a 16th of the codes, value scales 2 of a token's D / 2 bytes
+        const bool of_keys = i < D / 8;
+        sc_base = of_keys ? k_scales(a) : reinterpret_cast<const uint8_t *>(v_scales(a));
+        sc_shift = of_keys ? 4 : __builtin_ctz(PER / 2);
+        sc_at = of_keys ? (w.hk * PPK + i / 4) * a.page + in_page + 4 * (i % 4) : 2 * row + 4 * (i % 8);
+    }
     __device__ __forceinline__ void pages(const AttentionArgs &a, unsigned j0) {
         entry = bt[min((j0 + 16 * granule) >> __builtin_ctz(a.page), (unsigned)a.max_pages - 1)];
     }
-    __device__ __forceinline__ void load(const AttentionArgs &a, int hk, unsigned j0) {
+    __device__ __forceinline__ void load(const AttentionArgs &a, unsigned j0) {
         const unsigned j = j0 + 16 * granule;
         own = j < end && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
-        const int in_page = (int)j & (a.page - 1);
-        const long long ph = (long long)max(own, 0) * a.num_kv_heads + hk, at = ph * a.page + in_page;
+        const uint64_t page = (uint64_t)(uint32_t)max(own, 0) * pitch;
         if constexpr (BOTH) {
-            kr = *reinterpret_cast<const u32x4 *>(a.k_cache + at * (D / 2) + 16 * i);
-            vr = *reinterpret_cast<const u32x4 *>(a.v_cache + at * (D / 2) + 16 * i);
+            kr = *reinterpret_cast<const u32x4 *>(a.k_cache + (page + at));
+            vr = *reinterpret_cast<const u32x4 *>(a.v_cache + (page + at));
         } else {
-            kr = vr = *reinterpret_cast<const u32x4 *>((keys ? a.k_cache : a.v_cache) + at * (D / 2) + 16 * i);
+            kr = vr = *reinterpret_cast<const u32x4 *>((keys ? a.k_cache : a.v_cache) + (page + at));
         }
-        const uint8_t *ks = k_scales(a) + (ph * (D / 32) + i / 4 % PPK) * a.page + in_page + 4 * (i % 4);
-        const uint8_t *vs = reinterpret_cast<const uint8_t *>(v_scales(a) + at + 2 * (i % 8));
-        sc = *reinterpret_cast<const uint32_t *>(i < D / 8 ? ks : vs);
+        sc = *reinterpret_cast<const uint32_t *>(sc_base + ((page >> sc_shift) + sc_at));
     }
     __device__ __forceinline__ void put(ManyLds<D> &lds, int buf) const {
         if (keys) {
@@ -706,14 +724,14 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
     if (j0 < k_hi) {
         stage.pages(a, j0);
-        stage.load(a, hk, j0);
+        stage.load(a, j0);
         stage.pages(a, j0 + kTileKeys);
         stage.put(lds, 0);
         __syncthreads();
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.load(a, hk, jn);
+        stage.load(a, jn);
         stage.pages(a, jn + kTileKeys);
         __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {
@@ -746,7 +764,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             }
             float mx = kNegInf;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, fmaxf(x[0][r], x[1][r]));
+            for (int r = 0; r < 16; ++r) mx = larger(larger(mx, x[0][r]), x[1][r]);
             mx = max_over32(mx) * factor;
             float f;
             if (new_maximum(mx, late, m, f)) {
@@ -755,14 +773,16 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 for (int i = 0; i < DT; ++i) o[i] *= f;
             }
             const float at = m == kNegInf ? 0.f : m;
-            const f32x4 *vst = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 32 * h2);
+            f32x4 vs[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) vs[i] = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 32 * h2)[i];
+            if (masked)
+#pragma unroll
+                for (int r = 0; r < 32; ++r) vs[r / 4][r & 3] = x[r & 1][r / 2] == kNegInf ? 0.f : vs[r / 4][r & 3];
             uint32_t pw[16];
 #pragma unroll
             for (int r = 0; r < 16; r += 2) {
-                f32x4 s = vst[r / 2];
-                if (masked)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[e] = x[e & 1][r + e / 2] == kNegInf ? 0.f : s[e];
+                const f32x4 s = vs[r / 2];
                 const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[0][r], factor, -at));
                 const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[1][r], factor, -at));
                 const float e2 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[0][r + 1], factor, -at));
@@ -857,14 +877,14 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     int j0 = first_tile(k_lo, kTileKeys, 0), buf = 0;
     if (j0 < k_hi) {
         stage.pages(a, j0);
-        stage.load(a, hk, j0);
+        stage.load(a, j0);
         stage.pages(a, j0 + kTileKeys);
         stage.put(lds, 0);
         __syncthreads();
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
         const int jn = j0 + kTileKeys;
-        stage.load(a, hk, jn);
+        stage.load(a, jn);
         stage.pages(a, jn + kTileKeys);
         __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {

@@ -136,8 +136,8 @@ int check_attention(const AttentionArgs &a, int64_t (*bytes)(int, int, int, int,
     if (rc) return rc;
     if (num_q_heads < 1 || num_q_heads % num_kv_heads)
         return fail(GDN_ERR_INVALID, "num_q_heads must be a positive multiple of num_kv_heads");
-    // offsets within a page of 8-bit codes are 32-bit where prompts are read
-    if (!four_bits && (int64_t)num_kv_heads * page_size * head_dim > 0x7fffffff)
+    // offsets within a page are 32-bit
+    if ((int64_t)num_kv_heads * page_size * head_dim > (four_bits ? 2LL : 1LL) * 0x7fffffff)
         return fail(GDN_ERR_UNSUPPORTED, "a page of %d heads x %d tokens x %d elements passes 2^31 - 1 bytes", num_kv_heads, page_size,
                     head_dim);
     if (max_pages < 1 || block_table_stride < max_pages)
