@@ -14,6 +14,11 @@
 // stands for them: every window of 64 tokens has its workgroups, whose waves take
 // the (granule, head) pairs that begin in it in turns.  That needs no list of
 // granules and no request boundaries, and no atomics.
+// Bound by q's way there and back for many tokens (16,384 of 32 + 8 heads of 128: 69
+// us, 354 MB; q and k alone 59, v alone 16.6, which waits for one thing after
+// another: its workgroups are spread among the others, 72 with all of them first), by
+// latency for few (32 tokens: 5.3 us).  q leaves by streaming stores (with ordinary
+// ones 7 us more).
 #include "fp4.h"
 #include "rope.h"
 
@@ -186,16 +191,18 @@ __device__ __forceinline__ void append_values(const RopeAppendArgs &a, uint8_t *
 }
 
 template <int D>
-__global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArgs a, int value_blocks, int ranks, int tokens) {
+__global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArgs a, int value_blocks, int per, int ranks, int tokens) {
     extern __shared__ CosSin cs[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long long slots = (long long)a.num_pages * a.page;
 
-    if ((int)blockIdx.x >= value_blocks) {
+    // a block of values, then per - 1 of rows; the rows that are left behind them
+    const unsigned block = blockIdx.x, turn = block / (unsigned)per;
+    if (turn >= (unsigned)value_blocks || block != turn * per) {
         // q and k of `tokens` tokens, a head per LPT lanes of eight elements
         constexpr int LPT = D / 8, TPI = 64 / LPT, UNROLL = 2, STEP = kWaves * TPI;
         const int half = a.rot / 2, heads = a.num_q_heads + a.num_kv_heads, shift = __builtin_ctz(a.page);
-        const long long t0 = (long long)(blockIdx.x - value_blocks) * tokens;
+        const long long t0 = (long long)(block - min(turn + 1, (unsigned)value_blocks)) * tokens;
         const int n = (int)min((long long)tokens, a.num_tokens - t0), rows = n * heads;
         const int e0 = (lane % LPT) * 8;
         const bool turns = e0 < a.rot;
@@ -226,7 +233,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
                 else unpack8(now[u].own, f);
                 if (h < a.num_q_heads) {
                     if (live && (turns || a.q != a.q_out))
-                        *reinterpret_cast<uint4 *>(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + e0) = pack8(f);
+                        store_stream16(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + e0, pack8(f));
                 } else {
                     const long long slot = a.slots[t0 + t];
                     const bool on = live && slot >= 0 && slot < slots;
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
 
     // the slots of the window's tokens and of as many behind them (a granule's run
     // may reach there), and which of them continue their predecessor's granule
-    const int first = (int)(blockIdx.x / (unsigned)ranks) * kWindow, rank = (int)(blockIdx.x % (unsigned)ranks);
+    const int first = (int)(turn / (unsigned)ranks) * kWindow, rank = (int)(turn % (unsigned)ranks);
     auto slot_at = [&](long long t) { return t >= 0 && t < a.num_tokens ? a.slots[t] : -2; };
     const long long mine = slot_at((long long)first + lane), behind = slot_at((long long)first + kWindow + lane);
     const bool on = mine == slot_at((long long)first + lane - 1) + 1 && (mine & (kGranule - 1)) != 0;
@@ -264,7 +271,9 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
 
 template <int D>
 static hipError_t launch_d(const RopeAppendArgs &a, hipStream_t stream) {
-    const int tokens = min(max(a.num_tokens / 512, 1), 8);
+    // two tokens per workgroup of rows where there are many (16,384 of 32 + 8 heads of 128: 72 us, 77
+    // with four, 79 with one)
+    const int tokens = a.num_tokens >= 1024 ? 2 : 1;
     const long long windows = ((long long)a.num_tokens + kWindow - 1) / kWindow;
     // a small call: a wave per (token, head), should each be a granule's first
     const int begin = a.num_tokens <= 512 ? min(a.num_tokens, kWindow) : 8;
@@ -274,7 +283,7 @@ static hipError_t launch_d(const RopeAppendArgs &a, hipStream_t stream) {
     // sines of the tokens, or the waves' codes of v
     const size_t lds = max((size_t)tokens * (a.rot / 2) * sizeof(CosSin), (size_t)kWaves * D * 8);
     hipLaunchKernelGGL((rope_append_kv4_kernel<D>), dim3((unsigned)(value_blocks + row_blocks)), dim3(kThreads), lds, stream, a,
-                       (int)value_blocks, ranks, tokens);
+                       (int)value_blocks, (int)(row_blocks / value_blocks) + 1, ranks, tokens);
     return hipGetLastError();
 }
 

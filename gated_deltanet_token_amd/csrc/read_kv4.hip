@@ -6,7 +6,10 @@
 // lanes per head, each with eight elements.  A key's eight codes are four bytes; the
 // eight elements' codes of a value lie in 64 bytes, for all 16 tokens.  A store is 16
 // bytes per lane, whole heads.
-// Bound by the stores, 32 bits for every 8.3 read.
+// Bound by the stores, 32 bits for every 8.3 read: streaming ones, that leave the
+// caches to what is still to be read (30,000 rows of 4 heads of 256: 27.7 us, 36.6
+// with ordinary ones; 131,071 of 8 of 128: 125 and 132, 5.4 TB/s of both directions).  Streaming
+// loads would lose the halves of a line that another load takes (33 and 134 us).
 #include "attention_split.h"
 #include "fp4.h"
 
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(kReadThreads) void paged_read_kv4_kernel(PagedReadA
             unpack8(v, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] *= scale;
-            if (t >= t0 && t < t1) *reinterpret_cast<uint4 *>(out + t * a.k_out_stride) = pack8(f);
+            if (t >= t0 && t < t1) store_stream16(out + t * a.k_out_stride, pack8(f));
         }
     } else {
         const uint4 *p = reinterpret_cast<const uint4 *>(a.v_cache + at * (D / 2) + e0 * 8);
@@ -95,7 +98,7 @@ __global__ __launch_bounds__(kReadThreads) void paged_read_kv4_kernel(PagedReadA
         uint16_t *out = a.v_out + row0 * a.v_out_stride + (long long)head * D + e0;
 #pragma unroll
         for (int t = 0; t < kGranule; ++t)
-            if (t >= t0 && t < t1) *reinterpret_cast<uint4 *>(out + t * a.v_out_stride) = value_row(w, t, scale[t]);
+            if (t >= t0 && t < t1) store_stream16(out + t * a.v_out_stride, value_row(w, t, scale[t]));
     }
 }
 
