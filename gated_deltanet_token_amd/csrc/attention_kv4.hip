@@ -1000,7 +1000,7 @@ int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_he
 
 template <int D>
 static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
-    const Plan p = plan_of(rules(D), a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len);
+    const Plan p = plan_of(rules(D), a.num_tokens, a.num_seqs, a.num_q_heads, a.num_kv_heads, D, a.max_seq_len, a.window);
     const long long few = p.few.units * p.few.splits, many = p.many.units * p.many.splits;
     if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;

@@ -235,7 +235,8 @@ struct Plan {
     Launch few, many;
 };
 
-Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len);
+// window: 0, or the keys that a row sees at most (a plan needs no more workspace for it)
+Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len, int window = 0);
 
 // the partial results of a launch at `ws`
 inline Division division(const Launch &p, bool by_rows, int d, float *ws) {

@@ -85,14 +85,16 @@ static Launch divide(long long tiles, long long busy, long long rows, int kv_hea
     return p;
 }
 
-Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len) {
+Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len, int window) {
     const long long G = q_heads / kv_heads;
+    // few rows that see no more than one part's keys are not split, wherever these lie
+    const int few_len = window > 0 && window <= rules.min_chunk ? window : max_seq_len;
     Plan p{};
     if (T <= S) {
         p.few_takes = Take::kAll;
         const long long full = T * G / kTileRows;
         const long long busy = full > T ? full : T;
-        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, max_seq_len, kCUs,
+        p.few = divide(full + S, busy, T * q_heads, kv_heads, d, few_len, kCUs,
                        busy * kv_heads * 4 <= kCUs ? rules.idle_chunk : rules.min_chunk);
     } else {
         p.few_takes = Take::kSmall;
@@ -101,7 +103,7 @@ Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int
         // workgroups take anyway: at least this many keys one after the other, where
         // a small request's waves share theirs
         const long long anyway = busy * kv_heads * (T / S) / 2 / room * rules.waves;
-        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, max_seq_len, kCUs,
+        p.few = divide(S * (kSmallRows / kTileRows), S, S * kSmallRows * kv_heads, kv_heads, d, few_len, kCUs,
                        anyway > rules.min_chunk ? anyway : rules.min_chunk);
         // the fewer tile numbers of two ways that are enough (a request of many rows has
         // more than kSmallRows): 29 decode rows and 16 tokens take 23 us with 3 per kv
