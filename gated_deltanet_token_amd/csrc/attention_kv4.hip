@@ -16,6 +16,8 @@
 // one keeps its 8 bits.  Codes are finite whatever they are; a key that a row
 // does not see gets a weight of zero there, and so no influence.
 // Scores and sums are fp32; the maximum is in units of log2.
+#include <cstddef>
+
 #include "attention_split.h"
 #include "fp4.h"
 
@@ -574,11 +576,17 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: one workgroup per (128 rows of one request that share a kv head,
-// split of its keys).  Bound by the matrix cores, the exponentials and the
-// values' conversion: tiles of 64 keys and values pass through the LDS once for
-// all waves, the next one on its way from HBM to registers meanwhile, with one
-// barrier per tile between two buffers.
+// Many rows: one workgroup of four waves per (128 rows of one request that share a kv
+// head, 64 at D = 256, split of its keys).  Tiles of 64 keys and values pass through
+// the LDS once for all waves, the next one on its way from HBM to registers
+// meanwhile, with one barrier per tile between two buffers.
+// Bound by vector arithmetic and what two or three waves per SIMD leave uncovered: of a
+// prompt of 8,192 tokens (32/8 heads of 128: 515 us, 1,070 TFLOP/s; of 64: 326; 16/4 of
+// 256: 525) the vector unit is busy for 73% of the time, the matrix cores for 43%.  What did
+// not help there: the values turned to bf16 once, on their way to the LDS (fewer
+// conversions, as much more waiting for the LDS: 534 us, 531 then without); q's parts in
+// the LDS for a third wave (666: registers spill, 341 of 336 at D = 64); a tile's scores
+// taken with the weights of the tile before (655 and 374: registers).
 //
 // Keys lie in the LDS as rows of 16-byte pieces (32 elements), values as in
 // memory, granule by granule.  The 16 lanes that a 16-byte read serves together are
@@ -586,75 +594,90 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the pieces that they read into 16 different places of the 256 bytes that the
 // banks span.  A read of values is of 512 bytes in a row.
 // ---------------------------------------------------------------------------
+constexpr int kManyThreads = 256;
+
 template <int D>
 struct ManyLds {
-    uint4 k[2][kTileKeys * D / 32], v[2][kTileKeys * D / 32];
-    uint32_t ks[2][kTileKeys * D / 128];   // [block of 32 elements][key], a byte each
-    float vs[2][kTileKeys];
-    int ok[2][4];                          // whether the tile's four granules have a page
+    uint4 k[kTileKeys * D / 32], v[kTileKeys * D / 32];
+    uint2 ks[kTileKeys * D / 128];         // [block of 32 elements][four keys]: their scales; the granule's page, or below 0
+    f32x2 vs[kTileKeys / 2];
+    uint2 none[2];                         // what no one reads
 };
 
 // Staging: D / 2 pieces of 16 bytes of a granule's keys, and as many of its values.  A
-// thread has one of each (at D = 64 one of either), of one page: the first ones also
-// four keys' scales or two values' of the same granule.  As in take_keys, loads are
+// thread has N of each (at D = 64 one of either), each of one granule: the first ones
+// also four keys' scales or two values' of the same granule.  As in take_keys, loads are
 // without conditions, tiles past the last one come from the first page.
-template <int D, int THREADS, int (*PLACE)(int, int)>
+template <int D, int (*PLACE)(int, int)>
 struct Staging {
+    static constexpr int THREADS = kManyThreads;
     static constexpr int PER = D / 2, PPK = D / 32;
-    static constexpr bool BOTH = 4 * PER == THREADS;
-    static_assert(BOTH || 8 * PER == THREADS, "");
+    static constexpr int N = 4 * PER / THREADS > 1 ? 4 * PER / THREADS : 1;
+    static constexpr bool BOTH = 4 * PER >= THREADS;
+    static_assert((BOTH ? 4 * PER == N * THREADS : 8 * PER == THREADS) && THREADS % PER == 0, "");
+    static constexpr int kNext = THREADS / PER;          // a thread's pieces are of every kNext-th granule
     const int32_t *bt;
     int granule, i;
     bool keys, values;
     unsigned end;
-    // of a page: bytes of codes, of all kv heads; where the thread's piece and its scales
+    // of a page: bytes of codes, of all kv heads; where the thread's pieces and their scales
     // are (a tile begins at a multiple of 64 keys: the same in every one)
-    uint32_t pitch, at, sc_at, sc_shift;
+    uint32_t pitch, at[N], sc_at[N], sc_shift, put_at[N];
     const uint8_t *sc_base;
-    u32x4 kr, vr;                // what is on its way
-    uint32_t sc;
-    int entry, own;              // the block table's entry for the tile behind it, as it came; its page
+    u32x4 kr[N], vr[N];          // what is on its way
+    uint32_t sc[N];
+    int entry[N], own[N];        // the block table's entries for the tile behind it, as they came; its pages
 
     __device__ __forceinline__ Staging(const AttentionArgs &a, const ManyShare &w)
         : bt(a.block_table + w.s * a.block_table_stride), granule((threadIdx.x % (4 * PER)) / PER), i(threadIdx.x % PER),
           keys(BOTH || threadIdx.x < 4 * PER), values(BOTH || threadIdx.x >= 4 * PER), end(max(w.k_hi, 0)),
           pitch((uint32_t)(a.num_kv_heads * a.page) * PER) {
-        const uint32_t in_page = 16 * granule & (a.page - 1), row = w.hk * a.page + in_page;
-        at = row * PER + 16 * i;
         // key scales are a 16th of the codes, value scales 2 of a token's D / 2 bytes
         const bool of_keys = i < D / 8;
         sc_base = of_keys ? k_scales(a) : reinterpret_cast<const uint8_t *>(v_scales(a));
         sc_shift = of_keys ? 4 : __builtin_ctz(PER / 2);
-        sc_at = of_keys ? (w.hk * PPK + i / 4) * a.page + in_page + 4 * (i % 4) : 2 * row + 4 * (i % 8);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint32_t in_page = 16 * (granule + n * kNext) & (a.page - 1), row = w.hk * a.page + in_page;
+            at[n] = row * PER + 16 * i;
+            sc_at[n] = of_keys ? (w.hk * PPK + i / 4) * a.page + in_page + 4 * (i % 4) : 2 * row + 4 * (i % 8);
+            const int gr = granule + n * kNext;
+            put_at[n] = keys && of_keys           ? offsetof(ManyLds<D>, ks) + 8 * ((i / 4) * 16 + gr * 4 + i % 4)
+                        : keys && i < D / 8 + 8 ? offsetof(ManyLds<D>, vs) + 8 * (8 * gr + i - D / 8)
+                                                  : offsetof(ManyLds<D>, none);
+        }
     }
     __device__ __forceinline__ void pages(const AttentionArgs &a, unsigned j0) {
-        entry = bt[min((j0 + 16 * granule) >> __builtin_ctz(a.page), (unsigned)a.max_pages - 1)];
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            entry[n] = bt[min((j0 + 16 * (granule + n * kNext)) >> __builtin_ctz(a.page), (unsigned)a.max_pages - 1)];
     }
     __device__ __forceinline__ void load(const AttentionArgs &a, unsigned j0) {
-        const unsigned j = j0 + 16 * granule;
-        own = j < end && (unsigned)entry < (unsigned)a.num_pages ? entry : -1;
-        const uint64_t page = (uint64_t)(uint32_t)max(own, 0) * pitch;
-        if constexpr (BOTH) {
-            kr = *reinterpret_cast<const u32x4 *>(a.k_cache + (page + at));
-            vr = *reinterpret_cast<const u32x4 *>(a.v_cache + (page + at));
-        } else {
-            kr = vr = *reinterpret_cast<const u32x4 *>((keys ? a.k_cache : a.v_cache) + (page + at));
-        }
-        sc = *reinterpret_cast<const uint32_t *>(sc_base + ((page >> sc_shift) + sc_at));
-    }
-    __device__ __forceinline__ void put(ManyLds<D> &lds, int buf) const {
-        if (keys) {
-            *reinterpret_cast<u32x4 *>(&lds.k[buf][PLACE(16 * granule + i / PPK, i % PPK)]) = kr;
-            if (i < D / 8) {
-                lds.ks[buf][(i / 4) * 16 + granule * 4 + i % 4] = sc;
-            } else if (i < D / 8 + 8) {
-                const int at = 16 * granule + 2 * (i - D / 8);
-                lds.vs[buf][at] = bf16_lo(sc);
-                lds.vs[buf][at + 1] = bf16_hi(sc);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const unsigned j = j0 + 16 * (granule + n * kNext);
+            own[n] = j < end && (unsigned)entry[n] < (unsigned)a.num_pages ? entry[n] : -1;
+            const uint64_t page = (uint64_t)(uint32_t)max(own[n], 0) * pitch;
+            if constexpr (BOTH) {
+                kr[n] = *reinterpret_cast<const u32x4 *>(a.k_cache + (page + at[n]));
+                vr[n] = *reinterpret_cast<const u32x4 *>(a.v_cache + (page + at[n]));
+            } else {
+                kr[n] = vr[n] = *reinterpret_cast<const u32x4 *>((keys ? a.k_cache : a.v_cache) + (page + at[n]));
             }
-            if (i == 0) lds.ok[buf][granule] = own >= 0;
+            sc[n] = *reinterpret_cast<const uint32_t *>(sc_base + ((page >> sc_shift) + sc_at[n]));
         }
-        if (values) *reinterpret_cast<u32x4 *>(&lds.v[buf][granule * PER + i]) = vr;
+    }
+    __device__ __forceinline__ void put(ManyLds<D> &lds) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int gr = granule + n * kNext;
+            if (keys) *reinterpret_cast<u32x4 *>(&lds.k[PLACE(16 * gr + i / PPK, i % PPK)]) = kr[n];
+            if (values) *reinterpret_cast<u32x4 *>(&lds.v[gr * PER + i]) = vr[n];
+            // one store for whatever the thread's scales are, without branches
+            const bool of_keys = i < D / 8;
+            *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(&lds) + put_at[n]) =
+                make_uint2(of_keys ? sc[n] : sc[n] << 16, of_keys ? (uint32_t)own[n] : sc[n] & 0xffff0000u);
+        }
     }
 };
 
@@ -667,8 +690,6 @@ struct Staging {
 // operands' scales are neighbouring bytes.  Row i of the V operands 2 u and 2 u + 1
 // is element 64 u + 2 i and the one behind it.
 // ---------------------------------------------------------------------------
-constexpr int kWideThreads = 256;
-
 // 32 lanes read the same piece of keys 32 (c / 4 % 2) + 8 (c / 8) + 2 (c % 4) + b
 template <int D>
 __device__ __forceinline__ int k_place(int key, int p) {
@@ -680,7 +701,7 @@ __device__ __forceinline__ int k_place(int key, int p) {
 }
 
 template <int D>
-__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
+__device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> (&lds)[2]) {
     constexpr int KS = D / 64;                       // contraction steps of 64
     constexpr int DT = D / 32;                       // operands of 32 value elements
 
@@ -716,7 +737,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
     }
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
 
-    Staging<D, kWideThreads, k_place<D>> stage(a, w);
+    Staging<D, k_place<D>> stage(a, w);
     const int key = 32 * (c >> 2 & 1) + 8 * (c >> 3) + 2 * (c & 3);
     const int k_row = k_place<D>(key, 0) & ~(D / 32 - 1), k_swap = k_place<D>(key, h2) - k_row;
     f32x16 o[DT] = {};
@@ -726,7 +747,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
         stage.pages(a, j0);
         stage.load(a, j0);
         stage.pages(a, j0 + kTileKeys);
-        stage.put(lds, 0);
+        stage.put(lds[0]);
         __syncthreads();
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
@@ -735,14 +756,15 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
         stage.pages(a, jn + kTileKeys);
         __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {
-            const bool ok0 = lds.ok[buf][2 * h2] != 0, ok1 = lds.ok[buf][2 * h2 + 1] != 0;
+            const ManyLds<D> &t = lds[buf];
+            const bool ok0 = (int)t.ks[8 * h2].y >= 0, ok1 = (int)t.ks[8 * h2 + 4].y >= 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!(ok0 && ok1)), late = j0 - k_lo >= kLateKeys;
-            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + h2 * D + c;
-            const uint8_t *kst = reinterpret_cast<const uint8_t *>(lds.ks[buf]) + key + 64 * h2;
+            const uint4 *kt = t.k + k_row, *vt = t.v + h2 * D + c;
+            const uint8_t *kst = reinterpret_cast<const uint8_t *>(t.ks) + 2 * (key & ~3) + (key & 3) + 128 * h2;
             f32x16 x[2] = {};
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                const int sc = *reinterpret_cast<const uint16_t *>(kst + 128 * st);
+                const int sc = *reinterpret_cast<const uint16_t *>(kst + 256 * st);
                 const uint4 k0 = kt[k_swap ^ 2 * st], k1 = kt[32 * (D / 32) + (k_swap ^ 2 * st)];
                 // (the products' operand selections are constants)
                 x[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k0), operand(q[st].part[0]), x[0], kE2m1, kE2m3, 0, sc, 0, q[st].scale);
@@ -775,7 +797,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             const float at = m == kNegInf ? 0.f : m;
             f32x4 vs[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vs[i] = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 32 * h2)[i];
+            for (int i = 0; i < 8; ++i) vs[i] = reinterpret_cast<const f32x4 *>(t.vs + 16 * h2)[i];
             if (masked)
 #pragma unroll
                 for (int r = 0; r < 32; ++r) vs[r / 4][r & 3] = x[r & 1][r / 2] == kNegInf ? 0.f : vs[r / 4][r & 3];
@@ -806,7 +828,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        stage.put(lds, buf ^ 1);
+        stage.put(lds[buf ^ 1]);
         __syncthreads();
     }
 
@@ -831,11 +853,12 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 }
 
 // ---------------------------------------------------------------------------
-// 16 rows per wave, eight waves, for D = 256: 32 rows' sums and q parts leave room
-// for one wave per SIMD only.  Lanes as in the few-rows kernel, operands from the
-// LDS.
+// 16 rows per wave, for D = 256: 32 rows' sums and q parts leave room for one wave per
+// SIMD only (with the parts in the LDS registers spill: a prompt of 8,192, 16/4 heads, takes
+// 687 us, 525 so).  Four waves: two workgroups on a CU do not wait for each other (eight
+// waves of 128 rows: 555).  Lanes as in the few-rows kernel, operands from the LDS.
 // ---------------------------------------------------------------------------
-constexpr int kNarrowThreads = 512;
+constexpr int kNarrowRows = 64;
 
 // 16 lanes read the same piece of keys 16 (c / 4) + 4 (c % 4) + t
 template <int D>
@@ -847,14 +870,14 @@ __device__ __forceinline__ int k_place_narrow(int key, int p) {
 }
 
 template <int D>
-__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> &lds) {
+__device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const Division &v, int block, int blocks, ManyLds<D> (&lds)[2]) {
     constexpr int KS = D / 128, DT = D / 16;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int G = a.num_q_heads / a.num_kv_heads;
     ManyShare w;
-    if (!many_share(a, v, block, blocks, w)) return;
+    if (!many_share<kNarrowRows>(a, v, block, blocks, w)) return;
     const Request &rq = w.rq;
     const int hk = w.hk, k_lo = w.k_lo, k_hi = w.k_hi;
     const int wrow = w.row0 + 16 * wave, row = wrow + c;
@@ -869,7 +892,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     q.split(Q16<D>::load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), g, a.scale < 0.f ? 0x80008000u : 0u);
     const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
 
-    Staging<D, kNarrowThreads, k_place_narrow<D>> stage(a, w);
+    Staging<D, k_place_narrow<D>> stage(a, w);
     const int key = 16 * (c >> 2) + 4 * (c & 3);
     const int k_row = k_place_narrow<D>(key, 0) & ~7, k_swap = k_place_narrow<D>(key, g) & 7;
     f32x4 o[DT] = {};
@@ -879,7 +902,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
         stage.pages(a, j0);
         stage.load(a, j0);
         stage.pages(a, j0 + kTileKeys);
-        stage.put(lds, 0);
+        stage.put(lds[0]);
         __syncthreads();
     }
     for (; j0 < k_hi; j0 += kTileKeys, buf ^= 1) {
@@ -888,13 +911,14 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
         stage.pages(a, jn + kTileKeys);
         __builtin_amdgcn_sched_barrier(0);
         if (j0 < wk.hi && jn > wk.lo) {
-            const bool ok = lds.ok[buf][g] != 0;
+            const ManyLds<D> &tile = lds[buf];
+            const bool ok = (int)tile.ks[4 * g].y >= 0;
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
-            const uint4 *kt = lds.k[buf] + k_row, *vt = lds.v[buf] + g * (D / 2) + c;
+            const uint4 *kt = tile.k + k_row, *vt = tile.v + g * (D / 2) + c;
             f32x4 x[4] = {};
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                const uint32_t ks = lds.ks[buf][16 * (4 * st + g) + key / 4];
+                const uint32_t ks = tile.ks[16 * (4 * st + g) + key / 4].x;
                 const int at = k_swap ^ 4 * st;
                 score16<0>(x[0], kt[at], ks, q, st);            // (key t is row 2 t of these eight)
                 score16<1>(x[1], kt[2 * 8 + at], ks, q, st);
@@ -902,7 +926,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 score16<3>(x[3], kt[6 * 8 + at], ks, q, st);
             }
             float vs[16];
-            const f32x4 *vst = reinterpret_cast<const f32x4 *>(lds.vs[buf] + 16 * g);
+            const f32x4 *vst = reinterpret_cast<const f32x4 *>(tile.vs + 8 * g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 s = vst[i];
@@ -924,7 +948,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        stage.put(lds, buf ^ 1);
+        stage.put(lds[buf ^ 1]);
         __syncthreads();
     }
 
@@ -943,10 +967,9 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 }
 
 // ---------------------------------------------------------------------------
-// The kernels: a token per request at most on average (few rows alone, eight
-// waves), and else both kinds of requests in one grid -- the large ones'
-// workgroups first, those of the small ones (decode rows) take the CUs that
-// are left and each that becomes free.
+// The kernels: a token per request at most on average (few rows alone), and else
+// both kinds of requests in one grid -- the large ones' workgroups first, those of
+// the small ones (decode rows) take the CUs that are left and each that becomes free.
 // ---------------------------------------------------------------------------
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attention_few_kv4_kernel(AttentionArgs a, Division v, bool ordered) {
@@ -957,15 +980,15 @@ __global__ __launch_bounds__(64 * W, 2) void attention_few_kv4_kernel(AttentionA
     few_rows<D, W, Take::kAll>(a, v, blockIdx.x, lds.few, ordered ? &lds.order : nullptr);
 }
 
-constexpr int mixed_threads(int d) { return d == 256 ? kNarrowThreads : kWideThreads; }
+constexpr int many_rows(int d) { return d == 256 ? kNarrowRows : kManyRows; }
 
 template <int D>
-__global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kv4_kernel(AttentionArgs a, Division few, Division many,
-                                                                                  int many_blocks) {
-    constexpr int W = mixed_threads(D) / 64;
+__global__ __launch_bounds__(kManyThreads, 2) void attention_mixed_kv4_kernel(AttentionArgs a, Division few, Division many,
+                                                                              int many_blocks) {
+    constexpr int W = kManyThreads / 64;
     __shared__ union {
         FewLds<D, W> few;
-        ManyLds<D> many;
+        ManyLds<D> many[2];
     } lds;
     const int block = blockIdx.x;
     if (block >= many_blocks) few_rows<D, W, Take::kSmall>(a, few, block - many_blocks, lds.few);
@@ -978,7 +1001,7 @@ __global__ __launch_bounds__(mixed_threads(D), 2) void attention_mixed_kv4_kerne
 // request of 4,000 keys, 16/4 heads of 256: 14.5 us, 10 and 5 to join the parts).
 constexpr int kMinChunk = 1024, kIdleChunk = 512, kManyChunk = 256;
 static SplitRules rules(int d) {
-    return {kMinChunk, kIdleChunk, kManyChunk, mixed_threads(d) / 64, d == 256 ? kCUs : 2 * kCUs};
+    return {kMinChunk, kIdleChunk, kManyChunk, kManyThreads / 64, 2 * kCUs, many_rows(d)};
 }
 
 // Workgroups of four waves: two of them on a CU, one of which streams while the other begins or
@@ -1016,10 +1039,10 @@ static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
         return hipGetLastError();
     }
     const Division vm = division(p.many, p.by_rows, D, a.workspace + p.few.floats);
-    hipLaunchKernelGGL((attention_mixed_kv4_kernel<D>), dim3((unsigned)(few + many)), dim3(mixed_threads(D)), 0, stream, a, vf, vm,
+    hipLaunchKernelGGL((attention_mixed_kv4_kernel<D>), dim3((unsigned)(few + many)), dim3(kManyThreads), 0, stream, a, vf, vm,
                        (int)many);
     launch_join(Take::kSmall, a, p.few, vf, kTileRows, stream);
-    launch_join(Take::kLarge, a, p.many, vm, kManyRows, stream);
+    launch_join(Take::kLarge, a, p.many, vm, many_rows(D), stream);
     return hipGetLastError();
 }
 

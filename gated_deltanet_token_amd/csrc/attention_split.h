@@ -166,6 +166,7 @@ struct ManyShare {
 };
 // The last tiles see the most keys and go first; a kv head's workgroups are
 // num_kv_heads apart, so that with eight heads an XCD keeps to one.
+template <int ROWS = kManyRows>
 __device__ __forceinline__ bool many_share(const AttentionArgs &a, const Division &v, int block, int blocks, ManyShare &w) {
     const int G = a.num_q_heads / a.num_kv_heads;
     const unsigned units = (unsigned)blocks / (unsigned)v.splits, unit = (unsigned)block / (unsigned)v.splits, hks = a.num_kv_heads;
@@ -173,14 +174,14 @@ __device__ __forceinline__ bool many_share(const AttentionArgs &a, const Divisio
     const int tile = (int)(units / hks - 1 - unit / hks);
     w.hk = (int)(unit % hks);
     int within;
-    w.s = v.by_rows ? find_request(a, tile, G, kSmallRows, 0, true, within) : find_request(a, tile, G, kManyRows, 1, false, within);
+    w.s = v.by_rows ? find_request(a, tile, G, kSmallRows, 0, true, within) : find_request(a, tile, G, ROWS, 1, false, within);
     w.rq = request_of(a, w.s);
     w.n_rows = w.rq.n * G;
-    if (within < 0 || (long long)within * kManyRows >= w.n_rows || w.n_rows <= kSmallRows) return false;
-    w.row0 = within * kManyRows;
+    if (within < 0 || (long long)within * ROWS >= w.n_rows || w.n_rows <= kSmallRows) return false;
+    w.row0 = within * ROWS;
     int lo, hi, x;
     key_range(a, w.rq, token_of(w.row0, G), lo, x);
-    key_range(a, w.rq, token_of(last_row(w.row0, kManyRows, w.n_rows), G), x, hi);
+    key_range(a, w.rq, token_of(last_row(w.row0, ROWS, w.n_rows), G), x, hi);
     const Splits sp = splits_of(lo, hi, v.chunk, v.splits);
     if (w.split != sp.first && (w.split < sp.first || w.split > sp.last)) return false;
     w.whole = sp.last <= sp.first;
@@ -219,7 +220,7 @@ constexpr int kCUs = 256;
 // workgroups of it that all CUs hold at once.
 struct SplitRules {
     int min_chunk, idle_chunk, many_chunk;
-    int waves, room;
+    int waves, room, many_rows = kManyRows;
 };
 
 struct Launch {

@@ -98,7 +98,7 @@ Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int
                        busy * kv_heads * 4 <= kCUs ? rules.idle_chunk : rules.min_chunk);
     } else {
         p.few_takes = Take::kSmall;
-        const long long full = T * G / kManyRows, busy = full > 1 ? full : 1, room = rules.room;
+        const long long full = T * G / rules.many_rows, busy = full > 1 ? full : 1, room = rules.room;
         // the small requests' parts need not be shorter than what the other
         // workgroups take anyway: at least this many keys one after the other, where
         // a small request's waves share theirs
