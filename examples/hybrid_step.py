@@ -1,12 +1,13 @@
 """An engine step of a small hybrid stack: Gated DeltaNet layers and one
 full-attention layer, decode rows and prompt chunks in one batch.
 
-    python examples/hybrid_step.py
+    python examples/hybrid_step.py [8 | 4]
 
 The step's lengths, free list, block table and positions live on the GPU and
 gdn_build_step_tables works on them there, so that a decode step is one HIP
-graph that is replayed as it is: no length comes back to the host.  Weights are
-random, and hidden states stand for the embedding and the feed-forward blocks.
+graph that is replayed as it is: no length comes back to the host.  The attention's
+paged cache holds 8 bits a number, or 4.  Weights are random, and hidden states
+stand for the embedding and the feed-forward blocks.
 """
 import os
 import sys
@@ -27,13 +28,15 @@ BF16 = torch.bfloat16
 
 
 class HybridStack:
-    def __init__(self, num_requests, max_len, seed=0, device="cuda"):
+    def __init__(self, num_requests, max_len, seed=0, device="cuda", cache_bits=8):
         gen = torch.Generator(device).manual_seed(seed)
 
         def normal(*shape, std=1.0, dtype=BF16):
             return (std * torch.randn(*shape, generator=gen, device=device)).to(dtype)
 
         self.max_len, S = max_len, num_requests
+        self.append, self.attend = {8: (gdn.gdn_rope_append_kv8, gdn.gdn_paged_attention_kv8),
+                                    4: (gdn.gdn_rope_append_kv4, gdn.gdn_paged_attention_kv4)}[cache_bits]
         columns = -(-max_len // PAGE)
         pages = S * columns
         i32 = dict(dtype=torch.int32, device=device)
@@ -61,10 +64,16 @@ class HybridStack:
                 p["w_out"] = normal(AQ * AD, HIDDEN, std=(AQ * AD) ** -0.5)
                 p["q_norm"], p["k_norm"] = normal(AD, std=0.1), normal(AD, std=0.1)
                 code = dict(dtype=torch.uint8, device=device)
-                p["k_cache"] = torch.zeros(pages, AK, PAGE, AD, **code).view(torch.float8_e4m3fn)
-                p["v_cache"] = torch.zeros(pages, AK, AD, PAGE, **code).view(torch.float8_e4m3fn)
-                p["k_scale"] = torch.zeros(pages, AK, device=device)
-                p["v_scale"] = torch.zeros(pages, AK, device=device)
+                if cache_bits == 8:
+                    p["k_cache"] = torch.zeros(pages, AK, PAGE, AD, **code).view(torch.float8_e4m3fn)
+                    p["v_cache"] = torch.zeros(pages, AK, AD, PAGE, **code).view(torch.float8_e4m3fn)
+                    p["k_scale"] = torch.zeros(pages, AK, device=device)
+                    p["v_scale"] = torch.zeros(pages, AK, device=device)
+                else:
+                    p["k_cache"] = torch.zeros(pages, AK, PAGE, AD // 2, **code)
+                    p["v_cache"] = torch.zeros(pages, AK, PAGE // 16, AD, 8, **code)
+                    p["k_scale"] = torch.zeros(pages, AK, AD // 32, PAGE, **code)
+                    p["v_scale"] = torch.zeros(pages, AK, PAGE, dtype=BF16, device=device)
             self.layers.append(p)
 
     def delta(self, p, h, t, decode):
@@ -94,11 +103,9 @@ class HybridStack:
         gdn.gdn_gated_rms_norm(q, p["q_norm"], q, eps=EPS, weight_offset=1.0)
         gdn.gdn_gated_rms_norm(k, p["k_norm"], k, eps=EPS, weight_offset=1.0)
         cache = (p["k_cache"], p["v_cache"], p["k_scale"], p["v_scale"])
-        gdn.gdn_rope_append_kv8(q, k, v, t["positions"], t["slot_mapping"], self.frequencies, q, *cache,
-                                rope_scale=self.rope_scale)
+        self.append(q, k, v, t["positions"], t["slot_mapping"], self.frequencies, q, *cache, rope_scale=self.rope_scale)
         o = torch.empty(T, AQ, AD, dtype=BF16, device=h.device)
-        gdn.gdn_paged_attention_kv8(q, *cache, self.block_table, t["seq_lens"], t["query_start_loc"], o, max_seq_len,
-                                    AD ** -0.5)
+        self.attend(q, *cache, self.block_table, t["seq_lens"], t["query_start_loc"], o, max_seq_len, AD ** -0.5)
         return (o * torch.sigmoid(gate)).view(T, AQ * AD) @ p["w_out"]
 
     def step(self, x, query_lens, max_seq_len, decode=False):
@@ -126,9 +133,9 @@ class HybridStack:
         return h, t
 
 
-def main():
+def main(cache_bits=8):
     lens, new = [300, 1, 517, 64], 32
-    stack = HybridStack(len(lens), max_len=1024)
+    stack = HybridStack(len(lens), max_len=1024, cache_bits=cache_bits)
     gen = torch.Generator("cuda").manual_seed(1)
     x = torch.randn(sum(lens), HIDDEN, generator=gen, device="cuda").to(BF16)
     h, t = stack.step(x, torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens))
@@ -159,4 +166,4 @@ def main():
 
 
 if __name__ == "__main__":
-    main()
+    main(int(sys.argv[1]) if len(sys.argv) > 1 else 8)

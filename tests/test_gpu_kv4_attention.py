@@ -121,6 +121,22 @@ def test_prompts(d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [17, 31, 32, 33, 48, 63, 64, 65, 96, 127, 129])
+def test_rows_about_a_tile(d, new):
+    """Two rows per token and kv head: 33 rows and more are a large request's, of whole and
+    of broken tiles."""
+    Case(new, [(new + 70, new), (5, 1), (new, new)], 4, 2, d, 16).check()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("window", [100, 1024, 1025])
+def test_windows_over_long_requests(d, window):
+    """A window of one part's keys or fewer, wherever it lies: few rows are not split."""
+    Case(31, [(9000, 1), (4097, 1), (1500, 1), (3, 1)], 4, 1, d, 16).check(window=window)
+    Case(32, [(9000, 1), (4097, 3), (5000, 90), (3, 1)], 4, 1, d, 16).check(window=window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_long_decode_in_parts(d):
     """Few rows over long contexts: the work is split along the keys and joined."""
     c = Case(4, [(9000, 1), (4097, 1), (3, 1)], 4, 1, d, 32, spread=4.0)
