@@ -3,7 +3,7 @@
 //
 // Rotation: (a, b) -> m (a cos t - b sin t, b cos t + a sin t), t = position *
 // frequency.  Angles, and their sines and cosines, are formed in 64 bits, once per
-// token and pair in the LDS for all heads of q and k; products are in fp32.
+// token and pair in the LDS for all heads of q and k; k's products are in 64 bits too.
 //
 // Keys: a scale belongs to 32 elements of one token, four lanes' eights.  Tokens
 // are independent of each other.
@@ -14,11 +14,11 @@
 // stands for them: every window of 64 tokens has its workgroups, whose waves take
 // the (granule, head) pairs that begin in it in turns.  That needs no list of
 // granules and no request boundaries, and no atomics.
-// Bound by q's way there and back for many tokens (16,384 of 32 + 8 heads of 128: 69
-// us, 354 MB; q and k alone 59, v alone 16.6, which waits for one thing after
-// another: its workgroups are spread among the others, 72 with all of them first), by
-// latency for few (32 tokens: 5.3 us).  q leaves by streaming stores (with ordinary
-// ones 7 us more).
+// Bound by q's way there and back for many tokens (16,384 of 32 + 8 heads of 128: 73
+// us, 354 MB; v alone 16.6, which waits for one thing after another: its workgroups
+// are spread among the others, 3 us more with all of them first), by latency for few (32
+// tokens: 5.3 us).  q leaves by streaming stores (with ordinary ones 7 us more).  A row
+// at a time per group of lanes: with two, fewer waves fit (4 us more).
 #include "fp4.h"
 #include "rope.h"
 
@@ -29,13 +29,25 @@ constexpr int kWindow = 64;             // tokens
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
+__device__ __forceinline__ float fma_of(float a, float b, float c) { return __builtin_fmaf(a, b, c); }
+__device__ __forceinline__ double fma_of(double a, double b, double c) { return __builtin_fma(a, b, c); }
+
 // a pair's cosine and sine, times the rope scale
+template <class T>
 struct CosSin {
-    float c, s;
+    T c, s;
 };
 
-// those of tokens [t0, t0 + n), n <= 16, into cs[n][half]
-__device__ __forceinline__ void fill_cos_sin(const RopeAppendArgs &a, CosSin *cs, long long t0, int n) {
+// those of `tokens` tokens, token by token, for k in 64 bits and for q
+struct Turns {
+    CosSin<double> *k;
+    CosSin<float> *q;
+    __device__ Turns(void *lds, int pairs) : k(static_cast<CosSin<double> *>(lds)), q(reinterpret_cast<CosSin<float> *>(k + pairs)) {}
+};
+constexpr size_t kTurnBytes = sizeof(CosSin<double>) + sizeof(CosSin<float>);
+
+// those of tokens [t0, t0 + n), n <= 16
+__device__ __forceinline__ void fill_cos_sin(const RopeAppendArgs &a, const Turns &turns, long long t0, int n) {
     const int half = a.rot / 2, across = half > 32 ? 64 : 32;       // lanes per token
     if (half == 0) return;
     // one load brings every token's position; the loop's lanes take theirs from there
@@ -46,21 +58,28 @@ __device__ __forceinline__ void fill_cos_sin(const RopeAppendArgs &a, CosSin *cs
         for (int t = threadIdx.x / across; t < n; t += kThreads / across) {
             double s, c;
             sin_cos_turns((double)__shfl(pos, t, 64) * f * 0.15915494309189533577, s, c);
-            if (p < half) cs[t * half + pair_at(a, p)] = {(float)(a.rope_scale * c), (float)(a.rope_scale * s)};
+            c *= a.rope_scale, s *= a.rope_scale;
+            if (p < half) {
+                turns.k[t * half + pair_at(a, p)] = {c, s};
+                turns.q[t * half + pair_at(a, p)] = {(float)c, (float)s};
+            }
         }
     }
 }
 
-// eight elements (e0 < rot), rotated; `cs` of their token
-__device__ __forceinline__ void rotated(const RopeAppendArgs &a, const Raw &r, int e0, const CosSin *cs, float (&f)[8]) {
+// eight elements (e0 < rot), rotated; `cs` of their token.  q's products are in fp32,
+// as it is rounded to bf16; k's in 64 bits: what fp32 leaves out (2^-23 of a pair) would turn
+// codes of elements between two of them, a few in ten million, into their neighbours.
+template <class T>
+__device__ __forceinline__ void rotated(const RopeAppendArgs &a, const Raw &r, int e0, const CosSin<T> *cs, float (&f)[8]) {
     unpack8(r.own, f);
     if (a.interleaved) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const CosSin w = cs[i * (a.rot / 8) + e0 / 8];
-            const float x = f[2 * i], y = f[2 * i + 1];
-            f[2 * i] = __builtin_fmaf(x, w.c, -(y * w.s));
-            f[2 * i + 1] = __builtin_fmaf(y, w.c, x * w.s);
+            const CosSin<T> w = cs[i * (a.rot / 8) + e0 / 8];
+            const T x = f[2 * i], y = f[2 * i + 1];
+            f[2 * i] = (float)fma_of(x, w.c, -(y * w.s));
+            f[2 * i + 1] = (float)fma_of(y, w.c, x * w.s);
         }
     } else {
         const int half = a.rot / 2;
@@ -71,8 +90,8 @@ __device__ __forceinline__ void rotated(const RopeAppendArgs &a, const Raw &r, i
         unpack8(make_uint4(r.other.x ^ turn, r.other.y ^ turn, r.other.z ^ turn, r.other.w ^ turn), g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const CosSin w = cs[i * (half / 8) + p0 / 8];
-            f[i] = __builtin_fmaf(f[i], w.c, g[i] * w.s);
+            const CosSin<T> w = cs[i * (half / 8) + p0 / 8];
+            f[i] = (float)fma_of((T)f[i], w.c, (T)g[i] * w.s);
         }
     }
 }
@@ -192,7 +211,7 @@ __device__ __forceinline__ void append_values(const RopeAppendArgs &a, uint8_t *
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArgs a, int value_blocks, int per, int ranks, int tokens) {
-    extern __shared__ CosSin cs[];
+    extern __shared__ double2 shared[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long long slots = (long long)a.num_pages * a.page;
 
@@ -200,47 +219,42 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
     const unsigned block = blockIdx.x, turn = block / (unsigned)per;
     if (turn >= (unsigned)value_blocks || block != turn * per) {
         // q and k of `tokens` tokens, a head per LPT lanes of eight elements
-        constexpr int LPT = D / 8, TPI = 64 / LPT, UNROLL = 2, STEP = kWaves * TPI;
+        constexpr int LPT = D / 8, TPI = 64 / LPT, STEP = kWaves * TPI;
         const int half = a.rot / 2, heads = a.num_q_heads + a.num_kv_heads, shift = __builtin_ctz(a.page);
         const long long t0 = (long long)(block - min(turn + 1, (unsigned)value_blocks)) * tokens;
         const int n = (int)min((long long)tokens, a.num_tokens - t0), rows = n * heads;
         const int e0 = (lane % LPT) * 8;
-        const bool turns = e0 < a.rot;
-        auto load = [&](int i0, Raw (&r)[UNROLL]) {
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int i = min(i0 + u * STEP, rows - 1), t = (unsigned)i / (unsigned)heads, h = i - t * heads;
-                const uint16_t *row = h < a.num_q_heads ? a.q + (t0 + t) * a.q_stride + (long long)h * D
-                                                        : a.k + (t0 + t) * a.k_stride + (long long)(h - a.num_q_heads) * D;
-                r[u] = load_raw(a, row, e0);
-            }
+        const bool turned = e0 < a.rot;
+        auto load = [&](int i) {
+            i = min(i, rows - 1);
+            const int t = (unsigned)i / (unsigned)heads, h = i - t * heads;
+            const uint16_t *row = h < a.num_q_heads ? a.q + (t0 + t) * a.q_stride + (long long)h * D
+                                                    : a.k + (t0 + t) * a.k_stride + (long long)(h - a.num_q_heads) * D;
+            return load_raw(a, row, e0);
         };
-        int i0 = wave * TPI + lane / LPT;
-        Raw now[UNROLL], next[UNROLL];
-        load(i0, now);
-        fill_cos_sin(a, cs, t0, n);
+        int i = wave * TPI + lane / LPT;
+        Raw now = load(i), next = now;
+        const Turns turns(shared, tokens * half);
+        fill_cos_sin(a, turns, t0, n);
         __syncthreads();
         // (every lane of a wave takes as many turns: keys' lanes look at each other)
-        for (int w0 = wave * TPI; w0 < rows; w0 += UNROLL * STEP, i0 += UNROLL * STEP) {
-            if (w0 + UNROLL * STEP < rows) load(i0 + UNROLL * STEP, next);
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int i = i0 + u * STEP;
-                const bool live = i < rows;
-                const int at = live ? i : rows - 1, t = (unsigned)at / (unsigned)heads, h = at - t * heads;
-                float f[8];
-                if (turns) rotated(a, now[u], e0, cs + t * half, f);
-                else unpack8(now[u].own, f);
-                if (h < a.num_q_heads) {
-                    if (live && (turns || a.q != a.q_out))
-                        store_stream16(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + e0, pack8(f));
-                } else {
-                    const long long slot = a.slots[t0 + t];
-                    const bool on = live && slot >= 0 && slot < slots;
-                    store_key<D>(a, f, (slot >> shift) * a.num_kv_heads + h - a.num_q_heads, (int)slot & (a.page - 1), e0, on);
-                }
-                now[u] = next[u];
+        for (int w0 = wave * TPI; w0 < rows; w0 += STEP, i += STEP) {
+            if (w0 + STEP < rows) next = load(i + STEP);
+            const bool live = i < rows;
+            const int at = live ? i : rows - 1, t = (unsigned)at / (unsigned)heads, h = at - t * heads;
+            float f[8];
+            if (!turned) unpack8(now.own, f);
+            else if (h < a.num_q_heads) rotated(a, now, e0, turns.q + t * half, f);
+            else rotated(a, now, e0, turns.k + t * half, f);
+            if (h < a.num_q_heads) {
+                if (live && (turned || a.q != a.q_out))
+                    store_stream16(a.q_out + (t0 + t) * a.q_out_stride + (long long)h * D + e0, pack8(f));
+            } else {
+                const long long slot = a.slots[t0 + t];
+                const bool on = live && slot >= 0 && slot < slots;
+                store_key<D>(a, f, (slot >> shift) * a.num_kv_heads + h - a.num_q_heads, (int)slot & (a.page - 1), e0, on);
             }
+            now = next;
         }
         return;
     }
@@ -257,7 +271,7 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
     unsigned long long todo = __ballot(mine >= 0 && mine < slots && !on);
     const int items = __builtin_popcountll(todo) * a.num_kv_heads;
     int leader = 0;
-    uint8_t *tile = reinterpret_cast<uint8_t *>(cs) + wave * D * 8;
+    uint8_t *tile = reinterpret_cast<uint8_t *>(shared) + wave * D * 8;
     for (int i = rank * kWaves + wave; i < items; i += ranks * kWaves) {
         const int l = (unsigned)i / (unsigned)a.num_kv_heads;
         for (; leader < l; ++leader) todo &= todo - 1;
@@ -271,8 +285,8 @@ __global__ __launch_bounds__(kThreads) void rope_append_kv4_kernel(RopeAppendArg
 
 template <int D>
 static hipError_t launch_d(const RopeAppendArgs &a, hipStream_t stream) {
-    // two tokens per workgroup of rows where there are many (16,384 of 32 + 8 heads of 128: 72 us, 77
-    // with four, 79 with one)
+    // two tokens per workgroup of rows where there are many (16,384 of 32 + 8 heads of 128: 73 us, 97
+    // with four, 83 with one)
     const int tokens = a.num_tokens >= 1024 ? 2 : 1;
     const long long windows = ((long long)a.num_tokens + kWindow - 1) / kWindow;
     // a small call: a wave per (token, head), should each be a granule's first
@@ -281,7 +295,7 @@ static hipError_t launch_d(const RopeAppendArgs &a, hipStream_t stream) {
     const long long value_blocks = windows * ranks, row_blocks = ((long long)a.num_tokens + tokens - 1) / tokens;
     if (value_blocks + row_blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     // sines of the tokens, or the waves' codes of v
-    const size_t lds = max((size_t)tokens * (a.rot / 2) * sizeof(CosSin), (size_t)kWaves * D * 8);
+    const size_t lds = max((size_t)tokens * (a.rot / 2) * kTurnBytes, (size_t)kWaves * D * 8);
     hipLaunchKernelGGL((rope_append_kv4_kernel<D>), dim3((unsigned)(value_blocks + row_blocks)), dim3(kThreads), lds, stream, a,
                        (int)value_blocks, (int)(row_blocks / value_blocks) + 1, ranks, tokens);
     return hipGetLastError();

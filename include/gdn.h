@@ -753,8 +753,8 @@ int gdn_paged_attention_kv8(const gdn_bf16 *q, int64_t q_stride, const uint8_t *
  * written into the cache, in one launch.
  *
  * Rotation, positions and frequencies are those of gdn_rope_append_kv8, and so is
- * the order that slot_mapping has to have; angles, and sines and cosines times
- * rope_scale, are in 64 bits, products in fp32.
+ * the order that slot_mapping has to have; angles, sines and cosines times
+ * rope_scale, and k's products are in 64 bits, q's products in fp32.
  *
  * Cache: k and v are rounded to nearest even at their scale.  A key's 32
  * elements' scale is the power of two below which their largest magnitude m has

@@ -171,6 +171,32 @@ def test_far_positions_scaled():
     check(x(4), x(2), x(2), pos, slots, freq, make_cache(r, 8, 2, 16, 128), rope_scale=m)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rotated_keys_are_rounded_once_before_their_codes(interleaved):
+    """8 million elements, some of which lie closer to the middle of two codes than fp32 products
+    are exact.  Angles up to 2^17 are off by 3 2^-53 of themselves and numpy's by one more, sines and
+    cosines by less than that: 2^-34 (|a| + |b|) before the rounding to fp32."""
+    r = np.random.default_rng(12)
+    T, hk, d, page = 8192, 8, 128, 64
+    freq, m = gdn.gdn_rope_frequencies(128, 1e6, "yarn", 4.0, original_context=32768)
+    pos = r.integers(0, 2 ** 17, T)
+    cache = make_cache(r, T // page, hk, page, d)
+    x = bf(r.standard_normal((T, hk, d)))
+    call(None, x, x.clone(), pos, np.arange(T), freq, cache, interleaved, m)
+    kc, _, ks, _ = numpy_of(cache)
+    codes, scale = (y.swapaxes(1, 2).reshape(T, hk, d // 32, 32) for y in (kc, ks[..., None].repeat(32, -1)))
+    k = ref.values(x)
+    want = ref.rotate(k, pos, freq, m, interleaved)
+    a, b = (want[..., 0::2], want[..., 1::2]) if interleaved else (want[..., :64], want[..., 64:])
+    off = 2.0 ** -33 * np.hypot(a, b)                                      # |a| + |b| <= sqrt 2 of it, rotation keeps it
+    off = np.stack([off, off], -1).reshape(want.shape) if interleaved else np.concatenate([off, off], -1)
+    s = np.exp2(scale - 127.0)
+    low, high = (kv4.VALUES[kv4.e2m1((want + sign * off).astype(np.float32).astype(np.float64).reshape(s.shape) / s)] for sign in (-1, 1))
+    got = kv4.VALUES[codes]
+    assert ((got >= low) & (got <= high)).all(), "%d codes" % ((got < low) | (got > high)).sum()
+    assert (low != high).mean() < 1e-6
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_every_significand_against_every_scale(d):
     """Values: largest magnitudes of all 128 significands, elements of all significands
