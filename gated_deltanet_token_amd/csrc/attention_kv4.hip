@@ -16,7 +16,9 @@
 // one keeps its 8 bits.  Codes are finite whatever they are; a key that a row
 // does not see gets a weight of zero there, and so no influence.
 // Scores and sums are fp32; the maximum is in units of log2.
+#include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "attention_split.h"
 #include "fp4.h"
@@ -251,14 +253,17 @@ __device__ __forceinline__ void put8(const AttentionArgs &a, const Division &v, 
 // way while it works on this one.  The waves' sums are joined in the LDS.  Of a
 // decode step of 32 requests of 1,100 keys (13.6 us) 1.3 us go to the request's
 // lengths, 2 to the first tile, 7 to 4.5 tiles of each wave, 1.5 to the join; 192
-// requests of 4,096 keys: 5.8 TB/s, as much as two tiles on their way, or more waves, gave.
+// requests of 4,096 keys (32/8 heads of 128) take 134 us, 6.3 TB/s.
 //
 // Lanes: with c = lane % 16 and g = lane / 16, a lane holds row c and the 16
 // keys from 16 g on of the tile, a granule of the cache: one page number per
 // lane for values, and one for the keys whose codes it loads.  Row i of the t-th K
-// operand is key 16 (i / 4) + 4 (i % 4) + t: the four operands' scales are
-// neighbouring bytes.  Row i of the V operands 2 u and 2 u + 1 is element 32 u + 2 i
-// and the one behind it: a 16-byte load has both.
+// operand is key 16 (i / 4) + 4 t + i % 4, so that a load has whole lines of 128
+// bytes; a lane's scale of each operand is a byte of another word.  At D = 256, where
+// a key is a line and a load has half of it either way, it is key 16 (i / 4) + 4 (i % 4) + t: the
+// four operands' scales are neighbouring bytes (64 requests of 1 to 4,000 keys: 32.4 us,
+// 34.3 the other way; 100 of 1,000 to 2,000 at D = 64: 24.8, and 23.6 the other way).  Row i of
+// the V operands 2 u and 2 u + 1 is element 32 u + 2 i and the one behind it: a 16-byte load has both.
 // ---------------------------------------------------------------------------
 // one of a kv head's tiles of 16 rows of a request
 struct RowTile {
@@ -301,13 +306,22 @@ __device__ __forceinline__ Entries entries_at(const AttentionArgs &a, int s, uns
     return {bt[min((j + 16 * (lane >> 2 & 3)) >> shift, last)], bt[min((j + 16 * (lane >> 4)) >> shift, last)]};
 }
 
+// 16 bytes of the cache
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint8_t *p) {
+    if constexpr (STREAM) return load_stream16(reinterpret_cast<const uint16_t *>(p));
+    else return *reinterpret_cast<const uint4 *>(p);
+}
+
 // One wave takes the keys [k_lo, k_hi) of a row tile from `first` on, 64 at a time and
 // `step` further on the next time, one tile on its way while it works on another.
 // `next`: the entries of the first one.
-template <int D>
+template <int D, bool STREAM>
 __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const Request &rq, int hk, const RowTile &w, int k_lo, int k_hi,
                                           int first, int step, Entries next, Sums<D> &sum) {
     constexpr int KS = Q16<D>::KS, DT = D / 16;      // DT operands of 16 value elements
+    constexpr bool kLines = D != 256;
+    constexpr int kRow = kLines ? 1 : 4, kNext = kLines ? 4 : 1;                  // keys from a lane's to the next one's, and to its next
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4, kg = c >> 2;
     const int jb = max(w.jb, k_lo), je = min(w.je, k_hi);
     const int in_page = a.page - 1;
@@ -323,24 +337,26 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
     auto page_of = [&](int entry, unsigned j) { return j < end && good(entry) ? entry : -1; };
 
     uint4 kr[4][KS], vr[DT / 2], vw[2];
-    uint32_t ks[KS];
+    using Scales = typename std::conditional<kLines, uint4, uint32_t>::type;
+    Scales kw[KS];                                   // the keys' scales
+    const uint32_t pick = (c & 3) | (4 + (c & 3)) << 8;
     int pv;                                          // the values' page
     // a tile begins at a multiple of 64 keys: places in a page stay the same
     const uint32_t pitch = (uint32_t)(a.num_kv_heads * a.page) * (D / 2);        // bytes of codes, all kv heads
-    const uint32_t k_row = hk * a.page + (16 * kg + 4 * (c & 3) & in_page), v_row = hk * a.page + (16 * g & in_page);
+    const uint32_t k_row = hk * a.page + (16 * kg + kRow * (c & 3) & in_page), v_row = hk * a.page + (16 * g & in_page);
     const uint8_t *k_at = a.k_cache + (k_row * (D / 2) + 16 * (D == 64 ? g & 1 : g));
-    const uint8_t *ks_at = k_scales(a) + ((hk * (D / 32) + (D == 64 ? g & 1 : g)) * a.page + (16 * kg + 4 * (c & 3) & in_page));
+    const uint8_t *ks_at = k_scales(a) + ((hk * (D / 32) + (D == 64 ? g & 1 : g)) * a.page + (16 * kg + (kLines ? 0 : 4 * (c & 3)) & in_page));
     const uint8_t *v_at = a.v_cache + (v_row * (D / 2) + 16 * c);
     const uint8_t *vs_at = reinterpret_cast<const uint8_t *>(v_scales(a) + v_row);
     auto load_k = [&](int page) {
         const uint64_t off = (uint64_t)(uint32_t)max(page, 0) * pitch;
         const uint8_t *p = k_at + off, *sc = ks_at + (off >> 4);                 // (scales: a 16th of the codes)
 #pragma unroll
-        for (int st = 0; st < KS; ++st) ks[st] = *reinterpret_cast<const uint32_t *>(sc + 4 * st * a.page);
+        for (int st = 0; st < KS; ++st) kw[st] = *reinterpret_cast<const Scales *>(sc + 4 * st * a.page);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int st = 0; st < KS; ++st) kr[t][st] = *reinterpret_cast<const uint4 *>(p + t * (D / 2) + 64 * st);
+            for (int st = 0; st < KS; ++st) kr[t][st] = load16<STREAM && kLines>(p + kNext * t * (D / 2) + 64 * st);
     };
     auto load_v = [&]() {
         const uint64_t off = (uint64_t)(uint32_t)max(pv, 0) * pitch;
@@ -349,7 +365,7 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
         vw[1] = sc[1];
         const uint8_t *p = v_at + off;
 #pragma unroll
-        for (int u = 0; u < DT / 2; ++u) vr[u] = *reinterpret_cast<const uint4 *>(p + 256 * u);
+        for (int u = 0; u < DT / 2; ++u) vr[u] = load16<STREAM>(p + 256 * u);
         asm volatile("" ::: "memory");
     };
 
@@ -380,10 +396,16 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
         f32x4 x[4] = {};
 #pragma unroll
         for (int st = 0; st < KS; ++st) {
-            score16<0>(x[0], kr[0][st], ks[st], q, st);
-            score16<1>(x[1], kr[1][st], ks[st], q, st);
-            score16<2>(x[2], kr[2][st], ks[st], q, st);
-            score16<3>(x[3], kr[3][st], ks[st], q, st);
+            uint32_t ks;
+            if constexpr (kLines)
+                ks = __builtin_amdgcn_perm(__builtin_amdgcn_perm(kw[st].w, kw[st].z, pick),
+                                           __builtin_amdgcn_perm(kw[st].y, kw[st].x, pick), 0x05040100u);
+            else
+                ks = kw[st];
+            score16<0>(x[0], kr[0][st], ks, q, st);
+            score16<1>(x[1], kr[1][st], ks, q, st);
+            score16<2>(x[2], kr[2][st], ks, q, st);
+            score16<3>(x[3], kr[3][st], ks, q, st);
         }
         const bool seen_page = good(pv);
         turn(j0 + step);
@@ -394,6 +416,11 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
         unpack8(vw[0], vs);
         unpack8(vw[1], vs + 8);
         uint32_t pw[8];
+        if constexpr (kLines) {
+            const f32x4 y[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) x[t] = f32x4{y[0][t], y[1][t], y[2][t], y[3][t]};
+        }
         weigh16(x, factor, vs, j - k_lo >= kLateKeys, masked, seen_page, j + 16 * g, jb, je, m, l, sum.o, pw);
         const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
 #pragma unroll
@@ -481,7 +508,7 @@ __device__ __forceinline__ int nth_longest(const AttentionArgs &a, int r, OrderL
     return s;
 }
 
-template <int D, int W, Take TAKE>
+template <int D, int W, Take TAKE, bool STREAM = false>
 __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division &v, int block, FewLds<D, W> &lds, OrderLds *order = nullptr) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
@@ -522,7 +549,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
     const int first = first_tile(k_lo, kTileKeys, wave);
     if (first != start) next = entries_at(a, s, first);
     Sums<D> sum;
-    take_keys<D>(a, s, rq, hk, w, k_lo, k_hi, first, W * kTileKeys, next, sum);
+    take_keys<D, STREAM>(a, s, rq, hk, w, k_lo, k_hi, first, W * kTileKeys, next, sum);
 
     // join the waves: maxima, then each wave's sums at the common maximum
     float l = sum.l;
@@ -971,13 +998,13 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
 // both kinds of requests in one grid -- the large ones' workgroups first, those of
 // the small ones (decode rows) take the CUs that are left and each that becomes free.
 // ---------------------------------------------------------------------------
-template <int D, int W>
+template <int D, int W, bool STREAM>
 __global__ __launch_bounds__(64 * W, 2) void attention_few_kv4_kernel(AttentionArgs a, Division v, bool ordered) {
     __shared__ union {
         FewLds<D, W> few;
         OrderLds order;
     } lds;
-    few_rows<D, W, Take::kAll>(a, v, blockIdx.x, lds.few, ordered ? &lds.order : nullptr);
+    few_rows<D, W, Take::kAll, STREAM>(a, v, blockIdx.x, lds.few, ordered ? &lds.order : nullptr);
 }
 
 constexpr int many_rows(int d) { return d == 256 ? kNarrowRows : kManyRows; }
@@ -1005,20 +1032,37 @@ static SplitRules rules(int d) {
 }
 
 // Workgroups of four waves: two of them on a CU, one of which streams while the other begins or
-// ends (192 requests of 4,096 keys, 32/8 heads of 128: 146 us, 156 with eight waves; 32 of
-// 1,100, 16/4 of 256: 13.6, 14.4).  Of eight where parts are long and there is one for
-// a CU at most (five of 40,000 to 131,000: 108 us, 113 with four; eight of up to
-// 30,000: 37.6 and 40.9).
+// ends (200 requests of 1 to 8,000 keys, 32/8 heads of 128: 150 us, 158 with eight waves; 32
+// of 1,100, 16/4 of 256: 13.5, 14.4).  Of eight where parts are long and there is one for
+// a CU at most (five of 40,000 to 131,000: 96 us, 137 with four; eight of up to
+// 30,000: 36.5 and 50).
 constexpr int kLongPart = 2048;
 // Longest requests first where there are two rounds of workgroups and more: the last ones
-// then end together (200 requests of 1 to 8,000 keys, 32/8 heads of 128: 168 us, 184 in
-// order).  Finding its request costs a workgroup 1.9 us (100 requests of 1,000 to 2,000, 32/8 of
-// 64, in one round: 27.8 us, 24.7 in order).
+// then end together (200 requests of 1 to 8,000 keys, 32/8 heads of 128: 150 us, 165 in
+// order; 192 of 4,096 each: 137 and 133).  Finding its request costs a workgroup 1.9 us (100
+// requests of 1,000 to 2,000, 32/8 of 64, in one round: 27.8 us, 24.7 in order).
 constexpr int kManyUnits = 4 * kCUs;
 
 int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int d, int max_seq_len) {
     const Plan p = plan_of(rules(d), num_tokens, num_seqs, num_q_heads, num_kv_heads, d, max_seq_len);
     return (p.few.floats + p.many.floats) * 4;
+}
+
+// Streaming loads of the cache where a call may read more of it than this: what is kept is
+// of no use, and is kept at the expense of what is still to be read (200 requests of 1 to
+// 8,000 keys, 32/8 heads of 128, 953 MB: 151 us, 170 with ordinary loads; five of 40,000 to
+// 131,000, 577 MB: 96 and 107).  Smaller caches are still there in the next step (32 requests of
+// 1,100, 16/4 of 256, 38 MB each, three sets of inputs in turn: 16.1 us, 13.5 with ordinary ones).
+constexpr double kStreamed = 1 << 27;
+
+template <int D, bool STREAM>
+static void launch_few(const AttentionArgs &a, const Launch &few, const Division &v, hipStream_t stream) {
+    const dim3 grid((unsigned)(few.units * few.splits));
+    if (few.splits > 1 && few.chunk >= kLongPart)
+        hipLaunchKernelGGL((attention_few_kv4_kernel<D, 8, STREAM>), grid, dim3(512), 0, stream, a, v, false);
+    else
+        hipLaunchKernelGGL((attention_few_kv4_kernel<D, 4, STREAM>), grid, dim3(kOrderThreads), 0, stream, a, v,
+                           (long long)a.num_tokens * a.num_kv_heads > kManyUnits && a.num_seqs <= kOrdered * kOrderThreads);
 }
 
 template <int D>
@@ -1029,12 +1073,11 @@ static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
         return hipErrorInvalidConfiguration;
     const Division vf = division(p.few, false, D, a.workspace);
     if (p.few_takes == Take::kAll) {
-        const dim3 grid((unsigned)few);
-        if (p.few.splits > 1 && p.few.chunk >= kLongPart)
-            hipLaunchKernelGGL((attention_few_kv4_kernel<D, 8>), grid, dim3(512), 0, stream, a, vf, false);
-        else
-            hipLaunchKernelGGL((attention_few_kv4_kernel<D, 4>), grid, dim3(kOrderThreads), 0, stream, a, vf,
-                               (long long)a.num_tokens * a.num_kv_heads > kManyUnits && a.num_seqs <= kOrdered * kOrderThreads);
+        // the most that the call can see: the requests' keys, or every page
+        const double keys = a.window > 0 && a.window < a.max_seq_len ? a.window : a.max_seq_len;
+        const double seen = std::min(a.num_seqs * keys, (double)a.num_pages * a.page) * a.num_kv_heads * (D + D / 32 + 2);
+        if (seen > kStreamed) launch_few<D, true>(a, p.few, vf, stream);
+        else launch_few<D, false>(a, p.few, vf, stream);
         launch_join(Take::kAll, a, p.few, vf, kTileRows, stream);
         return hipGetLastError();
     }
