@@ -1009,7 +1009,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_few_kv4_kernel(AttentionA
 
 constexpr int many_rows(int d) { return d == 256 ? kNarrowRows : kManyRows; }
 
-template <int D>
+template <int D, bool STREAM>
 __global__ __launch_bounds__(kManyThreads, 2) void attention_mixed_kv4_kernel(AttentionArgs a, Division few, Division many,
                                                                               int many_blocks) {
     constexpr int W = kManyThreads / 64;
@@ -1018,7 +1018,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_mixed_kv4_kernel(At
         ManyLds<D> many[2];
     } lds;
     const int block = blockIdx.x;
-    if (block >= many_blocks) few_rows<D, W, Take::kSmall>(a, few, block - many_blocks, lds.few);
+    if (block >= many_blocks) few_rows<D, W, Take::kSmall, STREAM>(a, few, block - many_blocks, lds.few);
     else if constexpr (D == 256) many_rows_narrow<D>(a, many, block, many_blocks, lds.many);
     else many_rows_wide<D>(a, many, block, many_blocks, lds.many);
 }
@@ -1048,10 +1048,11 @@ int64_t attention_kv4_workspace_bytes(int num_tokens, int num_seqs, int num_q_he
     return (p.few.floats + p.many.floats) * 4;
 }
 
-// Streaming loads of the cache where a call may read more of it than this: what is kept is
-// of no use, and is kept at the expense of what is still to be read (200 requests of 1 to
-// 8,000 keys, 32/8 heads of 128, 953 MB: 151 us, 170 with ordinary loads; five of 40,000 to
-// 131,000, 577 MB: 96 and 107).  Smaller caches are still there in the next step (32 requests of
+// Streaming loads of few rows' keys and values where a call may read more of the cache
+// than this: what is kept is of no use, and is kept at the expense of what is still to be
+// read (200 requests of 1 to 8,000 keys, 32/8 heads of 128, 953 MB: 151 us, 170 with ordinary
+// loads; five of 40,000 to 131,000, 577 MB: 96 and 107; 150 of 4,000 to 8,000 beside a chunk
+// of 512: 186 and 203).  Smaller caches are still there in the next step (32 requests of
 // 1,100, 16/4 of 256, 38 MB each, three sets of inputs in turn: 16.1 us, 13.5 with ordinary ones).
 constexpr double kStreamed = 1 << 27;
 
@@ -1072,18 +1073,19 @@ static hipError_t launch_d(const AttentionArgs &a, hipStream_t stream) {
     if (few + many > 0x7fffffffLL || p.few.rows > 0x7fffffffLL || p.many.rows > 0x7fffffffLL)
         return hipErrorInvalidConfiguration;
     const Division vf = division(p.few, false, D, a.workspace);
+    // the most that the call can see: the requests' keys, or every page
+    const double keys = a.window > 0 && a.window < a.max_seq_len ? a.window : a.max_seq_len;
+    const double seen = std::min(a.num_seqs * keys, (double)a.num_pages * a.page) * a.num_kv_heads * (D + D / 32 + 2);
     if (p.few_takes == Take::kAll) {
-        // the most that the call can see: the requests' keys, or every page
-        const double keys = a.window > 0 && a.window < a.max_seq_len ? a.window : a.max_seq_len;
-        const double seen = std::min(a.num_seqs * keys, (double)a.num_pages * a.page) * a.num_kv_heads * (D + D / 32 + 2);
         if (seen > kStreamed) launch_few<D, true>(a, p.few, vf, stream);
         else launch_few<D, false>(a, p.few, vf, stream);
         launch_join(Take::kAll, a, p.few, vf, kTileRows, stream);
         return hipGetLastError();
     }
     const Division vm = division(p.many, p.by_rows, D, a.workspace + p.few.floats);
-    hipLaunchKernelGGL((attention_mixed_kv4_kernel<D>), dim3((unsigned)(few + many)), dim3(kManyThreads), 0, stream, a, vf, vm,
-                       (int)many);
+    const dim3 grid((unsigned)(few + many)), block(kManyThreads);
+    if (seen > kStreamed) hipLaunchKernelGGL((attention_mixed_kv4_kernel<D, true>), grid, block, 0, stream, a, vf, vm, (int)many);
+    else hipLaunchKernelGGL((attention_mixed_kv4_kernel<D, false>), grid, block, 0, stream, a, vf, vm, (int)many);
     launch_join(Take::kSmall, a, p.few, vf, kTileRows, stream);
     launch_join(Take::kLarge, a, p.many, vm, many_rows(D), stream);
     return hipGetLastError();

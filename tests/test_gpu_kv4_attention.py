@@ -454,6 +454,32 @@ def test_cache_past_4_gib():
     c.near(o, *c.want())
 
 
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16), (128, 64), (256, 16)])
+@pytest.mark.parametrize("lens,longest", [([(5, 1), (2000, 1), (70, 1), (0, 1), (6001, 1), (130, 1)], 2 ** 21),
+                                          ([(1 + 37 * i % 700, 1) for i in range(130)], 60000),
+                                          ([(300, 2), (65, 0), (0, 0), (900, 1), (40, 1), (3, 0)], 2 ** 21),
+                                          ([(300, 90), (2000, 1), (70, 1), (4000, 3)], 2 ** 21)])
+def test_a_pool_that_no_cache_holds(d, page, lens, longest):
+    """A bound of the lengths and a pool of more than 128 MiB: few rows read it another way."""
+    hk = 2
+    c = Case(50 + d, lens, 8, hk, d, page)
+    pages = 2 ** 27 // (hk * page * d) + 20
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")                      # noqa: E731
+    big = dict(k_cache=u8(pages, hk, page, d // 2), v_cache=u8(pages, hk, page // 16, d, 8), k_scale=u8(pages, hk, d // 32, page),
+               v_scale=torch.zeros(pages, hk, page, dtype=torch.bfloat16, device="cuda"))
+    at = pages - 1 - np.arange(c.kq.shape[0])
+    g = c.gpu()
+    for name in big:
+        big[name][at.tolist()] = g[name]
+    table = np.where(c.table >= 0, at[np.maximum(c.table, 0)], -1)
+    g.update(big, block_table=cuda(table, torch.int32))
+    for window in (0, 100):
+        o = torch.full(c.q.shape, 77.0, dtype=torch.bfloat16, device="cuda")
+        gdn.gdn_paged_attention_kv4(c.q, o=o, max_seq_len=longest, scale=c.scale, window=window, **g)
+        torch.cuda.synchronize()
+        c.near(o, *c.want(window=window))
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_repeats_are_bit_identical(d):
     c = Case(22, MIXED + [(3000, 1)], 8, 2, d, 16)
