@@ -801,6 +801,11 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 x[0] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k0), operand(q[st].part[2]), x[0], kE2m1, kE2m3, 0, sc, 2, q[st].scale);
                 x[1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(k1), operand(q[st].part[2]), x[1], kE2m1, kE2m3, 1, sc, 2, q[st].scale);
             }
+            // asked for before the weights are formed: the compiler would read each just before its product
+            uint4 w4[2][DT / 2];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) w4[i / (DT / 2)][i % (DT / 2)] = vt[i / (DT / 2) * (D / 2) + 32 * (i % (DT / 2))];
+            __builtin_amdgcn_sched_barrier(0);
             const int jg = j0 + 32 * h2;
             if (masked) {
                 // from the row's first and past its last key of these, none of a missing page
@@ -846,11 +851,11 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 const bf16x8 p1 = as_bf16x8(pw[8 * b + 4], pw[8 * b + 5], pw[8 * b + 6], pw[8 * b + 7]);
 #pragma unroll
                 for (int u = 0; u < DT / 2; ++u) {
-                    const uint4 w4 = vt[b * (D / 2) + 32 * u];
-                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.x), p0, o[2 * u], 0, 0, 0);
-                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.y), p1, o[2 * u], 0, 0, 0);
-                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.z), p0, o[2 * u + 1], 0, 0, 0);
-                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w4.w), p1, o[2 * u + 1], 0, 0, 0);
+                    const uint4 &w = w4[b][u];
+                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w.x), p0, o[2 * u], 0, 0, 0);
+                    o[2 * u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w.y), p1, o[2 * u], 0, 0, 0);
+                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w.z), p0, o[2 * u + 1], 0, 0, 0);
+                    o[2 * u + 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(values8(w.w), p1, o[2 * u + 1], 0, 0, 0);
                 }
             }
         }
@@ -943,15 +948,26 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
             const uint4 *kt = tile.k + k_row, *vt = tile.v + g * (D / 2) + c;
             f32x4 x[4] = {};
+            uint4 kr[KS][4];
+            uint32_t ks[KS];
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
-                const uint32_t ks = tile.ks[16 * (4 * st + g) + key / 4].x;
-                const int at = k_swap ^ 4 * st;
-                score16<0>(x[0], kt[at], ks, q, st);            // (key t is row 2 t of these eight)
-                score16<1>(x[1], kt[2 * 8 + at], ks, q, st);
-                score16<2>(x[2], kt[4 * 8 + at], ks, q, st);
-                score16<3>(x[3], kt[6 * 8 + at], ks, q, st);
+                ks[st] = tile.ks[16 * (4 * st + g) + key / 4].x;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) kr[st][t] = kt[2 * t * 8 + (k_swap ^ 4 * st)];       // (key t is row 2 t of these eight)
             }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int st = 0; st < KS; ++st) {
+                score16<0>(x[0], kr[st][0], ks[st], q, st);
+                score16<1>(x[1], kr[st][1], ks[st], q, st);
+                score16<2>(x[2], kr[st][2], ks[st], q, st);
+                score16<3>(x[3], kr[st][3], ks[st], q, st);
+            }
+            // asked for before the weights are formed: the compiler would read each just before its product
+            uint4 w4[DT / 2];
+#pragma unroll
+            for (int u = 0; u < DT / 2; ++u) w4[u] = vt[16 * u];
             float vs[16];
             const f32x4 *vst = reinterpret_cast<const f32x4 *>(tile.vs + 8 * g);
 #pragma unroll
@@ -962,16 +978,17 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 vs[4 * i + 2] = s.z;
                 vs[4 * i + 3] = s.w;
             }
+            __builtin_amdgcn_sched_barrier(0);
             uint32_t pw[8];
             weigh16(x, factor, vs, j0 - k_lo >= kLateKeys, masked, ok, j0 + 16 * g, jb, je, m, l, o, pw);
             const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
 #pragma unroll
             for (int u = 0; u < DT / 2; ++u) {
-                const uint4 w4 = vt[16 * u];
-                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.x), p0, o[2 * u], 0, 0, 0);
-                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.y), p1, o[2 * u], 0, 0, 0);
-                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.z), p0, o[2 * u + 1], 0, 0, 0);
-                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w4.w), p1, o[2 * u + 1], 0, 0, 0);
+                const uint4 &w = w4[u];
+                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w.x), p0, o[2 * u], 0, 0, 0);
+                o[2 * u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w.y), p1, o[2 * u], 0, 0, 0);
+                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w.z), p0, o[2 * u + 1], 0, 0, 0);
+                o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w.w), p1, o[2 * u + 1], 0, 0, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
