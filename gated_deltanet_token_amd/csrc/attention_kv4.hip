@@ -608,12 +608,12 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the LDS once for all waves, the next one on its way from HBM to registers
 // meanwhile, with one barrier per tile between two buffers.
 // Bound by vector arithmetic and what two or three waves per SIMD leave uncovered: of a
-// prompt of 8,192 tokens (32/8 heads of 128: 515 us, 1,070 TFLOP/s; of 64: 326; 16/4 of
-// 256: 525) the vector unit is busy for 73% of the time, the matrix cores for 43%.  What did
+// prompt of 8,192 tokens (32/8 heads of 128: 521 us, 1,055 TFLOP/s; of 64: 335; 16/4 of
+// 256: 529) the vector unit is busy for 76% of the time, the matrix cores for 44%.  What did
 // not help there: the values turned to bf16 once, on their way to the LDS (fewer
-// conversions, as much more waiting for the LDS: 534 us, 531 then without); q's parts in
-// the LDS for a third wave (666: registers spill, 341 of 336 at D = 64); a tile's scores
-// taken with the weights of the tile before (655 and 374: registers).
+// conversions, more traffic there: 543 us); q's parts in the LDS for a third wave (666:
+// registers spill; at D = 64 341, 336 then without); a tile's scores taken with the weights
+// of the tile before (655 and 374: registers).
 //
 // Keys lie in the LDS as rows of 16-byte pieces (32 elements), values as in
 // memory, granule by granule.  The 16 lanes that a 16-byte read serves together are
@@ -887,7 +887,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // ---------------------------------------------------------------------------
 // 16 rows per wave, for D = 256: 32 rows' sums and q parts leave room for one wave per
 // SIMD only (with the parts in the LDS registers spill: a prompt of 8,192, 16/4 heads, takes
-// 687 us, 525 so).  Four waves: two workgroups on a CU do not wait for each other (eight
+// 687 us, 529 so).  Four waves: two workgroups on a CU do not wait for each other (eight
 // waves of 128 rows: 555).  Lanes as in the few-rows kernel, operands from the LDS.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowRows = 64;
