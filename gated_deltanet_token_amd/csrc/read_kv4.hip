@@ -7,9 +7,10 @@
 // eight elements' codes of a value lie in 64 bytes, for all 16 tokens.  A store is 16
 // bytes per lane, whole heads.
 // Bound by the stores, 32 bits for every 8.3 read: streaming ones, that leave the
-// caches to what is still to be read (30,000 rows of 4 heads of 256: 27.7 us, 36.6
-// with ordinary ones; 131,071 of 8 of 128: 125 and 132, 5.4 TB/s of both directions).  Streaming
-// loads would lose the halves of a line that another load takes (33 and 134 us).
+// caches to what is still to be read (30,000 rows of 4 heads of 256: 26.4 us; 131,071 of
+// 8 of 128: 124, 5.5 TB/s of both directions; with ordinary ones 9 and 7 us more).
+// Streaming loads would lose the halves of a line that another load takes (6 and 9 us
+// more).  All keys before all values: granule by granule 1.3 us more each.
 #include "attention_split.h"
 #include "fp4.h"
 
@@ -38,9 +39,10 @@ __global__ __launch_bounds__(kReadThreads) void paged_read_kv4_kernel(PagedReadA
     const int lane = threadIdx.x & 63;
     const long long unit = (long long)blockIdx.x * (kReadThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (unit >= waves) return;
-    const int tile = (int)(unit / (2 * groups)), item = (int)(unit - (long long)tile * 2 * groups);
-    const bool is_k = item < groups;
-    const int head = (is_k ? item : item - groups) * HEADS + lane / LPH, e0 = (lane % LPH) * 8;
+    // all keys, then all values
+    const bool is_k = unit < waves / 2;
+    const long long of = is_k ? unit : unit - waves / 2;
+    const int tile = (int)(of / groups), head = (int)(of - (long long)tile * groups) * HEADS + lane / LPH, e0 = (lane % LPH) * 8;
     if (is_k ? !a.k_out : !a.v_out) return;
     // request s owns the tile numbers from floor(out_start_loc[s] / 16) + 2 s on: as
     // many as its granules or more
