@@ -608,9 +608,11 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // the LDS once for all waves, the next one on its way from HBM to registers
 // meanwhile, with one barrier per tile between two buffers.
 // Bound by vector arithmetic and what two or three waves per SIMD leave uncovered: of a
-// prompt of 8,192 tokens (32/8 heads of 128: 521 us, 1,055 TFLOP/s; of 64: 335; 16/4 of
-// 256: 529) the vector unit is busy for 76% of the time, the matrix cores for 44%.  What did
-// not help there: the values turned to bf16 once, on their way to the LDS (fewer
+// prompt of 8,192 tokens (32/8 heads of 128: 516 us, 1,065 TFLOP/s; of 64: 328; 16/4 of
+// 256: 517) the vector unit is busy for 76% of the time, the matrix cores for 44%.  Waves
+// that feed the matrix cores go before those that form weights (s_setprio: the same prompt
+// at D = 64 333 us without, 29 decode rows with 2,019 tokens at D = 256 40.0 and 37.6 with it).
+// What did not help: the values turned to bf16 once, on their way to the LDS (fewer
 // conversions, more traffic there: 543 us); q's parts in the LDS for a third wave (666:
 // registers spill; at D = 64 341, 336 then without); a tile's scores taken with the weights
 // of the tile before (655 and 374: registers).
@@ -789,6 +791,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             const uint4 *kt = t.k + k_row, *vt = t.v + h2 * D + c;
             const uint8_t *kst = reinterpret_cast<const uint8_t *>(t.ks) + 2 * (key & ~3) + (key & 3) + 128 * h2;
             f32x16 x[2] = {};
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int st = 0; st < KS; ++st) {
                 const int sc = *reinterpret_cast<const uint16_t *>(kst + 256 * st);
@@ -806,6 +809,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 #pragma unroll
             for (int i = 0; i < DT; ++i) w4[i / (DT / 2)][i % (DT / 2)] = vt[i / (DT / 2) * (D / 2) + 32 * (i % (DT / 2))];
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(0);
             const int jg = j0 + 32 * h2;
             if (masked) {
                 // from the row's first and past its last key of these, none of a missing page
@@ -845,6 +849,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 pw[r] = pack_bf16x2(e0 * s.x, e1 * s.y);
                 pw[r + 1] = pack_bf16x2(e2 * s.z, e3 * s.w);
             }
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const bf16x8 p0 = as_bf16x8(pw[8 * b], pw[8 * b + 1], pw[8 * b + 2], pw[8 * b + 3]);
@@ -859,6 +864,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
                 }
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         stage.put(lds[buf ^ 1]);
         __syncthreads();
@@ -887,7 +893,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
 // ---------------------------------------------------------------------------
 // 16 rows per wave, for D = 256: 32 rows' sums and q parts leave room for one wave per
 // SIMD only (with the parts in the LDS registers spill: a prompt of 8,192, 16/4 heads, takes
-// 687 us, 529 so).  Four waves: two workgroups on a CU do not wait for each other (eight
+// 687 us, 517 so).  Four waves: two workgroups on a CU do not wait for each other (eight
 // waves of 128 rows: 555).  Lanes as in the few-rows kernel, operands from the LDS.
 // ---------------------------------------------------------------------------
 constexpr int kNarrowRows = 64;
@@ -948,6 +954,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
             const bool masked = j0 < wk.all0 || jn > wk.all1 || __any(!ok);
             const uint4 *kt = tile.k + k_row, *vt = tile.v + g * (D / 2) + c;
             f32x4 x[4] = {};
+            __builtin_amdgcn_s_setprio(1);
             uint4 kr[KS][4];
             uint32_t ks[KS];
 #pragma unroll
@@ -979,8 +986,10 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 vs[4 * i + 3] = s.w;
             }
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(0);
             uint32_t pw[8];
             weigh16(x, factor, vs, j0 - k_lo >= kLateKeys, masked, ok, j0 + 16 * g, jb, je, m, l, o, pw);
+            __builtin_amdgcn_s_setprio(1);
             const bf16x8 p0 = as_bf16x8(pw[0], pw[1], pw[2], pw[3]), p1 = as_bf16x8(pw[4], pw[5], pw[6], pw[7]);
 #pragma unroll
             for (int u = 0; u < DT / 2; ++u) {
@@ -991,6 +1000,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
                 o[2 * u + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(values8(w.w), p1, o[2 * u + 1], 0, 0, 0);
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         stage.put(lds[buf ^ 1]);
         __syncthreads();
