@@ -544,11 +544,13 @@ def gdn_chunk_rule_and_fused_decode_noalloc(q, k, v, g, beta, state_indices, o, 
 # ---------------------------------------------------------------------------
 
 # Host time counts here: a decode step's calls take the GPU a few microseconds.
-# So each tensor's shape, strides and device are asked for once.
+# So each tensor's shape, strides and device are asked for once, and types are
+# looked up in this module.
+_BF16, _U8, _I32, _I64, _F64 = torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float64
 
 def _vector(t, dt, n, name):
     """A packed 1-D operand of n entries."""
-    if t.dtype != dt:
+    if t.dtype is not dt:
         raise TypeError("%s must be %s, got %s" % (name, dt, t.dtype))
     if t.shape != (n,) or not t.is_contiguous():
         raise ValueError("%s must be packed with %d entries, got shape %s" % (name, n, tuple(t.shape)))
@@ -650,24 +652,22 @@ def _kv8(k_cache, v_cache, k_scale, v_scale):
 
 def _bf16_heads(t, T, H, d, name):
     """Token stride of a bf16 [T][H][d] operand with packed heads."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    shape = (T, H, d)
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    strides = t.stride()
-    if T > 1 and strides[2] == 1 and strides[1] == d:
-        return strides[0]
-    return _head_stride(shape, strides, name)
+    if t.shape != (T, H, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (T, H, d), tuple(t.shape)))
+    token, head, element = strides = t.stride()
+    if element == 1 and head == d and T > 1:
+        return token
+    return _head_stride((T, H, d), strides, name)
 
 
 def _kv4(k_cache, v_cache, k_scale, v_scale):
     """dtypes and shapes of the 4-bit paged cache; returns (pages, HK, page, D)."""
-    u8 = torch.uint8
-    if k_cache.dtype != u8 or v_cache.dtype != u8 or k_scale.dtype != u8:
+    if k_cache.dtype is not _U8 or v_cache.dtype is not _U8 or k_scale.dtype is not _U8:
         raise TypeError("k_cache, v_cache and k_scale must be torch.uint8, got %s, %s and %s"
                         % (k_cache.dtype, v_cache.dtype, k_scale.dtype))
-    if v_scale.dtype != torch.bfloat16:
+    if v_scale.dtype is not _BF16:
         raise TypeError("v_scale must be torch.bfloat16, got %s" % v_scale.dtype)
     shape = k_cache.shape
     if len(shape) != 4:
@@ -700,9 +700,9 @@ def _rope_append(call, name, shape, q, k, v, positions, slot_mapping, frequencie
     if frequencies is not None:
         _dims(frequencies, 1, "frequencies")
         rot = 2 * frequencies.shape[0]
-    args = (_ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _vector(positions, torch.int32, T, "positions"),
-            _vector(slot_mapping, torch.int64, T, "slot_mapping"),
-            _vector(frequencies, torch.float64, rot // 2, "frequencies") if rot else None, rot, 1 if interleaved else 0,
+    args = (_ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _vector(positions, _I32, T, "positions"),
+            _vector(slot_mapping, _I64, T, "slot_mapping"),
+            _vector(frequencies, _F64, rot // 2, "frequencies") if rot else None, rot, 1 if interleaved else 0,
             rope_scale, _ptr(q_out), os_, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             n, page, T, hq, hk, d)
     dev = _on_current("k v positions slot_mapping frequencies k_cache v_cache k_scale v_scale q q_out", k, v, positions,
@@ -764,8 +764,8 @@ def gdn_paged_read_kv4(k_cache, v_cache, k_scale, v_scale, block_table, key_star
     _table(block_table, S)
     args = (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
             block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
-            None if key_starts is None else _vector(key_starts, torch.int32, S, "key_starts"),
-            _vector(out_start_loc, torch.int32, S + 1, "out_start_loc"), _ptr(k_out), ks, _ptr(v_out), vs, S, R, hk, d)
+            None if key_starts is None else _vector(key_starts, _I32, S, "key_starts"),
+            _vector(out_start_loc, _I32, S + 1, "out_start_loc"), _ptr(k_out), ks, _ptr(v_out), vs, S, R, hk, d)
     dev = _on_current("k_cache v_cache k_scale v_scale block_table key_starts out_start_loc k_out v_out", k_cache, v_cache,
                       k_scale, v_scale, block_table, key_starts, out_start_loc, k_out, v_out)
     _check(lib.gdn_paged_read_kv4(*args, _stream_on(stream, dev)), "gdn_paged_read_kv4")
@@ -786,7 +786,7 @@ def gdn_paged_attention_kv4_workspace_size(num_tokens, num_seqs, num_q_heads, nu
 
 
 def _table(block_table, S):
-    if block_table.dtype != torch.int32:
+    if block_table.dtype is not _I32:
         raise TypeError("block_table must be torch.int32, got %s" % block_table.dtype)
     if block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("block_table must have %d rows, got shape %s" % (S, tuple(block_table.shape)))
@@ -803,8 +803,8 @@ def _paged_attention(call, size, name, shape, q, k_cache, v_cache, k_scale, v_sc
     _table(block_table, S)
     args = (q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n, page,
             block_table.data_ptr(), _rows(block_table, "block_table"), block_table.shape[1],
-            _vector(seq_lens, torch.int32, S, "seq_lens"),
-            _vector(query_start_loc, torch.int32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
+            _vector(seq_lens, _I32, S, "seq_lens"),
+            _vector(query_start_loc, _I32, S + 1, "query_start_loc"), max_seq_len, o.data_ptr(), os_, S, T, hq, hk,
             d, scale, 1 if causal else 0, window)
     dev = _on_current("q k_cache v_cache k_scale v_scale block_table seq_lens query_start_loc o workspace", q, k_cache,
                       v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, o, workspace)
