@@ -58,7 +58,8 @@ def key_values(codes, scale):
 
 
 def value_values(codes, scale):
-    return VALUES[codes] * np.asarray(scale, np.float64)[..., None]
+    with np.errstate(invalid="ignore"):
+        return VALUES[codes] * np.asarray(scale, np.float64)[..., None]
 
 
 # the arrays as they lie in memory; codes [pages][hk][page][D]
