@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attention_keys.h"
+#include "attention_plan.h"
 #include "gdn_device.h"
 #include "serving_internal.h"
 
@@ -16,8 +17,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
-constexpr int kTileKeys = 64;           // keys a wave takes at once
-constexpr int kTileRows = 16;           // rows of a workgroup of the few-rows kernel
 
 __device__ __forceinline__ Request request_of(const AttentionArgs &a, int s) {
     Request r;
@@ -113,11 +112,6 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
 constexpr int kLateKeys = 256;
 __device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
-// Which requests a launch takes: all, those of at most kSmallRows rows per kv
-// head, or the larger ones.
-enum class Take { kAll, kSmall, kLarge };
-constexpr int kSmallRows = 32;
-
 // A launch's division of its requests' keys, and its partial results: a row's D
 // sums per split, and behind all of them a maximum and a sum of weights per
 // (row, split).  Rows are (token, q head), or for the small requests alone
@@ -138,8 +132,6 @@ __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int
     return TAKE == Take::kSmall ? ((long long)s * kSmallRows + row) * a.num_kv_heads + hk
                                 : (long long)t * a.num_q_heads + h;
 }
-
-constexpr int kManyRows = 128;
 
 // use(i, read(i)) for i < N, each read A steps before its use and, left alone
 // by the compiler, not earlier: it would read until it runs out of registers.
@@ -208,36 +200,6 @@ __device__ __forceinline__ WaveKeys wave_keys(const AttentionArgs &a, const Many
     }
     return k;
 }
-
-// ---------------------------------------------------------------------------
-// How a call is divided (attention_split.hip).
-// ---------------------------------------------------------------------------
-constexpr int kCUs = 256;
-
-// What a format's kernels and their measured times decide of it: the least keys
-// of a part of the few-rows kernel, of the same where three of four CUs are
-// idle, and of the many-rows kernel; waves of a workgroup of both kinds of rows;
-// workgroups of it that all CUs hold at once.
-struct SplitRules {
-    int min_chunk, idle_chunk, many_chunk;
-    int waves, room, many_rows = kManyRows;
-};
-
-struct Launch {
-    long long units;        // (row tile, kv head) pairs, upper bound; 0: none
-    long long rows;         // of partial results
-    int chunk, splits;
-    long long floats;       // of partial results
-};
-
-struct Plan {
-    Take few_takes;
-    bool by_rows;
-    Launch few, many;
-};
-
-// window: 0, or the keys that a row sees at most (a plan needs no more workspace for it)
-Plan plan_of(const SplitRules &rules, long long T, long long S, int q_heads, int kv_heads, int d, int max_seq_len, int window = 0);
 
 // the partial results of a launch at `ws`
 inline Division division(const Launch &p, bool by_rows, int d, float *ws) {

@@ -132,7 +132,9 @@ def test_rows_about_a_tile(d, new):
 @pytest.mark.parametrize("window", [100, 1024, 1025])
 def test_windows_over_long_requests(d, window):
     """A window of one part's keys or fewer, wherever it lies: few rows are not split."""
-    Case(31, [(9000, 1), (4097, 1), (1500, 1), (3, 1)], 4, 1, d, 16).check(window=window)
+    c = Case(31, [(9000, 1), (4097, 1), (1500, 1), (3, 1)], 4, 1, d, 16)
+    for longest in (None, 1, 100, 1023, 1024, 2 ** 31 - 1):
+        c.check(longest, window=window)
     Case(32, [(9000, 1), (4097, 3), (5000, 90), (3, 1)], 4, 1, d, 16).check(window=window)
 
 
