@@ -519,3 +519,25 @@ def test_on_a_stream_of_its_own_and_in_a_graph():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, o)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_batches(seed):
+    """Sizes, masks, bounds and missing pages in combinations that no other test here names."""
+    r = np.random.default_rng(1000 + seed)
+    pick = lambda *x: x[r.integers(len(x))]                                                # noqa: E731
+    d, page, hk = pick(64, 128, 256), pick(16, 32, 64), pick(1, 1, 2, 3, 8)
+    hq = hk * pick(1, 2, 3, 4, 5, 8, 16)
+    lens = []
+    for _ in range(pick(1, 2, 3, 5, 17, 40)):
+        kind, length = r.random(), int(2 ** r.uniform(0, 11.2))
+        new = int(2 ** r.uniform(0, 7.2))
+        lens.append((pick(0, -3, 1, 3), pick(0, 1, 2)) if kind < 0.15 else (length, pick(1, 1, 1, 2, 4)) if kind < 0.8 else
+                    (new + pick(0, length), new))
+    lens.append((int(2 ** r.uniform(0, 11.2)), 1))
+    c = Case(seed, lens, hq, hk, d, page, spread=pick(1.0, 3.0))
+    if r.random() < 0.3:
+        c.table[r.random(c.table.shape) < 0.1] = -1
+    for _ in range(2):
+        c.check(pick(None, 1, 100, 1000, 2 ** 31 - 1), most=1.0, causal=bool(r.random() < 0.8),
+                window=pick(0, 0, 1, 16, 63, 65, 200, 512, 1024, 1500))
