@@ -46,25 +46,19 @@ __device__ __forceinline__ const uint16_t *v_scales(const AttentionArgs &a) { re
 
 __device__ __forceinline__ bf16x8 values8(uint32_t w) { return __builtin_bit_cast(bf16x8, e2m1_bf16(w)); }
 
-// 32 values as e2m3 codes and back, over the power of two s.  These instructions
-// write their first results before they have read their last operands (with the
-// scale's register among the results', codes came out at other scales), which the
-// compiler does not know: operands are kept until they are done.
-__device__ __forceinline__ u32x6 e2m3_codes(const bf16x32 &x, float s) {
-    u32x6 w = __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x, s);
-    asm("" : "+v"(w) : "v"(x), "v"(s));
-    return w;
-}
+// 32 values as e2m3 codes and back, over the power of two s.  These instructions write
+// their first results before they have read their last operands.  The compiler keeps them
+// apart, but for the one that takes fp32 values, of which it does not know: that one is
+// written out, its result declared as early (and with the two wait states that a matrix
+// instruction needs behind a vector one; with the values brought to bf16 for the first
+// conversion instead a call took 0.2 us more).
+__device__ __forceinline__ u32x6 e2m3_codes(const bf16x32 &x, float s) { return __builtin_amdgcn_cvt_scalef32_pk32_fp6_bf16(x, s); }
 __device__ __forceinline__ u32x6 e2m3_codes(const f32x16 &even, const f32x16 &odd, float s) {
-    u32x6 w = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, s);
-    asm("" : "+v"(w) : "v"(even), "v"(odd), "v"(s));
+    u32x6 w;
+    asm("v_cvt_scalef32_2xpk16_fp6_f32 %0, %1, %2, %3\n\ts_nop 1" : "=&v"(w) : "v"(even), "v"(odd), "v"(s));
     return w;
 }
-__device__ __forceinline__ f32x32 e2m3_values(const u32x6 &w, float s) {
-    f32x32 x = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s);
-    asm("" : "+v"(x) : "v"(w), "v"(s));
-    return x;
-}
+__device__ __forceinline__ f32x32 e2m3_values(const u32x6 &w, float s) { return __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(w, s); }
 
 // 32 elements of q in three parts, x = s (hi + mid / 32 + lo / 1024), s the power
 // of two that brings their largest to [2, 4).  A part has four significant bits and
