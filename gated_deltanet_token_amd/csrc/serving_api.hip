@@ -376,7 +376,8 @@ GDN_EXPORT int gdn_paged_attention_kv4(const gdn_bf16 *q, int64_t q_stride, cons
                           window};
     const int rc = check_attention(a, attention_kv4_workspace_bytes, workspace_bytes, true);
     if (rc) return rc;
-    if (!isfinite(scale)) return fail(GDN_ERR_INVALID, "scale must be finite");
+    // scores are in units of log2; a score of zero times an infinite factor would be NaN
+    if (!isfinite(scale * 1.4426950408889634f)) return fail(GDN_ERR_INVALID, "scale and its product with log2(e) must be finite");
     return hip_status(launch_attention_kv4(a, (hipStream_t)stream), "paged attention launch");
 }
 

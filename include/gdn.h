@@ -828,12 +828,12 @@ int gdn_paged_read_kv4(const uint8_t *k_cache, const uint8_t *v_cache, const uin
  * The split of the work, and what a padded batch or a max_seq_len far above the
  * lengths costs, are as gdn_paged_attention_kv8's.
  *
- *   scale        finite
+ *   scale        finite, and so its product with log2(e) (below 2^127.47)
  *   others       as gdn_paged_attention_kv8's, the workspace of
  *                gdn_paged_attention_kv4_workspace_size bytes
  *
- * Errors: as gdn_paged_attention_kv8's, and GDN_ERR_INVALID where scale is not
- * finite.
+ * Errors: as gdn_paged_attention_kv8's, and GDN_ERR_INVALID where scale or its
+ * product with log2(e) is not finite.
  */
 size_t gdn_paged_attention_kv4_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
                                               int32_t num_kv_heads, int32_t head_dim, int32_t max_seq_len);
