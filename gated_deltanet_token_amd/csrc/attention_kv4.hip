@@ -165,6 +165,11 @@ __device__ __forceinline__ void score16(f32x4 &x, const uint4 &k, uint32_t ks, c
         x = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(k), operand(q.part[st][2]), x, kE2m1, kE2m3, T, ks, 2, q.scale[st]);
 }
 
+// From products of q and k to scores in units of log2 (their sign is q's).  Not zero: a
+// masked score stays at -infinity.  The least number there is instead: products may be
+// as large as 2^126, and count for nothing at a scale of zero.
+__device__ __forceinline__ float to_log2(float scale) { return fmaxf(fabsf(scale) * kLog2e, 0x1p-149f); }
+
 // The larger of two scores, NaN if one is (the row is, then, whatever its maximum: fmaxf
 // would first turn each operand into a quiet one).
 __device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
@@ -383,7 +388,7 @@ __device__ __forceinline__ void take_keys(const AttentionArgs &a, int s, const R
     __builtin_amdgcn_sched_barrier(0);
     Q16<D> q;
     q.split(raw, g, a.scale < 0.f ? 0x80008000u : 0u);
-    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+    const float factor = to_log2(a.scale);
     const int all0 = max(w.x0, k_lo), all1 = min(w.x1, k_hi) - kTileKeys;
 
     for (; j0 < end; j0 += step) {
@@ -758,7 +763,7 @@ __device__ __forceinline__ void many_rows_wide(const AttentionArgs &a, const Div
             q[st] = split_q(e, a.scale < 0.f ? 0x80008000u : 0u);
         }
     }
-    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+    const float factor = to_log2(a.scale);
 
     Staging<D, k_place<D>> stage(a, w);
     const int key = 32 * (c >> 2 & 1) + 8 * (c >> 3) + 2 * (c & 3);
@@ -922,7 +927,7 @@ __device__ __forceinline__ void many_rows_narrow(const AttentionArgs &a, const D
     const WaveKeys wk = wave_keys(a, w, wrow, 16);
     Q16<D> q;
     q.split(Q16<D>::load(a.q + (long long)(rq.begin + i_row) * a.q_stride + (long long)h * D, g), g, a.scale < 0.f ? 0x80008000u : 0u);
-    const float factor = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-126f);      // not zero: a masked score stays at -infinity
+    const float factor = to_log2(a.scale);
 
     Staging<D, k_place_narrow<D>> stage(a, w);
     const int key = 16 * (c >> 2) + 4 * (c & 3);

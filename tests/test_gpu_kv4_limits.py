@@ -1,5 +1,6 @@
 """GPU checks of the 4-bit paged cache's calls at the ends of their ranges, with the bounds of
 test_gpu_kv4_attention.py unless a test says otherwise."""
+import numpy as np
 import pytest
 
 from test_gpu_kv4_attention import Case
@@ -16,3 +17,14 @@ def test_scores_of_zero_at_the_largest_scale(d, new):
     for sign in (1, -1):
         c.scale = sign * float(largest_scale())
         c.check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -149, -2.0 ** -140, 1e-38])
+def test_large_products_at_a_scale_of_zero_and_tiny_ones(d, scale):
+    """Products of q and k up to 2^126: at a scale of zero all keys weigh the same all the same."""
+    c = Case(61, [(5, 1), (9, 3), (70, 40), (300, 1)], 4, 2, d, 16)
+    c.q.mul_(2.0 ** 40)
+    c.ks = np.where(c.ks == 255, 255, c.ks + 80).astype(np.uint8)
+    c.scale = scale
+    c.check()
