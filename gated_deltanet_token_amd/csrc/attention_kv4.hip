@@ -63,8 +63,9 @@ __device__ __forceinline__ f32x32 e2m3_values(const u32x6 &w, float s) { return 
 // 32 elements of q in three parts, x = s (hi + mid / 32 + lo / 1024), s the power
 // of two that brings their largest to [2, 4).  A part has four significant bits and
 // steps of 1/8 below 2: exact for elements down to 2^-7 of the largest, and
-// within 2^-15 of that for smaller ones.  Scale bytes: hi's, mid's and lo's.  An
-// infinity or NaN: scales of NaN, as the parts have none.
+// within 2^-15 of that for smaller ones.  s is 2^-111 at least, so that lo's steps are
+// normal numbers: below a largest of 2^-110 elements are held within 2^-125.  Scale
+// bytes: hi's, mid's and lo's.  An infinity or NaN: scales of NaN, as the parts have none.
 struct SplitQ {
     u32x6 part[3];
     uint32_t scale;

@@ -818,7 +818,8 @@ int gdn_paged_read_kv4(const uint8_t *k_cache, const uint8_t *v_cache, const uin
  * Scores are products of the cache's codes and scales with q in three 6-bit parts
  * per 32 elements (exact for elements of at least 2^-7 of those 32's largest,
  * within 2^-15 of that largest for smaller ones: bf16 itself is off by up to 2^-9
- * of it there), summed in fp32; softmax statistics and sums are fp32.  A weight is
+ * of it there; where that largest is below 2^-110, within 2^-125), summed in fp32;
+ * softmax statistics and sums are fp32.  A weight is
  * rounded to bf16 in its product with a value, with the value's scale in it: off
  * by at most 2^-8 of itself while that product is above 2^-126.  o is rounded to
  * bf16.  A head of q with an infinity or NaN gives NaN, and so does a seen key or
