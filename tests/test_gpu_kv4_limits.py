@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import gated_deltanet_token_amd as gdn
 import serving_ref as ref
 from test_gpu_kv4_attention import Case
 from test_kv4_limits_host import largest_scale
@@ -65,3 +66,48 @@ def test_tiny_queries(d, new, top):
     bound = want * (2 * 2.0 ** -8 + 2.0 ** -15 + np.repeat(np.expm1(off / small * np.abs(x)), new))
     err = np.abs(ref.values(c.run(causal=False))[:, 0] - want[:, None]).max(-1)
     assert (err <= bound).all(), (err / bound).max()
+
+
+def guarded(shape, dtype, fill, rows=64):
+    """(a buffer of `fill`, its middle of that shape)"""
+    whole = torch.full((shape[0] + 2 * rows, *shape[1:]), fill, dtype=dtype, device="cuda")
+    return whole, whole[rows:rows + shape[0]]
+
+
+def untouched(whole, fill, rows=64):
+    return bool((whole[:rows] == fill).all() and (whole[-rows:] == fill).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,qsl", [
+    ([(50, 10), (60, 10), (70, 10)], [0, 25, 12, 900]), ([(50, 10), (60, 10), (70, 10)], [-9, 40, -3, 2 ** 31 - 1]),
+    ([(300, 70), (400, 60), (90, 20)], [0, 140, 20, 2 ** 31 - 1]), ([(9000, 1), (5000, 1), (70, 1), (3, 0)], [0, 3, -2 ** 31, 2, 3000]),
+    ([(9000, 2), (6000, 40), (70, 3)], [44, 10, 45, 0])], ids=["rows", "signs", "prompts", "decode", "parts"])
+def test_malformed_query_start_loc_writes_nowhere_else(d, lens, qsl):
+    """Bounds that decrease or lie outside: whose rows are whose is not said, but o's neighbours and the workspace's
+    are as they were."""
+    c = Case(63, lens, 8, 2, d, 16)
+    T, c.qsl = c.q.shape[0], np.array(qsl, np.int32)
+    n = gdn.gdn_paged_attention_kv4_workspace_size(T, len(lens), 8, 2, d, c.longest())
+    whole, o = guarded(c.q.shape, torch.bfloat16, 77.0)
+    ws_whole, ws = guarded((max(n, 1),), torch.uint8, 91, 4096)
+    assert ws.data_ptr() % 256 == 0
+    gdn.gdn_paged_attention_kv4(c.q, o=o, max_seq_len=c.longest(), scale=c.scale, workspace=ws, **c.gpu())
+    torch.cuda.synchronize()
+    assert untouched(whole, 77.0) and untouched(ws_whole, 91, 4096)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("loc", [[0, 50, 20, 900], [-7, 60, -2 ** 31, 2 ** 31 - 1], [90, 10, 100, 0]])
+def test_malformed_out_start_loc_writes_nowhere_else(d, loc):
+    c = Case(64, [(80, 1), (60, 1), (200, 1)], 2, 2, d, 16)
+    g = c.gpu()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")                      # noqa: E731
+    for starts in (None, i32([5, -3, 2 ** 31 - 1])):
+        for which in ("kv", "k", "v"):
+            outs = [guarded((100, 2, d), torch.bfloat16, 77.0) for _ in range(2)]
+            gdn.gdn_paged_read_kv4(*(g[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale", "block_table")), starts, i32(loc),
+                                   *(o if n in which else None for n, (_, o) in zip("kv", outs)))
+            torch.cuda.synchronize()
+            for n, (whole, o) in zip("kv", outs):
+                assert untouched(whole, 77.0) and (n in which or (o == 77.0).all())
