@@ -1,11 +1,13 @@
 """GPU checks of gdn_rope_append_kv4 against its definition in 64 bits.
 
-Values, unrotated elements and every scale of theirs: equality.  Rotated elements:
+Values, unrotated elements and every scale of theirs: equality.  Rotated elements of q:
 sines and cosines rounded to fp32 (2^-24 of each), a product and a sum of two
 rounded (2^-24 each) are off by at most 2^-24 (2 |a c| + 3 |b s|) < 3 2^-24 (|a c| +
-|b s|), and a subnormal step; a code has to be that of some number this close to the
-exact one, a scale that of a magnitude this close to the largest, and q within that
-and half a bf16 step (2^-8)."""
+|b s|), and a subnormal step; q has to be within that and half a bf16 step (2^-8).
+Keys are held to the same here: a code has to be that of some number this close to the
+exact one, a scale that of a magnitude this close to the largest.  That they are rotated in
+64 bits and rounded once is checked by test_rotated_keys_are_rounded_once_before_their_codes
+and, for all shapes, in test_gpu_kv4_rotated_keys.py."""
 import numpy as np
 import pytest
 import torch
