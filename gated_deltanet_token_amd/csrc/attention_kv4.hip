@@ -38,7 +38,8 @@ constexpr int kE2m1 = 4, kE2m3 = 2;             // operand formats of the scaled
 // workgroup's part: most tiles have a new maximum for some row of a wave, hardly
 // any one above that, and sums follow only then.  (In the first keys the heaviest
 // often makes up the sum, and its weight of 1 is exact.)  A weight is never above
-// 1, so that no product with a scale passes the values' own range.
+// 1, so that no product with a scale passes the values' own range; at the other end a
+// product is rounded as a normal number of bf16 from 2^-118 times the heaviest's on.
 constexpr float kHeadroom = 8.f;
 
 __device__ __forceinline__ const uint8_t *k_scales(const AttentionArgs &a) { return static_cast<const uint8_t *>(a.k_scale); }
@@ -609,7 +610,7 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // meanwhile, with one barrier per tile between two buffers.
 // Bound by vector arithmetic and what two or three waves per SIMD leave uncovered: of a
 // prompt of 8,192 tokens (32/8 heads of 128: 516 us, 1,065 TFLOP/s; of 64: 328; 16/4 of
-// 256: 517) the vector unit is busy for 76% of the time, the matrix cores for 44%.  Waves
+// 256: 517) the vector unit is busy for 77% of the time, the matrix cores for 45%.  Waves
 // that feed the matrix cores go before those that form weights (s_setprio: the same prompt
 // at D = 64 333 us without, 29 decode rows with 2,019 tokens at D = 256 40.0 and 37.6 with it).
 // What did not help: the values turned to bf16 once, on their way to the LDS (fewer

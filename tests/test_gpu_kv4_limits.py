@@ -111,3 +111,29 @@ def test_malformed_out_start_loc_writes_nowhere_else(d, loc):
             torch.cuda.synchronize()
             for n, (whole, o) in zip("kv", outs):
                 assert untouched(whole, 77.0) and (n in which or (o == 77.0).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 3, 40], ids=["decode", "small", "large"])
+@pytest.mark.parametrize("exponent", [-90, -100])
+def test_light_keys_of_tiny_values_beside_heavy_ones_that_come_late(d, new, exponent):
+    """Keys of 2^-17.17 of the heaviest's weight, with a value scale of 1.5 times 2^-100: their product is above 2^-117.
+    It is rounded to bf16 once, as a normal number, also where the maximum is set behind the first keys.  (Sums below
+    2^-126 are subnormal: a step of 2^-149 per sum, 700 of them.)"""
+    c = Case(65, [(700, new)], 2, 1, d, 16, spread=0.0)
+    c.q[:, :, 0] = 17.0
+    c.kq[:, :, :, 0] = 0
+    c.ks[...] = 127
+    c.scale = float(1.01 * np.log(2.0))
+    c.vs[...] = 1.5 * 2.0 ** exponent
+    for i, p in enumerate(c.table[0, :44]):
+        c.vq[p, 0, :, :] = c.r.integers(1, 8, (16, d)) + 8 * c.r.integers(0, 2, (16, 1))
+        if i >= 18:
+            c.kq[p, 0, ::5, 0] = 2                # these weigh 2^17.17 times the others
+            c.vq[p, 0, ::5] = 0
+    assert c.split_error() == 0.0
+    want, mag = c.want()
+    got = ref.values(c.run())
+    heaviest = 1 / 140                            # at least, of the sum of weights
+    bound = np.abs(want) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -11) + 700 * 2.0 ** -149 * 2.0 ** 8 * heaviest
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
