@@ -151,6 +151,16 @@ __device__ __forceinline__ void split_q16(const Row16<D> &q, float up, i32x8 (&q
 // so that it keeps a masked score at -infinity.
 __device__ __forceinline__ float usable(float factor) { return factor == 0.f ? 0x1p-126f : factor < 0.f ? -factor : factor; }
 
+// The sums are brought to a row's new maximum only where that is more than this
+// above the maximum m that they are relative to (in units of log2): weights up
+// to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
+// row of a wave, hardly any such a one (a prompt of 8,192 tokens, heads of 128: 589
+// us with none, 573).  None is let through where the values' scale is so large
+// that weight times scale or their sum could pass fp32's end, nor in the first
+// kLateKeys keys of a workgroup's part: of few keys the heaviest often makes up
+// the sum, and its weight of 1 is exact.  (A wave that begins behind them begins
+// with its first tile's maximum, too.)
+__device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
 // One tile of a wave with 16 rows: the scores x (keys jg + 4 t + r of the lane's
 // row) become weights, packed to bf16 pairs with the values' scale in them;
@@ -554,6 +564,21 @@ __device__ __forceinline__ void few_rows(const AttentionArgs &a, const Division 
 // ---------------------------------------------------------------------------
 constexpr int kWideThreads = 256;      // of a workgroup with 32 rows per wave
 constexpr int kWideAhead = 3;
+
+// use(i, read(i)) for i < N, each read A steps before its use and, left alone
+// by the compiler, not earlier: it would read until it runs out of registers.
+template <int N, int A, typename Read, typename Use>
+__device__ __forceinline__ void run_ahead(Read read, Use use) {
+    decltype(read(0)) w[N];          // all but A + 1 of them dead at any time
+#pragma unroll
+    for (int i = 0; i < (A < N ? A : N); ++i) w[i] = read(i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (i + A < N) w[i + A] = read(i + A);
+        asm volatile("" ::: "memory");
+        use(i, w[i]);
+    }
+}
 
 template <int D>
 struct ManyLds {

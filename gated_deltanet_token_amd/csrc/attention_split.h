@@ -100,17 +100,9 @@ __device__ __forceinline__ bf16x8 as_bf16x8(uint32_t a, uint32_t b, uint32_t c, 
     return __builtin_bit_cast(bf16x8, v);
 }
 
-// The sums are brought to a row's new maximum only where that is more than this
-// above the maximum m that they are relative to (in units of log2): weights up
-// to 2^8 cost bf16 and fp32 nothing, and most tiles have a new maximum for some
-// row of a wave, hardly any such a one (a prompt of 8,192 tokens, heads of 128: 589
-// us with none, 573).  None is let through where the values' scale is so large
-// that weight times scale or their sum could pass fp32's end, nor in the first
-// kLateKeys keys of a workgroup's part: of few keys the heaviest often makes up
-// the sum, and its weight of 1 is exact.  (A wave that begins behind them begins
-// with its first tile's maximum, too.)
+// In this many keys of a workgroup's part a row's sums follow every new maximum;
+// behind them each format lets some pass.
 constexpr int kLateKeys = 256;
-__device__ __forceinline__ float slack(float vs, bool late) { return late && fabsf(vs) < 0x1p64f ? 8.f : 0.f; }
 
 // A launch's division of its requests' keys, and its partial results: a row's D
 // sums per split, and behind all of them a maximum and a sum of weights per
@@ -131,21 +123,6 @@ template <Take TAKE>
 __device__ __forceinline__ long long part_row(const AttentionArgs &a, int s, int t, int h, long long row, int hk) {
     return TAKE == Take::kSmall ? ((long long)s * kSmallRows + row) * a.num_kv_heads + hk
                                 : (long long)t * a.num_q_heads + h;
-}
-
-// use(i, read(i)) for i < N, each read A steps before its use and, left alone
-// by the compiler, not earlier: it would read until it runs out of registers.
-template <int N, int A, typename Read, typename Use>
-__device__ __forceinline__ void run_ahead(Read read, Use use) {
-    decltype(read(0)) w[N];          // all but A + 1 of them dead at any time
-#pragma unroll
-    for (int i = 0; i < (A < N ? A : N); ++i) w[i] = read(i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (i + A < N) w[i + A] = read(i + A);
-        asm volatile("" ::: "memory");
-        use(i, w[i]);
-    }
 }
 
 // A workgroup's share of a many-rows launch.
